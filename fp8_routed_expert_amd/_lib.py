@@ -66,11 +66,22 @@ SIGNATURES = {
     "moe_gate_up_act_fp8_gather_e8m0": (ctypes.c_int32, [
         _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp,
         _vp, _vp]),
+    "moe_sort_tokens": (ctypes.c_int32, [
+        _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _size,
+        _vp, _vp]),
+    "moe_permute_rows": (ctypes.c_int32, [
+        _vp, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _vp, _vp]),
+    "moe_permute_rows_grad": (ctypes.c_int32, [
+        _vp, _c_int, _c_int, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
+    "moe_combine_rows": (ctypes.c_int32, [
+        _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
+    "moe_combine_rows_grad": (ctypes.c_int32, [
+        _vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp]),
     "moe_ceiling_copy": (ctypes.c_int32, [_vp, _vp, _size, _vp]),
     "moe_ceiling_mfma_fp8": (ctypes.c_int32, [_c_int, _c_int, _vp, _vp, _vp]),
 }
 
-ABI_VERSION = 9
+ABI_VERSION = 10
 
 _lib = None
 

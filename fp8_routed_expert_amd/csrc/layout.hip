@@ -419,6 +419,57 @@ extern "C" size_t moe_layout_workspace_bytes(int T, int K, int E) {
   return (size_t)(2 * nc * E) * sizeof(int32_t);
 }
 
+// The index work shared by the dispatch and moe_sort_tokens: argument checks
+// of the routing arguments (they launch nothing), then the count / scan /
+// rank launches.  *rows_total receives the buffer's row count.
+static moe_status_t check_routing(const int32_t* topk_idx, int T, int K, int E, int layout,
+                                  int align_m, int rows, const int32_t* counts,
+                                  const int32_t* offsets, const int32_t* slot_of,
+                                  const int32_t* row_src, const int32_t* row_expert,
+                                  const void* workspace, size_t workspace_bytes,
+                                  const int32_t* status_dev, long long* rows_total) {
+  if (T < 0 || K <= 0 || K > MOE_MAX_TOPK || E <= 0 || E > MOE_MAX_EXPERTS || rows < 0)
+    return MOE_INVALID_ARG;
+  if (layout != MOE_LAYOUT_CONTIGUOUS && layout != MOE_LAYOUT_MASKED)
+    return MOE_INVALID_ARG;
+  if (layout == MOE_LAYOUT_CONTIGUOUS && align_m < 1) return MOE_INVALID_ARG;
+  if (!counts || !offsets || !status_dev || !workspace) return MOE_INVALID_ARG;
+  *rows_total = layout == MOE_LAYOUT_MASKED ? (long long)E * rows : (long long)rows;
+  if (*rows_total > 0x7fffffffLL) return MOE_UNSUPPORTED_SHAPE;
+  if ((long long)T * K > 0x7fffffffLL) return MOE_UNSUPPORTED_SHAPE;
+  if (workspace_bytes < moe_layout_workspace_bytes(T, K, E)) return MOE_INVALID_ARG;
+  if (T > 0 && (!topk_idx || !slot_of)) return MOE_INVALID_ARG;
+  if (*rows_total > 0 && (!row_src || !row_expert)) return MOE_INVALID_ARG;
+  return MOE_OK;
+}
+
+static void launch_index(const int32_t* topk_idx, int T, int K, int E, int layout, int align_m,
+                         int rows, int rows_total, int32_t* counts, int32_t* offsets,
+                         int32_t* slot_of, int32_t* row_src, int32_t* row_expert,
+                         void* workspace, int32_t* status_dev, hipStream_t st) {
+  const long long F = (long long)T * K;
+  long long nc = n_chunks(T, K);
+  int32_t* chunk_counts = reinterpret_cast<int32_t*>(workspace);
+  int32_t* chunk_base = chunk_counts + (nc < 1 ? 1 : nc) * E;
+  const int cap = layout == MOE_LAYOUT_MASKED ? rows : 0;
+
+  const int ncl = (int)(nc < 1 ? 1 : nc);   // count always runs: it also clears row_src
+  hipLaunchKernelGGL(layout_count, dim3((unsigned)ncl), dim3(kLayoutThreads),
+                     E * sizeof(int32_t), st, topk_idx, F, E, key_bits_for(E), chunk_counts,
+                     row_src, row_expert, rows_total, status_dev);
+  // few chunks: the rank blocks compute the scan themselves (one launch less)
+  const int fold = nc > 0 && E <= kLayoutThreads && nc * (long long)E <= kFoldMax;
+  if (!fold)
+    hipLaunchKernelGGL(layout_scan, dim3(1), dim3(kScanThreads), 0, st, chunk_counts, ncl, E,
+                       scan_group(E), layout, align_m, cap, chunk_base, counts, offsets);
+  if (nc > 0)
+    hipLaunchKernelGGL(layout_rank, dim3((unsigned)nc), dim3(kLayoutThreads),
+                       (3 + kWaves) * E * sizeof(int32_t), st, topk_idx, F, K,
+                       E, key_bits_for(E), layout, rows_total, cap,
+                       offsets, chunk_base, slot_of, row_src, row_expert,
+                       status_dev, fold, chunk_counts, ncl, align_m, counts);
+}
+
 // hw = 4-byte scale words per source row (H/128 fp32 scales, or H/512
 // rounded up of packed E8M0 words).
 static moe_status_t dispatch(
@@ -434,42 +485,20 @@ static moe_status_t dispatch(
     return MOE_INVALID_ARG;
   if (layout == MOE_LAYOUT_CONTIGUOUS && align_m < 1) return MOE_INVALID_ARG;
   if (H % kBlock != 0) return MOE_UNSUPPORTED_SHAPE;
-  if (!counts || !offsets || !status_dev || !workspace) return MOE_INVALID_ARG;
-  long long rows_total =
-      layout == MOE_LAYOUT_MASKED ? (long long)E * rows : (long long)rows;
-  if (rows_total > 0x7fffffffLL) return MOE_UNSUPPORTED_SHAPE;
-  if ((long long)T * K > 0x7fffffffLL) return MOE_UNSUPPORTED_SHAPE;
-  if (workspace_bytes < moe_layout_workspace_bytes(T, K, E))
-    return MOE_INVALID_ARG;
+  long long rows_total = 0;
+  const moe_status_t ok =
+      check_routing(topk_idx, T, K, E, layout, align_m, rows, counts, offsets, slot_of, row_src,
+                    row_expert, workspace, workspace_bytes, status_dev, &rows_total);
+  if (ok != MOE_OK) return ok;
   // a == nullptr: the rows are not copied (the *_gather GEMM calls read them
   // from x through row_src); indices and permuted scales are still written
-  if (T > 0 && (!topk_idx || (a && !x) || !x_scale || !slot_of)) return MOE_INVALID_ARG;
-  if (rows_total > 0 && (!row_src || !row_expert || !a_scale))
-    return MOE_INVALID_ARG;
+  if (T > 0 && ((a && !x) || !x_scale)) return MOE_INVALID_ARG;
+  if (rows_total > 0 && !a_scale) return MOE_INVALID_ARG;
   if (((uintptr_t)x | (uintptr_t)a) & 15) return MOE_UNSUPPORTED_SHAPE;
 
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const long long F = (long long)T * K;
-  long long nc = n_chunks(T, K);
-  int32_t* chunk_counts = reinterpret_cast<int32_t*>(workspace);
-  int32_t* chunk_base = chunk_counts + (nc < 1 ? 1 : nc) * E;
-  const int cap = layout == MOE_LAYOUT_MASKED ? rows : 0;
-
-  const int ncl = (int)(nc < 1 ? 1 : nc);   // count always runs: it also clears row_src
-  hipLaunchKernelGGL(layout_count, dim3((unsigned)ncl), dim3(kLayoutThreads),
-                     E * sizeof(int32_t), st, topk_idx, F, E, key_bits_for(E), chunk_counts,
-                     row_src, row_expert, (int)rows_total, status_dev);
-  // few chunks: the rank blocks compute the scan themselves (one launch less)
-  const int fold = nc > 0 && E <= kLayoutThreads && nc * (long long)E <= kFoldMax;
-  if (!fold)
-    hipLaunchKernelGGL(layout_scan, dim3(1), dim3(kScanThreads), 0, st, chunk_counts, ncl, E,
-                       scan_group(E), layout, align_m, cap, chunk_base, counts, offsets);
-  if (nc > 0)
-    hipLaunchKernelGGL(layout_rank, dim3((unsigned)nc), dim3(kLayoutThreads),
-                       (3 + kWaves) * E * sizeof(int32_t), st, topk_idx, F, K,
-                       E, key_bits_for(E), layout, (int)rows_total, cap,
-                       offsets, chunk_base, slot_of, row_src, row_expert,
-                       status_dev, fold, chunk_counts, ncl, align_m, counts);
+  launch_index(topk_idx, T, K, E, layout, align_m, rows, (int)rows_total, counts, offsets,
+               slot_of, row_src, row_expert, workspace, status_dev, st);
   if (T > 0 && rows_total > 0) {
     const int n16 = H / 16;
     const int pieces = (n16 + 64 * kPermChunks - 1) / (64 * kPermChunks);
@@ -482,6 +511,23 @@ static moe_status_t dispatch(
                        0, st, x, slot_of, T, K, H, pieces, plen, (int)rows_total, a, x_scale,
                        row_src, hw, a_scale, (int)scale_blocks);
   }
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
+}
+
+extern "C" moe_status_t moe_sort_tokens(const int32_t* topk_idx, int T, int K, int E, int layout,
+                                        int align_m, int rows, int32_t* counts,
+                                        int32_t* offsets, int32_t* slot_of, int32_t* row_src,
+                                        int32_t* row_expert, void* workspace,
+                                        size_t workspace_bytes, int32_t* status_dev,
+                                        void* stream) {
+  long long rows_total = 0;
+  const moe_status_t ok =
+      check_routing(topk_idx, T, K, E, layout, align_m, rows, counts, offsets, slot_of, row_src,
+                    row_expert, workspace, workspace_bytes, status_dev, &rows_total);
+  if (ok != MOE_OK) return ok;
+  launch_index(topk_idx, T, K, E, layout, align_m, rows, (int)rows_total, counts, offsets,
+               slot_of, row_src, row_expert, workspace, status_dev,
+               reinterpret_cast<hipStream_t>(stream));
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
 }
 

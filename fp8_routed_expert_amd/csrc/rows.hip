@@ -1,0 +1,507 @@
+// Rows sorted by expert and back, with their gradients, in 32-, 16- and 8-bit
+// types: the row movement of the dispatch and the weighted sum of the combine
+// for layers that are trained or that keep their activations in other types
+// than FP8 (whose own calls are moe_dispatch_layout and moe_combine).
+//
+//   permute          a[slot(t, k)] = x[t]
+//   permute, grad    dx[t] = sum_k da[slot(t, k)]
+//   combine          out[t] = sum_k w[t, k] y[slot(t, k)]
+//   combine, grad    dy[slot(t, k)] = w[t, k] dout[t]
+//                    dw[t, k] = <dout[t], y[slot(t, k)]>
+//
+// All four walk the source tokens: a token's row is read or written once, and
+// each of its slots' rows once, so a call moves every byte it has to and no
+// other; sums are gathers in ascending k, held in fp32, with no atomics, so a
+// call's result does not depend on its schedule.  Bound by HBM bandwidth.
+//
+// A row is a run of H elements cut into 16-byte chunks.  Rows whose length in
+// bytes is no multiple of 16 (or whose buffers are not 16-byte aligned) are
+// read through unaligned 16-byte accesses, and their last chunk starts 16
+// bytes before the row's end: it overlaps the one before it, so that every
+// access is wide and none leaves the row.  The overlap writes the same values
+// twice and is left out of dot products.  Rows shorter than 16 bytes are one
+// chunk of single bytes.
+#include "device_common.hpp"
+
+namespace moe {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowWaves = kRowThreads / 64;
+constexpr int kRowChunks = 2;      // 16-byte chunks per lane and piece of a row
+
+struct F32 {
+  static constexpr int kSize = 4, kN = 4;
+  __device__ __forceinline__ static void unpack(const uint4& v, float (&f)[kN]) {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+  }
+  __device__ __forceinline__ static uint4 pack(const float (&f)[kN]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+};
+
+// 16-bit types: eight elements, rounded to nearest even once, when stored.
+struct BF16 {
+  static constexpr int kSize = 2, kN = 8;
+  __device__ __forceinline__ static void unpack(const uint4& v, float (&f)[kN]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_to_f32(w[i] & 0xffffu);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ static uint4 pack(const float (&f)[kN]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = f32_to_bf16(f[2 * i]) | ((uint32_t)f32_to_bf16(f[2 * i + 1]) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+struct F16 {
+  static constexpr int kSize = 2, kN = 8;
+  typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+  __device__ __forceinline__ static void unpack(const uint4& v, float (&f)[kN]) {
+    const h8 h = __builtin_bit_cast(h8, v);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) f[i] = (float)h[i];
+  }
+  __device__ __forceinline__ static uint4 pack(const float (&f)[kN]) {
+    h8 h;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) h[i] = (_Float16)f[i];
+    return __builtin_bit_cast(uint4, h);
+  }
+};
+
+// A row's chunks: chunk c starts at byte start(c).
+struct RowShape {
+  int bytes;    // of a row
+  int chunks;   // ceil(bytes / 16)
+  __device__ __forceinline__ int start(int c) const {
+    return bytes >= 16 ? min(16 * c, bytes - 16) : 0;
+  }
+};
+
+// Sixteen bytes at p (all of the row where it is shorter).  kAligned: p is
+// 16-byte aligned and the row a multiple of 16 bytes.
+template <bool kAligned>
+__device__ __forceinline__ uint4 load_chunk(const uint8_t* p, int row_bytes) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (kAligned) {
+    v = *reinterpret_cast<const uint4*>(p);
+  } else if (row_bytes >= 16) {
+    __builtin_memcpy(&v, p, 16);
+  } else {
+    uint32_t w[4] = {0, 0, 0, 0};
+    for (int i = 0; i < row_bytes; ++i) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+
+template <bool kAligned>
+__device__ __forceinline__ void store_chunk(uint8_t* p, int row_bytes, const uint4& v) {
+  if (kAligned) {
+    *reinterpret_cast<uint4*>(p) = v;
+  } else if (row_bytes >= 16) {
+    __builtin_memcpy(p, &v, 16);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < row_bytes; ++i) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
+// Lane k of a wave holds pick k's slot (-1: none, or not a row).  Returns
+// the valid picks as a bit mask; `bad` says whether a slot lies past the
+// buffer.
+__device__ __forceinline__ unsigned long long token_slots(const int32_t* slot_of, long long t,
+                                                          int K, int rows_total, int lane,
+                                                          int& s, bool& bad) {
+  s = lane < K ? slot_of[t * K + lane] : -1;
+  bad = __ballot(s >= rows_total) != 0;
+  return __ballot(s >= 0 && s < rows_total);
+}
+
+// Rows of the buffer that no token goes to are set to zero: one wave per 64
+// rows reads their sources and clears those without one.
+__device__ __forceinline__ void zero_rows(long long w, const int32_t* __restrict__ row_src,
+                                          int rows_total, long long row_bytes, uint8_t* a) {
+  const int lane = threadIdx.x & 63;
+  const long long r0 = w * 64;
+  const long long r = r0 + lane;
+  unsigned long long m = __ballot(r < rows_total && row_src[r < rows_total ? r : 0] < 0);
+  while (m) {
+    const int i = __ffsll((long long)m) - 1;
+    m &= m - 1;
+    uint8_t* p = a + (r0 + i) * row_bytes;
+    // the row's 16-byte aligned part by 16, its ends byte by byte
+    const long long head = min((long long)((16 - ((uintptr_t)p & 15)) & 15), row_bytes);
+    const long long mid = (row_bytes - head) / 16;
+    for (long long c = lane; c < mid; c += 64)
+      reinterpret_cast<uint4*>(p + head)[c] = make_uint4(0, 0, 0, 0);
+    if (lane < head) p[lane] = 0;
+    const long long tail = head + mid * 16 + lane;
+    if (lane < 16 && tail < row_bytes) p[tail] = 0;
+  }
+}
+
+// One wave per piece of a source row (at most 64 kRowChunks chunks).
+template <bool kAligned>
+__global__ __launch_bounds__(kRowThreads) void permute_rows_kernel(
+    const uint8_t* __restrict__ x, const int32_t* __restrict__ slot_of, int T, int K,
+    RowShape row, int pieces, int plen, int rows_total, uint8_t* __restrict__ a,
+    const int32_t* __restrict__ row_src, long long zero_waves, int32_t* __restrict__ status) {
+  const int lane = threadIdx.x & 63;
+  const long long units = zero_waves + (long long)T * pieces;
+  for (long long w = (long long)blockIdx.x * kRowWaves + (threadIdx.x >> 6); w < units;
+       w += (long long)gridDim.x * kRowWaves) {
+    if (w < zero_waves) {
+      zero_rows(w, row_src, rows_total, row.bytes, a);
+      continue;
+    }
+    const long long u0 = w - zero_waves;
+    const long long t = u0 / pieces;
+    const int c0 = (int)(u0 - t * pieces) * plen;
+    const int cend = min(c0 + plen, row.chunks);
+    int s;
+    bool bad;
+    unsigned long long m = token_slots(slot_of, t, K, rows_total, lane, s, bad);
+    if (bad && lane == 0 && c0 == 0) atomicOr(status, MOE_ERR_BAD_INDEX);
+    const uint8_t* src = x + t * (long long)row.bytes;
+    uint4 v[kRowChunks];
+#pragma unroll
+    for (int u = 0; u < kRowChunks; ++u) {
+      const int c = c0 + lane + u * 64;
+      v[u] = load_chunk<kAligned>(src + row.start(c < cend ? c : c0), row.bytes);
+    }
+    while (m) {
+      const int k = __ffsll((long long)m) - 1;
+      m &= m - 1;
+      uint8_t* dst = a + (long long)__builtin_amdgcn_readlane(s, k) * row.bytes;
+#pragma unroll
+      for (int u = 0; u < kRowChunks; ++u) {
+        const int c = c0 + lane + u * 64;
+        if (c < cend) store_chunk<kAligned>(dst + row.start(c), row.bytes, v[u]);
+      }
+    }
+  }
+}
+
+// out[t] = sum over the valid picks, in ascending k, of (w[t, k] *) y[slot]:
+// the combine, and (kWeighted false) the gradient of the permute.
+template <typename El, bool kAligned, bool kWeighted>
+__global__ __launch_bounds__(kRowThreads) void gather_sum_kernel(
+    const uint8_t* __restrict__ y, int rows_total, const int32_t* __restrict__ slot_of,
+    const float* __restrict__ topk_w, int T, int K, RowShape row, int pieces, int plen,
+    uint8_t* __restrict__ out, int32_t* __restrict__ status) {
+  constexpr int N = El::kN;
+  const int lane = threadIdx.x & 63;
+  const long long units = (long long)T * pieces;
+  for (long long w = (long long)blockIdx.x * kRowWaves + (threadIdx.x >> 6); w < units;
+       w += (long long)gridDim.x * kRowWaves) {
+    const long long t = w / pieces;
+    const int c0 = (int)(w - t * pieces) * plen;
+    const int cend = min(c0 + plen, row.chunks);
+    int s;
+    bool bad;
+    unsigned long long m = token_slots(slot_of, t, K, rows_total, lane, s, bad);
+    const float wt = kWeighted && lane < K ? topk_w[t * K + lane] : 1.f;
+    if (bad && lane == 0 && c0 == 0) atomicOr(status, MOE_ERR_BAD_INDEX);
+    float acc[kRowChunks][N];
+#pragma unroll
+    for (int u = 0; u < kRowChunks; ++u)
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[u][i] = 0.f;
+    while (m) {
+      const int k = __ffsll((long long)m) - 1;
+      m &= m - 1;
+      const uint8_t* src = y + (long long)__builtin_amdgcn_readlane(s, k) * row.bytes;
+      const float wk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wt), k));
+      uint4 v[kRowChunks];
+#pragma unroll
+      for (int u = 0; u < kRowChunks; ++u) {
+        const int c = c0 + lane + u * 64;
+        v[u] = load_chunk<kAligned>(src + row.start(c < cend ? c : c0), row.bytes);
+      }
+#pragma unroll
+      for (int u = 0; u < kRowChunks; ++u) {
+        float f[N];
+        El::unpack(v[u], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          acc[u][i] = kWeighted ? fmaf(wk, f[i], acc[u][i]) : acc[u][i] + f[i];
+      }
+    }
+    uint8_t* dst = out + t * (long long)row.bytes;
+#pragma unroll
+    for (int u = 0; u < kRowChunks; ++u) {
+      const int c = c0 + lane + u * 64;
+      if (c < cend) store_chunk<kAligned>(dst + row.start(c), row.bytes, El::pack(acc[u]));
+    }
+  }
+}
+
+// Gradient of the combine, one workgroup per token: its dout row is read
+// once and kept in registers piece by piece, each of its y rows is read and
+// its dy row written in the same pass.  A wave's partial dot products are
+// summed over its lanes, and the waves' in a fixed order.
+template <typename El, bool kAligned>
+__global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(
+    const uint8_t* __restrict__ dout, const uint8_t* __restrict__ y, int rows_total,
+    const int32_t* __restrict__ slot_of, const float* __restrict__ topk_w, int T, int K,
+    RowShape row, uint8_t* __restrict__ dy, float* __restrict__ dw,
+    const int32_t* __restrict__ row_src, long long zero_blocks, int32_t* __restrict__ status) {
+  constexpr int N = El::kN;
+  __shared__ float part[kRowWaves][MOE_MAX_TOPK];
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const long long blocks = zero_blocks + T;
+  for (long long b = blockIdx.x; b < blocks; b += gridDim.x) {
+    if (b < zero_blocks) {
+      zero_rows(b * kRowWaves + wave, row_src, rows_total, row.bytes, dy);
+      continue;
+    }
+    const long long t = b - zero_blocks;
+    int s;
+    bool bad;
+    const unsigned long long valid = token_slots(slot_of, t, K, rows_total, lane, s, bad);
+    const float wt = topk_w && lane < K ? topk_w[t * K + lane] : 0.f;
+    if (bad && threadIdx.x == 0) atomicOr(status, MOE_ERR_BAD_INDEX);
+    float dots = 0.f;   // of pick `lane`
+    for (int c0 = wave * 64; c0 < row.chunks; c0 += kRowThreads) {
+      const int c = c0 + lane;
+      const bool in = c < row.chunks;
+      const int at = row.start(in ? c : 0);
+      // elements of this chunk that the chunk before it has too
+      const int skip = kAligned ? 0 : (16 * c - at) / El::kSize;
+      float g[N];
+      El::unpack(load_chunk<kAligned>(dout + t * (long long)row.bytes + at, row.bytes), g);
+      unsigned long long m = valid;
+      while (m) {
+        const int k = __ffsll((long long)m) - 1;
+        m &= m - 1;
+        const long long off = (long long)__builtin_amdgcn_readlane(s, k) * row.bytes + at;
+        const float wk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wt), k));
+        if (dw) {
+          float f[N];
+          El::unpack(load_chunk<kAligned>(y + off, row.bytes), f);
+          float d = 0.f;
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (kAligned || i >= skip) d = fmaf(g[i], f[i], d);
+          d = in ? d : 0.f;
+          for (int o = 32; o >= 1; o >>= 1) d += __shfl_xor(d, o);
+          if (lane == k) dots += d;
+        }
+        if (dy && in) {
+          float f[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) f[i] = wk * g[i];
+          store_chunk<kAligned>(dy + off, row.bytes, El::pack(f));
+        }
+      }
+    }
+    if (dw) {
+      part[wave][lane] = dots;
+      __syncthreads();
+      if (threadIdx.x < K) {
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRowWaves; ++i) d += part[i][threadIdx.x];
+        dw[t * K + threadIdx.x] = d;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+static int type_size(int dtype) {
+  switch (dtype) {
+    case MOE_TYPE_F32: return 4;
+    case MOE_TYPE_BF16:
+    case MOE_TYPE_F16: return 2;
+    case MOE_TYPE_U8: return 1;
+    default: return 0;
+  }
+}
+
+// Workgroups of a launch over `units` units, `per` of them to a workgroup:
+// a grid past 2^22 workgroups walks (HIP bounds a launch's threads by 2^32).
+static unsigned grid_for(long long units, int per) {
+  const long long b = (units + per - 1) / per;
+  return (unsigned)(b < 1 ? 1 : b > (1 << 22) ? (1 << 22) : b);
+}
+
+// Pieces of a row for one wave each, and their length in chunks.
+static void cut(const RowShape& row, int& pieces, int& plen) {
+  pieces = (row.chunks + 64 * kRowChunks - 1) / (64 * kRowChunks);
+  plen = (row.chunks + pieces - 1) / pieces;
+}
+
+// The checks that the four calls share.  Sizes first, then (by the caller)
+// the pointers that the sizes make necessary.
+static moe_status_t row_args(int dtype, int T, int K, int H, int rows_total, bool bytes_too,
+                             RowShape* row) {
+  const int es = type_size(dtype);
+  if (es == 0 || (es == 1 && !bytes_too)) return MOE_INVALID_ARG;
+  if (T < 0 || K <= 0 || K > MOE_MAX_TOPK || H <= 0 || rows_total < 0) return MOE_INVALID_ARG;
+  if ((long long)H * es > 0x7fffffffLL - 64) return MOE_UNSUPPORTED_SHAPE;
+  if ((long long)T * K > 0x7fffffffLL) return MOE_UNSUPPORTED_SHAPE;
+  row->bytes = H * es;
+  row->chunks = (row->bytes + 15) / 16;
+  return MOE_OK;
+}
+
+static bool wide(const RowShape& row, uintptr_t pointers) {
+  return row.bytes % 16 == 0 && (pointers & 15) == 0;
+}
+
+static moe_status_t launched() {
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
+}
+
+template <typename El, bool kWeighted>
+static moe_status_t gather_sum(const void* y, int rows_total, const int32_t* slot_of,
+                               const float* topk_w, int T, int K, const RowShape& row, void* out,
+                               int32_t* status, hipStream_t st) {
+  int pieces, plen;
+  cut(row, pieces, plen);
+  const dim3 grid(grid_for((long long)T * pieces, kRowWaves)), block(kRowThreads);
+  const uint8_t* yb = static_cast<const uint8_t*>(y);
+  uint8_t* ob = static_cast<uint8_t*>(out);
+  if (wide(row, (uintptr_t)y | (uintptr_t)out))
+    hipLaunchKernelGGL((gather_sum_kernel<El, true, kWeighted>), grid, block, 0, st, yb,
+                       rows_total, slot_of, topk_w, T, K, row, pieces, plen, ob, status);
+  else
+    hipLaunchKernelGGL((gather_sum_kernel<El, false, kWeighted>), grid, block, 0, st, yb,
+                       rows_total, slot_of, topk_w, T, K, row, pieces, plen, ob, status);
+  return launched();
+}
+
+template <bool kWeighted>
+static moe_status_t gather_sum_any(int dtype, const void* y, int rows_total,
+                                   const int32_t* slot_of, const float* topk_w, int T, int K,
+                                   const RowShape& row, void* out, int32_t* status,
+                                   void* stream) {
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == MOE_TYPE_F32)
+    return gather_sum<F32, kWeighted>(y, rows_total, slot_of, topk_w, T, K, row, out, status, st);
+  if (dtype == MOE_TYPE_BF16)
+    return gather_sum<BF16, kWeighted>(y, rows_total, slot_of, topk_w, T, K, row, out, status,
+                                       st);
+  return gather_sum<F16, kWeighted>(y, rows_total, slot_of, topk_w, T, K, row, out, status, st);
+}
+
+template <typename El>
+static moe_status_t combine_grad(const void* dout, const void* y, int rows_total,
+                                 const int32_t* slot_of, const float* topk_w, int T, int K,
+                                 const RowShape& row, void* dy, float* dw,
+                                 const int32_t* row_src, int32_t* status, void* stream) {
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const long long zero = row_src && dy ? ((long long)rows_total + 64 * kRowWaves - 1) /
+                                             (64 * kRowWaves) : 0;
+  const dim3 grid(grid_for(zero + T, 1)), block(kRowThreads);
+  const uint8_t* db = static_cast<const uint8_t*>(dout);
+  const uint8_t* yb = static_cast<const uint8_t*>(y);
+  uint8_t* gb = static_cast<uint8_t*>(dy);
+  if (wide(row, (uintptr_t)dout | (uintptr_t)y | (uintptr_t)dy))
+    hipLaunchKernelGGL((combine_grad_kernel<El, true>), grid, block, 0, st, db, yb, rows_total,
+                       slot_of, topk_w, T, K, row, gb, dw, row_src, zero, status);
+  else
+    hipLaunchKernelGGL((combine_grad_kernel<El, false>), grid, block, 0, st, db, yb, rows_total,
+                       slot_of, topk_w, T, K, row, gb, dw, row_src, zero, status);
+  return launched();
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status_t moe_permute_rows(const void* x, int dtype, int T, int K, int H,
+                                         const int32_t* slot_of, int rows_total, void* a,
+                                         const int32_t* row_src, int32_t* status_dev,
+                                         void* stream) {
+  RowShape row;
+  const moe_status_t ok = row_args(dtype, T, K, H, rows_total, true, &row);
+  if (ok != MOE_OK) return ok;
+  if (rows_total == 0 && T == 0) return MOE_OK;
+  if (!status_dev || (T > 0 && (!x || !slot_of)) || (rows_total > 0 && !a))
+    return MOE_INVALID_ARG;
+  if (((uintptr_t)x | (uintptr_t)a) & (type_size(dtype) - 1)) return MOE_UNSUPPORTED_SHAPE;
+  int pieces, plen;
+  cut(row, pieces, plen);
+  const long long zero = row_src ? ((long long)rows_total + 63) / 64 : 0;
+  const long long units = zero + (long long)T * pieces;
+  if (units == 0) return MOE_OK;
+  const dim3 grid(grid_for(units, kRowWaves)), block(kRowThreads);
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const uint8_t* xb = static_cast<const uint8_t*>(x);
+  uint8_t* ab = static_cast<uint8_t*>(a);
+  if (wide(row, (uintptr_t)x | (uintptr_t)a))
+    hipLaunchKernelGGL((permute_rows_kernel<true>), grid, block, 0, st, xb, slot_of, T, K, row,
+                       pieces, plen, rows_total, ab, row_src, zero, status_dev);
+  else
+    hipLaunchKernelGGL((permute_rows_kernel<false>), grid, block, 0, st, xb, slot_of, T, K, row,
+                       pieces, plen, rows_total, ab, row_src, zero, status_dev);
+  return launched();
+}
+
+extern "C" moe_status_t moe_permute_rows_grad(const void* da, int dtype, int rows_total,
+                                              const int32_t* slot_of, int T, int K, int H,
+                                              void* dx, int32_t* status_dev, void* stream) {
+  RowShape row;
+  const moe_status_t ok = row_args(dtype, T, K, H, rows_total, false, &row);
+  if (ok != MOE_OK) return ok;
+  if (T == 0) return MOE_OK;
+  if (!slot_of || !dx || !status_dev || (rows_total > 0 && !da)) return MOE_INVALID_ARG;
+  if (((uintptr_t)da | (uintptr_t)dx) & (type_size(dtype) - 1)) return MOE_UNSUPPORTED_SHAPE;
+  return gather_sum_any<false>(dtype, da, rows_total, slot_of, nullptr, T, K, row, dx,
+                               status_dev, stream);
+}
+
+extern "C" moe_status_t moe_combine_rows(const void* y, int dtype, int rows_total,
+                                         const int32_t* slot_of, const float* topk_w, int T,
+                                         int K, int H, void* out, int32_t* status_dev,
+                                         void* stream) {
+  RowShape row;
+  const moe_status_t ok = row_args(dtype, T, K, H, rows_total, false, &row);
+  if (ok != MOE_OK) return ok;
+  if (T == 0) return MOE_OK;
+  if (!slot_of || !topk_w || !out || !status_dev || (rows_total > 0 && !y))
+    return MOE_INVALID_ARG;
+  if (((uintptr_t)y | (uintptr_t)out) & (type_size(dtype) - 1)) return MOE_UNSUPPORTED_SHAPE;
+  return gather_sum_any<true>(dtype, y, rows_total, slot_of, topk_w, T, K, row, out, status_dev,
+                              stream);
+}
+
+extern "C" moe_status_t moe_combine_rows_grad(const void* dout, const void* y, int dtype,
+                                              int rows_total, const int32_t* slot_of,
+                                              const float* topk_w, int T, int K, int H, void* dy,
+                                              float* dtopk_w, const int32_t* row_src,
+                                              int32_t* status_dev, void* stream) {
+  RowShape row;
+  const moe_status_t ok = row_args(dtype, T, K, H, rows_total, false, &row);
+  if (ok != MOE_OK) return ok;
+  // (an output without elements may be NULL as well)
+  if (!dy && !dtopk_w) return T == 0 || rows_total == 0 ? MOE_OK : MOE_INVALID_ARG;
+  if (!status_dev || (T > 0 && (!dout || !slot_of))) return MOE_INVALID_ARG;
+  if (dy && T > 0 && !topk_w) return MOE_INVALID_ARG;
+  if (dtopk_w && rows_total > 0 && !y) return MOE_INVALID_ARG;
+  if (((uintptr_t)dout | (uintptr_t)(dtopk_w ? y : nullptr) | (uintptr_t)dy) &
+      (type_size(dtype) - 1))
+    return MOE_UNSUPPORTED_SHAPE;
+  if (T == 0 && !(row_src && dy && rows_total > 0)) return MOE_OK;
+  if (!dtopk_w) y = nullptr;   // not read
+  if (dtype == MOE_TYPE_F32)
+    return combine_grad<F32>(dout, y, rows_total, slot_of, topk_w, T, K, row, dy, dtopk_w,
+                             row_src, status_dev, stream);
+  if (dtype == MOE_TYPE_BF16)
+    return combine_grad<BF16>(dout, y, rows_total, slot_of, topk_w, T, K, row, dy, dtopk_w,
+                              row_src, status_dev, stream);
+  return combine_grad<F16>(dout, y, rows_total, slot_of, topk_w, T, K, row, dy, dtopk_w,
+                           row_src, status_dev, stream);
+}

@@ -372,6 +372,125 @@ def moe_act_requant_e8m0(h, offsets, counts, q, q_scale, status, stream=None):
     check(st, "moe_act_requant_e8m0")
 
 
+# ---- rows in 32-, 16- and 8-bit types, sorted by expert and back, with their
+# gradients
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_BYTE_TYPES = {torch.uint8: 3, torch.int8: 3, torch.float8_e4m3fn: 3}
+
+
+def _type(t, name, bytes_too=False):
+    code = _TYPES.get(t.dtype)
+    if code is None and bytes_too:
+        code = _BYTE_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: dtype {t.dtype} is not supported")
+    return code
+
+
+def _call(name, stream, tensors, *args):
+    """Calls library function `name` on the device that the tensors share
+    (which need not be the current one), on `stream` or that device's
+    current stream."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"{name}: tensors on {dev}, stream on {stream.device}")
+    fn = getattr(load(), name)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    check(st, name)
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: must have two dimensions, has {t.dim()}")
+    return t.shape
+
+
+def moe_sort_tokens(topk_idx, E, layout, align_m, rows, counts, offsets, slot_of, row_src,
+                    row_expert, workspace, status, stream=None):
+    """The indices of moe_dispatch_layout (counts, offsets, slot_of, row_src,
+    row_expert; status bits) without moving any rows.  rows is M_cap
+    (contiguous) or the per-expert capacity C (masked); workspace holds
+    moe_layout_workspace_bytes(T, K, E) bytes."""
+    T, K = _matrix(topk_idx, "topk_idx")
+    rows_total = E * rows if layout == LAYOUT_MASKED else rows
+    _call("moe_sort_tokens", stream,
+          (topk_idx, counts, offsets, slot_of, row_src, row_expert, workspace, status),
+          _ptr(topk_idx, _I32, "topk_idx"), T, K, E, layout, align_m, rows,
+          _ptr(counts, _I32, "counts", (E,)), _ptr(offsets, _I32, "offsets", (E + 1,)),
+          _ptr(slot_of, _I32, "slot_of", (T, K)), _ptr(row_src, _I32, "row_src", (rows_total,)),
+          _ptr(row_expert, _I32, "row_expert", (rows_total,)),
+          _ptr(workspace, (torch.uint8,), "workspace"), workspace.numel(),
+          _ptr(status, _I32, "status", (1,)))
+
+
+def moe_permute_rows(x, slot_of, a, status, row_src=None, stream=None):
+    """a[slot_of[t, k]] = x[t] for every valid pick: x [T, H], a [rows_total, H]
+    of the same dtype (float32, bfloat16, float16 or an 8-bit type), any H.
+    Rows of a that no token goes to are left as they are, or set to zero if
+    row_src [rows_total] is given."""
+    T, H = _matrix(x, "x")
+    K = _matrix(slot_of, "slot_of")[1]
+    R = _matrix(a, "a")[0]
+    code = _type(x, "x", True)
+    ts = (x, slot_of, a, status) + (() if row_src is None else (row_src,))
+    _call("moe_permute_rows", stream, ts, _ptr(x, (x.dtype,), "x"), code, T, K, H,
+          _ptr(slot_of, _I32, "slot_of", (T, K)), R, _ptr(a, (x.dtype,), "a", (R, H)),
+          None if row_src is None else _ptr(row_src, _I32, "row_src", (R,)),
+          _ptr(status, _I32, "status", (1,)))
+
+
+def moe_permute_rows_grad(da, slot_of, dx, status, stream=None):
+    """dx[t] = sum_k da[slot_of[t, k]]: the gradient of moe_permute_rows
+    (float32, bfloat16 or float16; fp32 sums in ascending k)."""
+    R, H = _matrix(da, "da")
+    T, K = _matrix(slot_of, "slot_of")
+    code = _type(da, "da")
+    _call("moe_permute_rows_grad", stream, (da, slot_of, dx, status),
+          _ptr(da, (da.dtype,), "da"), code, R, _ptr(slot_of, _I32, "slot_of"), T, K, H,
+          _ptr(dx, (da.dtype,), "dx", (T, H)), _ptr(status, _I32, "status", (1,)))
+
+
+def moe_combine_rows(y, slot_of, topk_w, out, status, stream=None):
+    """out[t] = sum_k topk_w[t, k] * y[slot_of[t, k]] in float32, bfloat16 or
+    float16 (fp32 sums in ascending k); y [rows_total, H], any H."""
+    R, H = _matrix(y, "y")
+    T, K = _matrix(slot_of, "slot_of")
+    code = _type(y, "y")
+    _call("moe_combine_rows", stream, (y, slot_of, topk_w, out, status),
+          _ptr(y, (y.dtype,), "y"), code, R, _ptr(slot_of, _I32, "slot_of"),
+          _ptr(topk_w, _F32, "topk_w", (T, K)), T, K, H, _ptr(out, (y.dtype,), "out", (T, H)),
+          _ptr(status, _I32, "status", (1,)))
+
+
+def moe_combine_rows_grad(dout, y, slot_of, topk_w, dy, dtopk_w, status, row_src=None,
+                          stream=None):
+    """Gradients of moe_combine_rows: dy[slot_of[t, k]] = topk_w[t, k] * dout[t]
+    and dtopk_w[t, k] = <dout[t], y[slot_of[t, k]]> (float32; 0 without a
+    row).  dy or dtopk_w may be None.  Rows of dy that no token has are left
+    as they are, or set to zero if row_src is given."""
+    T, H = _matrix(dout, "dout")
+    K = _matrix(slot_of, "slot_of")[1]
+    R = _matrix(y, "y")[0]
+    code = _type(dout, "dout")
+    if dy is None and dtopk_w is None:
+        raise ValueError("moe_combine_rows_grad: neither dy nor dtopk_w is given")
+    given = [t for t in (dy, dtopk_w, row_src) if t is not None]
+    _call("moe_combine_rows_grad", stream, (dout, y, slot_of, topk_w, status, *given),
+          _ptr(dout, (dout.dtype,), "dout"), _ptr(y, (dout.dtype,), "y", (R, H)), code, R,
+          _ptr(slot_of, _I32, "slot_of", (T, K)), _ptr(topk_w, _F32, "topk_w", (T, K)), T, K, H,
+          None if dy is None else _ptr(dy, (dout.dtype,), "dy", (R, H)),
+          None if dtopk_w is None else _ptr(dtopk_w, _F32, "dtopk_w", (T, K)),
+          None if row_src is None else _ptr(row_src, _I32, "row_src", (R,)),
+          _ptr(status, _I32, "status", (1,)))
+
+
 def moe_ceiling_copy(src, dst, stream=None):
     """Copy src to dst (same byte size) with the library's plain copy kernel
     (a measurement helper: HBM ceiling)."""

@@ -69,6 +69,13 @@ typedef int32_t moe_status_t;
 #define MOE_LAYOUT_CONTIGUOUS 0 /* prefill: expert segments stacked along M */
 #define MOE_LAYOUT_MASKED 1     /* decode: fixed [E, C, .] + device counts  */
 
+/* element types of the calls that take one (moe_permute_rows and the others
+ * in 32, 16 and 8 bits) */
+#define MOE_TYPE_F32 0
+#define MOE_TYPE_BF16 1
+#define MOE_TYPE_F16 2  /* IEEE binary16 */
+#define MOE_TYPE_U8 3   /* any 8-bit codes, moved as bytes */
+
 /* bits OR-ed into *status_dev */
 #define MOE_ERR_BAD_EXPERT 1 /* topk id outside [-1, E): entry skipped     */
 #define MOE_ERR_OVERFLOW 2   /* row did not fit: dropped in stable order  */
@@ -420,6 +427,64 @@ moe_status_t moe_gate_up_act_fp8_gather_e8m0(const uint8_t* x, int T, const int3
                                              const int32_t* counts, int E, int rows_total,
                                              int I, int H, uint8_t* q2, uint32_t* q2_scale,
                                              int32_t* status_dev, void* stream);
+
+/*
+ * Tokens sorted by expert and back, in 32-, 16- and 8-bit types, with the
+ * gradients [H100-EP 基于 DeepEP 的专家并行: the same token shuffle and combine
+ * as moe_dispatch_layout and moe_combine, for rows that are not FP8 and for
+ * training, where both are differentiated].
+ *
+ * moe_sort_tokens writes exactly the indices that moe_dispatch_layout
+ * writes (counts, offsets, slot_of, row_src, row_expert, the same order,
+ * drops and status bits) and moves no rows.  Arguments as there.
+ *
+ * The row calls take slot_of [T, K] (row of each (token, pick), -1 = none;
+ * distinct for distinct picks, as moe_sort_tokens writes it) and rows of H
+ * elements of `dtype`; any H >= 1, every buffer aligned to its element.
+ * With S(t) = the picks k with 0 <= slot_of[t, k] < rows_total:
+ *
+ *   moe_permute_rows       a[slot_of[t, k], :] = x[t, :]         k in S(t)
+ *   moe_permute_rows_grad  dx[t, :] = round(sum_{k in S(t)} da[slot_of[t, k], :])
+ *   moe_combine_rows       out[t, :] = round(sum_{k in S(t)} topk_w[t, k] *
+ *                                            y[slot_of[t, k], :])
+ *   moe_combine_rows_grad  dy[slot_of[t, k], :] = round(topk_w[t, k] * dout[t, :])
+ *                          dtopk_w[t, k] = sum_h dout[t, h] * y[slot_of[t, k], h]
+ *                                          (0 for k not in S(t))
+ *
+ * Sums are fp32, in ascending k (no atomics: the same call gives the same
+ * bits), and rounded once, to nearest even; a token with no row gives 0.  A
+ * row that no token has is never read (whatever it holds), and is left as it
+ * is -- unless row_src [rows_total] (as moe_sort_tokens writes it) is given
+ * to the two calls that write rows: then rows with row_src < 0 are set to 0.
+ * moe_combine_rows in bf16 equals moe_combine bit for bit.
+ *
+ *   x, dx, dout, out [T, H]    a, da, y, dy [rows_total, H]
+ *   topk_w, dtopk_w [T, K] f32
+ *   dtype  MOE_TYPE_F32, _BF16 or _F16; moe_permute_rows also _U8
+ *   dy or dtopk_w may be NULL (that gradient is then not computed; without
+ *   dtopk_w, y is not read; without dy, topk_w is not); not both.
+ * Slots >= rows_total are skipped and set MOE_ERR_BAD_INDEX.  If one row is
+ * named by two tokens, moe_permute_rows and dy leave either's values (or
+ * 16-byte pieces of both) in it.  Outputs may not overlap inputs.
+ */
+moe_status_t moe_sort_tokens(const int32_t* topk_idx, int T, int K, int E, int layout,
+                             int align_m, int rows, int32_t* counts, int32_t* offsets,
+                             int32_t* slot_of, int32_t* row_src, int32_t* row_expert,
+                             void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                             void* stream);
+moe_status_t moe_permute_rows(const void* x, int dtype, int T, int K, int H,
+                              const int32_t* slot_of, int rows_total, void* a,
+                              const int32_t* row_src, int32_t* status_dev, void* stream);
+moe_status_t moe_permute_rows_grad(const void* da, int dtype, int rows_total,
+                                   const int32_t* slot_of, int T, int K, int H, void* dx,
+                                   int32_t* status_dev, void* stream);
+moe_status_t moe_combine_rows(const void* y, int dtype, int rows_total, const int32_t* slot_of,
+                              const float* topk_w, int T, int K, int H, void* out,
+                              int32_t* status_dev, void* stream);
+moe_status_t moe_combine_rows_grad(const void* dout, const void* y, int dtype, int rows_total,
+                                   const int32_t* slot_of, const float* topk_w, int T, int K,
+                                   int H, void* dy, float* dtopk_w, const int32_t* row_src,
+                                   int32_t* status_dev, void* stream);
 
 /*
  * Measurement helpers (not steps of the layer).  They time the two
