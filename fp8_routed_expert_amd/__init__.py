@@ -13,7 +13,11 @@ from .ops import (moe_layout_workspace_bytes, moe_gemm_large_tiles, moe_gemm_til
                   moe_gate_up_act_fp8_gather, moe_gate_up_act_fp8_gather_e8m0,
                   moe_sort_tokens, moe_permute_rows, moe_permute_rows_grad,
                   moe_combine_rows, moe_combine_rows_grad,
+                  moe_quantize_int8, moe_gemm_int8, moe_linear_int8,
+                  moe_linear_int8_workspace_bytes, moe_grouped_gemm_int8,
+                  moe_grouped_gemm_int8_gather, moe_act_requant_int8,
                   moe_ceiling_copy, moe_ceiling_mfma_fp8,
                   LAYOUT_CONTIGUOUS, LAYOUT_MASKED,
                   ERR_BAD_EXPERT, ERR_OVERFLOW, ERR_BAD_INDEX)
 from .layer import MoELayer, contiguous_rows  # noqa: F401
+from .routing import SortedTokens, sort_tokens, permute_tokens, combine_tokens  # noqa: F401

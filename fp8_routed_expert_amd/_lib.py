@@ -77,6 +77,19 @@ SIGNATURES = {
         _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
     "moe_combine_rows_grad": (ctypes.c_int32, [
         _vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp]),
+    "moe_quantize_int8": (ctypes.c_int32, [_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
+    "moe_gemm_int8": (ctypes.c_int32, [
+        _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp]),
+    "moe_grouped_gemm_int8": (ctypes.c_int32, [
+        _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp]),
+    "moe_grouped_gemm_int8_gather": (ctypes.c_int32, [
+        _vp, _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _c_int,
+        _vp, _vp]),
+    "moe_act_requant_int8": (ctypes.c_int32, [
+        _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp]),
+    "moe_linear_int8_workspace_bytes": (_size, [_c_int, _c_int]),
+    "moe_linear_int8": (ctypes.c_int32, [
+        _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _size, _vp]),
     "moe_ceiling_copy": (ctypes.c_int32, [_vp, _vp, _size, _vp]),
     "moe_ceiling_mfma_fp8": (ctypes.c_int32, [_c_int, _c_int, _vp, _vp, _vp]),
 }

@@ -18,20 +18,6 @@ namespace moe {
 constexpr int kActThreads = 256;
 constexpr int kActCols = kActThreads * 8;   // columns per workgroup
 
-// Is permuted row m inside an expert segment?  Binary search for the last
-// segment start <= m, then check that segment's valid range.
-__device__ __forceinline__ bool row_valid(const int32_t* offsets, const int32_t* counts,
-                                          int E, int rows_total, int m) {
-  int lo = 0, hi = E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (offsets[mid] <= m) lo = mid; else hi = mid - 1;
-  }
-  int s, en;
-  expert_rows(offsets, counts, lo, rows_total, s, en);
-  return m >= s && m < en;
-}
-
 // kPow2: power-of-two scales stored as E8M0 bytes, four 128-column blocks
 // per 32-bit word, words K-block-major ([ceil(I/512), rows_total]).
 template <bool kPow2>

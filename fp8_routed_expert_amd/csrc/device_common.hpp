@@ -153,6 +153,20 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets,
   end = (int)lim;
 }
 
+// Is permuted row m inside an expert segment?  Binary search for the last
+// segment start <= m, then check that segment's valid range.
+__device__ __forceinline__ bool row_valid(const int32_t* offsets, const int32_t* counts,
+                                          int E, int rows_total, int m) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (offsets[mid] <= m) lo = mid; else hi = mid - 1;
+  }
+  int s, en;
+  expert_rows(offsets, counts, lo, rows_total, s, en);
+  return m >= s && m < en;
+}
+
 // Does the segment table fail to describe segments?  True when a start is
 // negative, the starts decrease, or a count is negative, for any expert
 // handled by this wave (expert base + lane, for base = 0, 64, ...).  A

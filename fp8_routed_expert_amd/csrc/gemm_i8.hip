@@ -1,0 +1,466 @@
+// Matrix products in 8-bit integers with one scale per token and one per
+// output channel, dense and over the expert segments:
+//
+//   c[m, n] = round( a_scale[m] * w_scale[e, n] * sum_k a[m, k] * w[e, n, k] )
+//
+// The sums are exact 32-bit integers (|a|, |w| <= 128: K may reach 131,056),
+// so the order of K does not matter, and neither does any split of it; the
+// scales are applied once, in fp32, when a tile is stored.
+//
+// Tiles, as the FP8 products have them (gfx950): a workgroup multiplies a
+// BM x BN tile with waves of WM x WN, K advancing 128 bytes a step.  The
+// tile's rows of a and w come from global memory straight into LDS
+// (buffer_load ... lds), a's a step further ahead than w's; a wave reads
+// fragments of 16 rows x 32 bytes and v_mfma_i32_16x16x64_i8 consumes 16 of
+// the 32 at a time (which 64 of the 128 k an instruction takes is free, as
+// long as both operands agree).  The weights are the first operand, so a
+// lane's four sums are four channels of one token.
+//
+// K need only be a multiple of 16: where it is none of 128 (kRagged) every
+// load compares its place in the row with K, and lanes past the end take an
+// offset out of the descriptor's range, which reads zero.  Channels past N
+// lie past the weight descriptor's range in the same way.
+#include <type_traits>
+
+#include "gemm_tiles.hpp"
+
+namespace moe {
+
+constexpr uint32_t kOutOfRange = 0x80000000u;
+
+__device__ __forceinline__ v4i mfma_i8(const v4i& a, const v4i& b, const v4i& c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, (h2){(_Float16)lo, (_Float16)hi});
+}
+
+// The arguments of a product.  offsets == nullptr: dense (one weight matrix,
+// every row of it).  row_src != nullptr: buffer row r is row row_src[r] of a
+// [src_rows, K], its scale a_scale[row_src[r]].
+struct I8Args {
+  const uint8_t* a;
+  const float* a_scale;
+  const uint8_t* w;
+  const float* w_scale;
+  const int32_t* offsets;
+  const int32_t* counts;
+  const int32_t* row_src;
+  int E, rows_total, N, K, src_rows;
+  void* c;
+  int c_type;
+  int32_t* status;
+};
+
+template <int BM, int BN, int WM, int WN, int GM, bool kGather, bool kRagged>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_kernel(I8Args p) {
+  constexpr int NWM = BM / WM;
+  constexpr int NWN = BN / WN;
+  constexpr int NW = NWM * NWN;
+  constexpr int MI = WM / 16;
+  constexpr int NJ = WN / 16;
+  constexpr int CA = BM / 8 / NW;   // 1 KB chunks (8 rows) of a stage per wave
+  constexpr int CB = BN / 8 / NW;
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "chunks must split evenly");
+  static_assert(MI >= 2, "the late loads need a subtile row before the barrier");
+  constexpr int SA_B = BM * kBK, SB_B = BN * kBK;
+  constexpr int NSA = 3 * SA_B + 2 * SB_B <= kLdsBytes ? 3 : 2;
+  static_assert(NSA * SA_B + 2 * SB_B <= kLdsBytes, "tile stages exceed the LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[SA_B];
+  __shared__ __attribute__((aligned(1024))) uint8_t sA1[SA_B];
+  uint8_t* const sA2 = ThirdStage<NSA == 3 ? SA_B : 0>::get();
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[SB_B];
+  __shared__ __attribute__((aligned(1024))) uint8_t sB1[SB_B];
+  auto stA = [&](int i) -> uint8_t* { return i == 0 ? sA0 : i == 1 ? sA1 : sA2; };
+  auto stB = [&](int i) -> uint8_t* { return i == 0 ? sB0 : sB1; };
+
+  // ---- which tile (the tile list's order is that of the FP8 products)
+  const int N = p.N, K = p.K, rows_total = p.rows_total;
+  const int lane = threadIdx.x & 63;
+  const int n_tiles = (N + BN - 1) / BN;
+  const bool dense = p.offsets == nullptr;
+  const int total_m = dense ? (rows_total + BM - 1) / BM
+                            : total_mtiles<BM>(p.offsets, p.counts, p.E, rows_total, lane);
+  const int logical = blockIdx.x;
+  if (!dense && logical == 0 && threadIdx.x < 64 && p.status &&
+      segments_bad(p.offsets, p.counts, p.E, lane) && lane == 0)
+    atomicOr(p.status, MOE_ERR_BAD_INDEX);
+  if ((long long)logical >= (long long)total_m * n_tiles) return;
+  const int grp = logical / (GM * n_tiles);
+  const int in_grp = logical - grp * (GM * n_tiles);
+  const int gm_cnt = min(GM, total_m - grp * GM);
+  const int tile_n = in_grp / gm_cnt;
+  const int tile_m = grp * GM + (in_grp - tile_n * gm_cnt);
+  int e_sel = 0, row0 = tile_m * BM, row_end = rows_total;
+  if (!dense) {
+    find_mtile<BM>(p.offsets, p.counts, p.E, rows_total, tile_m, lane, e_sel, row0, row_end);
+    if (e_sel < 0) return;
+  }
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / NWN;
+  const int wn = wave - wm * NWN;
+  const int Kb = (K + kBK - 1) / kBK;
+  const int n0 = tile_n * BN;
+
+  // ---- tile loads.  A chunk is 8 rows; the lane's row is lane / 8, its
+  // 16-byte piece the one that belongs at place lane % 8 of that row in an
+  // even (odd) 8-row half.
+  const int piece0 = (lane & 7) ^ (lane >> 3);
+  uint32_t vl[2];
+  int lim[2];
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    vl[o] = (uint32_t)(lane >> 3) * (uint32_t)K + (uint32_t)((piece0 ^ o) << 4);
+    lim[o] = K - ((piece0 ^ o) << 4);
+  }
+  const long long a_bytes = kGather ? (long long)p.src_rows * K : (long long)(rows_total - row0) * K;
+  const v4i rsrc_a = make_rsrc(kGather ? p.a : p.a + (size_t)row0 * K,
+                               (uint32_t)(a_bytes > 0x7ffff000LL ? 0x7ffff000LL : a_bytes));
+  const v4i rsrc_b = make_rsrc(p.w + ((size_t)e_sel * N + n0) * K,
+                               (uint32_t)((long long)min(BN, N - n0) * K));
+  uint32_t a_off[kGather ? CA : 1];
+  if constexpr (kGather) {
+#pragma unroll
+    for (int u = 0; u < CA; ++u) {
+      const int c = wave * CA + u;
+      const int r = row0 + c * 8 + (lane >> 3);
+      const int src = r < row_end ? p.row_src[r] : -1;
+      a_off[u] = (src >= 0 && src < p.src_rows)
+                     ? (uint32_t)src * (uint32_t)K + (uint32_t)((piece0 ^ (c & 1)) << 4)
+                     : kOutOfRange;
+    }
+#pragma unroll
+    for (int u = 0; u < CA; ++u) asm volatile("" : "+v"(a_off[u]));
+  }
+  // 16 bytes per lane: v + uni, or zero where the step does not exist or the
+  // lane's piece (parity o) lies past K.  A sum that wraps (out of range plus
+  // out of range) reads inside the buffer into a stage that is not read.
+  auto load16 = [&](const v4i& rsrc, uint8_t* lds, uint32_t v, uint32_t uni, int kofs, int o,
+                    bool live) {
+    if constexpr (kRagged) {
+      const bool in = live && kofs < lim[o];
+      dma16(rsrc, lds, in ? v + uni : kOutOfRange);
+    } else {
+      dma16_add(rsrc, lds, v, __builtin_amdgcn_readfirstlane(live ? uni : kOutOfRange));
+    }
+  };
+  auto issue_a = [&](int kb, uint8_t* tA, bool live) {
+#pragma unroll
+    for (int u = 0; u < CA; ++u) {
+      const int c = wave * CA + u;
+      const int o = CA % 2 == 0 ? (u & 1) : (c & 1);
+      if constexpr (kGather)
+        load16(rsrc_a, tA + c * 1024, a_off[u], (uint32_t)kb * kBK, kb * kBK, o, live);
+      else
+        load16(rsrc_a, tA + c * 1024, o ? vl[1] : vl[0],
+               (uint32_t)(c * 8) * (uint32_t)K + (uint32_t)kb * kBK, kb * kBK, o, live);
+    }
+  };
+  auto issue_b = [&](int kb, uint8_t* tB, bool live) {
+#pragma unroll
+    for (int u = 0; u < CB; ++u) {
+      const int c = wave * CB + u;
+      const int o = CB % 2 == 0 ? (u & 1) : (c & 1);
+      load16(rsrc_b, tB + c * 1024, o ? vl[1] : vl[0],
+             (uint32_t)(c * 8) * (uint32_t)K + (uint32_t)kb * kBK, kb * kBK, o, live);
+    }
+  };
+
+  const int g = lane >> 4, r16 = lane & 15;
+  FragLane fa = frag_lane(wm * WM, r16, g);
+  FragLane fb = frag_lane(wn * WN, r16, g);
+  v4i acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = (v4i){0, 0, 0, 0};
+  v8i bf[NJ];
+  v8i af_next;
+  auto lo = [](const v8i& v) { return (v4i){v[0], v[1], v[2], v[3]}; };
+  auto hi = [](const v8i& v) { return (v4i){v[4], v[5], v[6], v[7]}; };
+  auto multiply = [&](int i, const v8i& af) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_i8(lo(bf[j]), lo(af), acc[i][j]);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_i8(hi(bf[j]), hi(af), acc[i][j]);
+  };
+
+  // One K step, as the packed-scale FP8 product's: the next step's loads go
+  // out first (w) and after a subtile row (a); the step's barrier comes once
+  // the wave's last LDS read of it has landed, and the next step's fragments
+  // are read under the last subtile row's multiplications.
+  constexpr int kLateRow = MI >= 3 ? 1 : 0;
+  auto step = [&](int kb, auto sa_i, auto sb_i) __attribute__((always_inline)) {
+    constexpr int SAi = decltype(sa_i)::value;
+    constexpr int SBi = decltype(sb_i)::value;
+    // formed anew each step, so that no address per stage and subtile is kept
+    asm volatile("" : "+v"(fa.lo), "+v"(fa.hi), "+v"(fb.lo), "+v"(fb.hi));
+    if (kRagged) asm volatile("" : "+v"(vl[0]), "+v"(vl[1]));
+    const uint8_t* tA = stA(SAi);
+    const uint8_t* tAn = stA((SAi + 1) % NSA);
+    const uint8_t* tBn = stB((SBi + 1) % 2);
+    issue_b(kb + 1, stB((SBi + 1) % 2), kb + 1 < Kb);
+#pragma unroll
+    for (int i = 0; i < MI - 1; ++i) {
+      if (i == kLateRow) issue_a(kb + NSA - 1, stA((SAi + NSA - 1) % NSA), kb + NSA - 1 < Kb);
+      const v8i af = af_next;
+      af_next = load_frag_at(tA, (i + 1) * 16 * kBK, fa);
+      multiply(i, af);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < MI - 1; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(acc[i][j]));
+    if constexpr (NSA == 3)
+      wait_vm<CA>();
+    else
+      wait_vm<0>();
+    lds_barrier();
+    const v8i af = af_next;
+    // (the step's w fragments are replaced one by one, after their last use)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      acc[MI - 1][j] = mfma_i8(lo(bf[j]), lo(af), acc[MI - 1][j]);
+      acc[MI - 1][j] = mfma_i8(hi(bf[j]), hi(af), acc[MI - 1][j]);
+      bf[j] = load_frag_at(tBn, j * 16 * kBK, fb);
+    }
+    af_next = load_frag_at(tAn, 0, fa);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(acc[MI - 1][j]));
+  };
+
+  issue_b(0, sB0, true);
+  issue_a(0, sA0, true);
+  if constexpr (NSA == 3) {
+    issue_a(1, sA1, Kb > 1);
+    wait_vm<CA>();
+  } else {
+    wait_vm<0>();
+  }
+  lds_barrier();
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) bf[j] = load_frag_at(sB0, j * 16 * kBK, fb);
+  af_next = load_frag_at(sA0, 0, fa);
+  // unrolled by 6 = lcm(3, 2), so every step names its stages statically
+  auto step_u = [&](int kb, auto u) __attribute__((always_inline)) {
+    constexpr int U = decltype(u)::value;
+    if (U == 0 || kb < Kb)
+      step(kb, std::integral_constant<int, U % NSA>(), std::integral_constant<int, U % 2>());
+  };
+  for (int kb = 0; kb < Kb; kb += 6) {
+    step_u(kb, std::integral_constant<int, 0>());
+    step_u(kb + 1, std::integral_constant<int, 1>());
+    step_u(kb + 2, std::integral_constant<int, 2>());
+    step_u(kb + 3, std::integral_constant<int, 3>());
+    step_u(kb + 4, std::integral_constant<int, 4>());
+    step_u(kb + 5, std::integral_constant<int, 5>());
+  }
+  // the last steps' (zero) loads land in stages that the epilogue reuses
+  wait_vm<0>();
+  lds_barrier();
+
+  // ---- epilogue: scales, then 16-bit outputs staged in the stage memory
+  // (each wave its own region, rows of WN * 2 = 128 bytes, 8-byte pieces
+  // XOR-permuted by the row) and stored as 16-byte pieces of whole rows;
+  // fp32 outputs are stored by the lanes that hold them, four channels each.
+  const int wcol = n0 + wn * WN;
+  float sw[NJ][4];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int n = wcol + j * 16 + 4 * g;
+    const float* ws = p.w_scale + (size_t)e_sel * N;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sw[j][q] = n + q < N ? ws[n + q] : 0.f;
+  }
+  float sa[MI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int r = row0 + wm * WM + i * 16 + r16;
+    int at = r < row_end ? r : -1;
+    if (kGather) {
+      at = at >= 0 ? p.row_src[at] : -1;
+      if (at >= p.src_rows) at = -1;
+    }
+    sa[i] = at >= 0 ? p.a_scale[at] : 0.f;
+  }
+  auto value = [&](int i, int j, int q) -> float {
+    return (float)acc[i][j][q] * (sa[i] * sw[j][q]);
+  };
+  if (p.c_type == MOE_TYPE_F32) {
+    float* C = static_cast<float*>(p.c);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int row = row0 + wm * WM + i * 16 + r16;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int n = wcol + j * 16 + 4 * g;
+        if (row < row_end && n < N)
+          *reinterpret_cast<float4*>(C + (size_t)row * N + n) =
+              make_float4(value(i, j, 0), value(i, j, 1), value(i, j, 2), value(i, j, 3));
+      }
+    }
+    return;
+  }
+  const bool half = p.c_type == MOE_TYPE_F16;
+  static_assert(WN * 2 == 128, "staged rows are 128 bytes");
+  constexpr auto fits = [](int parts) {
+    const int region = WM / parts * WN * 2;
+    return (SA_B / region) * NSA + (SB_B / region) * 2 >= NW;
+  };
+  constexpr int kParts = fits(1) ? 1 : fits(2) ? 2 : 4;
+  static_assert(fits(kParts) && MI % kParts == 0, "staging space");
+  constexpr int PM = WM / kParts;
+  constexpr int kRegion = PM * WN * 2;
+  constexpr int kPerA = SA_B / kRegion, kPerB = SB_B / kRegion;
+  uint8_t* region;
+  if (wave < NSA * kPerA) {
+    const int st = wave / kPerA;
+    region = stA(st) + (wave - st * kPerA) * kRegion;
+  } else {
+    const int w = wave - NSA * kPerA;
+    region = w < kPerB ? sB0 + w * kRegion : sB1 + (w - kPerB) * kRegion;
+  }
+  uint16_t* C = static_cast<uint16_t*>(p.c);
+  const int c16 = lane & 7;
+#pragma unroll
+  for (int part = 0; part < kParts; ++part) {
+#pragma unroll
+    for (int i = part * (MI / kParts); i < (part + 1) * (MI / kParts); ++i) {
+      const int r = (i - part * (MI / kParts)) * 16 + r16;
+      const int f = ((r >> 1) & 7) << 1;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const float v0 = value(i, j, 0), v1 = value(i, j, 1), v2 = value(i, j, 2),
+                    v3 = value(i, j, 3);
+        uint2 o;
+        o.x = half ? pack2_f16(v0, v1) : pack2_bf16(v0, v1);
+        o.y = half ? pack2_f16(v2, v3) : pack2_bf16(v2, v3);
+        *reinterpret_cast<uint2*>(region + r * 128 + (((j * 4 + g) ^ f) << 3)) = o;
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int rr = 0; rr < PM; rr += 8) {
+      const int r = rr + (lane >> 3);
+      const uint4 v =
+          *reinterpret_cast<const uint4*>(region + r * 128 + ((c16 ^ ((r >> 1) & 7)) << 4));
+      const int row = row0 + wm * WM + part * PM + r;
+      const int n = wcol + c16 * 8;
+      if (row < row_end && n < N)
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v),
+                                    reinterpret_cast<u32x4*>(C + (size_t)row * N + n));
+    }
+  }
+}
+
+template <int BM, int BN, int WM, int WN, int GM>
+static moe_status_t launch_i8(const I8Args& p, hipStream_t st) {
+  const long long m_tiles = p.offsets ? (long long)p.rows_total / BM + p.E
+                                      : ((long long)p.rows_total + BM - 1) / BM;
+  constexpr int threads = 64 * (BM / WM) * (BN / WN);
+  long long blocks = m_tiles * ((p.N + BN - 1) / BN);
+  blocks = (blocks + kXcds - 1) / kXcds * kXcds;
+  if (blocks * threads > 0xffffffffLL) return MOE_UNSUPPORTED_SHAPE;
+  const dim3 grid((unsigned)blocks), block(threads);
+  const bool ragged = p.K % kBK != 0;
+  if (p.row_src) {
+    if (ragged)
+      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, true, true>), grid, block, 0,
+                         st, p);
+    else
+      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, true, false>), grid, block,
+                         0, st, p);
+  } else {
+    if (ragged)
+      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, false, true>), grid, block,
+                         0, st, p);
+    else
+      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, false, false>), grid, block,
+                         0, st, p);
+  }
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
+}
+
+static bool big_tiles_i8(long long rows_total, int N, int E) {
+  return rows_total >= 256LL * E && (rows_total / 256) * (N / 256) > 128;
+}
+
+// Launches the product in tiles chosen from the sizes alone (the same inside
+// graph capture).
+static moe_status_t product_i8(const I8Args& p, hipStream_t st) {
+  if (big_tiles_i8(p.rows_total, p.N, p.E)) return launch_i8<256, 256, 128, 64, 2>(p, st);
+  return launch_i8<128, 128, 64, 64, 4>(p, st);
+}
+
+// The checks that every product shares: sizes, then pointers.
+static moe_status_t product_args(const I8Args& p, bool grouped) {
+  if (p.E <= 0 || p.E > MOE_MAX_EXPERTS || p.rows_total < 0 || p.N <= 0 || p.K <= 0)
+    return MOE_INVALID_ARG;
+  if (p.c_type != MOE_TYPE_F32 && p.c_type != MOE_TYPE_BF16 && p.c_type != MOE_TYPE_F16)
+    return MOE_INVALID_ARG;
+  // 128 * 128 * K stays below 2^31
+  if (p.N % 16 != 0 || p.K % 16 != 0 || p.K > 131056) return MOE_UNSUPPORTED_SHAPE;
+  if (grouped && (!p.offsets || !p.counts)) return MOE_INVALID_ARG;
+  if (!p.w || !p.w_scale) return MOE_INVALID_ARG;
+  if (p.row_src) {
+    if (p.src_rows < 0 || (p.src_rows > 0 && !p.a)) return MOE_INVALID_ARG;
+    if ((long long)p.src_rows * p.K > 0x7ffff000LL) return MOE_UNSUPPORTED_SHAPE;
+  } else if (p.rows_total > 0 && !p.a) {
+    return MOE_INVALID_ARG;
+  }
+  if (p.rows_total > 0 && ((!p.a_scale && !(p.row_src && p.src_rows == 0)) || !p.c))
+    return MOE_INVALID_ARG;
+  if (((uintptr_t)p.a | (uintptr_t)p.w | (uintptr_t)p.c) & 15) return MOE_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status_t moe_gemm_int8(const int8_t* a, const float* a_scale, const int8_t* w,
+                                      const float* w_scale, int M, int N, int K, void* c,
+                                      int c_type, void* stream) {
+  const I8Args p{reinterpret_cast<const uint8_t*>(a), a_scale, reinterpret_cast<const uint8_t*>(w),
+                 w_scale, nullptr, nullptr, nullptr, 1, M, N, K, 0, c, c_type, nullptr};
+  const moe_status_t ok = product_args(p, false);
+  if (ok != MOE_OK || M == 0) return ok;
+  return product_i8(p, reinterpret_cast<hipStream_t>(stream));
+}
+
+extern "C" moe_status_t moe_grouped_gemm_int8(const int8_t* a, const float* a_scale,
+                                              const int8_t* w, const float* w_scale,
+                                              const int32_t* offsets, const int32_t* counts,
+                                              int E, int rows_total, int N, int K, void* c,
+                                              int c_type, int32_t* status_dev, void* stream) {
+  const I8Args p{reinterpret_cast<const uint8_t*>(a), a_scale, reinterpret_cast<const uint8_t*>(w),
+                 w_scale, offsets, counts, nullptr, E, rows_total, N, K, 0, c, c_type,
+                 status_dev};
+  const moe_status_t ok = product_args(p, true);
+  if (ok != MOE_OK || rows_total == 0) return ok;
+  return product_i8(p, reinterpret_cast<hipStream_t>(stream));
+}
+
+extern "C" moe_status_t moe_grouped_gemm_int8_gather(
+    const int8_t* x, const float* x_scale, int T, const int32_t* row_src, const int8_t* w,
+    const float* w_scale, const int32_t* offsets, const int32_t* counts, int E, int rows_total,
+    int N, int K, void* c, int c_type, int32_t* status_dev, void* stream) {
+  if (!row_src && rows_total != 0) return MOE_INVALID_ARG;
+  const I8Args p{reinterpret_cast<const uint8_t*>(x), x_scale, reinterpret_cast<const uint8_t*>(w),
+                 w_scale, offsets, counts, row_src, E, rows_total, N, K, T, c, c_type,
+                 status_dev};
+  const moe_status_t ok = product_args(p, true);
+  if (ok != MOE_OK || rows_total == 0) return ok;
+  return product_i8(p, reinterpret_cast<hipStream_t>(stream));
+}

@@ -491,6 +491,95 @@ def moe_combine_rows_grad(dout, y, slot_of, topk_w, dy, dtopk_w, status, row_src
           _ptr(status, _I32, "status", (1,)))
 
 
+# ---- products in 8-bit integers, one scale per token and one per channel
+_I8 = (torch.int8,)
+_FLOATS = tuple(_TYPES)
+
+
+def moe_quantize_int8(x, q, scale, stream=None):
+    """Codes q (int8, x's shape) and one scale per row (float32 [rows]) of
+    x [..., cols] in float32, bfloat16 or float16: tokens [M, K], or the
+    channels of weights [N, K] or [E, N, K] (scale then [E, N])."""
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    _call("moe_quantize_int8", stream, (x, q, scale), _ptr(x, _FLOATS, "x"), _type(x, "x"), rows,
+          cols, _ptr(q, _I8, "q", x.shape), _ptr(scale, _F32, "scale", x.shape[:-1]))
+
+
+def moe_gemm_int8(a, a_scale, w, w_scale, c, stream=None):
+    """c [M, N] (float32, bfloat16 or float16) = a [M, K] int8 with w [N, K]
+    int8, scaled by a_scale [M] and w_scale [N]."""
+    M, K = _matrix(a, "a")
+    N = _matrix(w, "w")[0]
+    _call("moe_gemm_int8", stream, (a, a_scale, w, w_scale, c), _ptr(a, _I8, "a"),
+          _ptr(a_scale, _F32, "a_scale", (M,)), _ptr(w, _I8, "w", (N, K)),
+          _ptr(w_scale, _F32, "w_scale", (N,)), M, N, K, _ptr(c, _FLOATS, "c", (M, N)),
+          _type(c, "c"))
+
+
+def moe_linear_int8_workspace_bytes(M, K):
+    return int(load().moe_linear_int8_workspace_bytes(int(M), int(K)))
+
+
+def moe_linear_int8(x, w, w_scale, c, workspace, stream=None):
+    """c [M, N] = x [M, K] (float32, bfloat16 or float16, quantised per row in
+    the call) with w [N, K] int8 and w_scale [N]; workspace (uint8) holds
+    moe_linear_int8_workspace_bytes(M, K) bytes."""
+    M, K = _matrix(x, "x")
+    N = _matrix(w, "w")[0]
+    _call("moe_linear_int8", stream, (x, w, w_scale, c, workspace), _ptr(x, _FLOATS, "x"),
+          _type(x, "x"), _ptr(w, _I8, "w", (N, K)), _ptr(w_scale, _F32, "w_scale", (N,)), M, N, K,
+          _ptr(c, _FLOATS, "c", (M, N)), _type(c, "c"),
+          _ptr(workspace, (torch.uint8,), "workspace"), workspace.numel())
+
+
+def _experts(w):
+    if w.dim() != 3:
+        raise ValueError(f"w: must have three dimensions, has {w.dim()}")
+    return w.shape
+
+
+def moe_grouped_gemm_int8(a, a_scale, w, w_scale, offsets, counts, c, status, stream=None):
+    """c[valid rows] = a [rows_total, K] int8 with w[expert] [N, K] int8, scaled
+    by a_scale [rows_total] and w_scale [E, N]; c float32, bfloat16 or float16."""
+    E, N, K = _experts(w)
+    R = _matrix(a, "a")[0]
+    _call("moe_grouped_gemm_int8", stream, (a, a_scale, w, w_scale, offsets, counts, c, status),
+          _ptr(a, _I8, "a", (R, K)), _ptr(a_scale, _F32, "a_scale", (R,)), _ptr(w, _I8, "w"),
+          _ptr(w_scale, _F32, "w_scale", (E, N)), _ptr(offsets, _I32, "offsets", (E + 1,)),
+          _ptr(counts, _I32, "counts", (E,)), E, R, N, K, _ptr(c, _FLOATS, "c", (R, N)),
+          _type(c, "c"), _ptr(status, _I32, "status", (1,)))
+
+
+def moe_grouped_gemm_int8_gather(x, x_scale, row_src, w, w_scale, offsets, counts, c, status,
+                                 stream=None):
+    """moe_grouped_gemm_int8 reading buffer row r from x[row_src[r]] (x [T, K]
+    int8, x_scale [T])."""
+    E, N, K = _experts(w)
+    T = _matrix(x, "x")[0]
+    R = row_src.numel()
+    _call("moe_grouped_gemm_int8_gather", stream,
+          (x, x_scale, row_src, w, w_scale, offsets, counts, c, status),
+          _ptr(x, _I8, "x", (T, K)), _ptr(x_scale, _F32, "x_scale", (T,)), T,
+          _ptr(row_src, _I32, "row_src", (R,)), _ptr(w, _I8, "w"),
+          _ptr(w_scale, _F32, "w_scale", (E, N)), _ptr(offsets, _I32, "offsets", (E + 1,)),
+          _ptr(counts, _I32, "counts", (E,)), E, R, N, K, _ptr(c, _FLOATS, "c", (R, N)),
+          _type(c, "c"), _ptr(status, _I32, "status", (1,)))
+
+
+def moe_act_requant_int8(h, offsets, counts, q, q_scale, status, stream=None):
+    """q [rows_total, I] int8, q_scale [rows_total] = silu(h[:, :I]) * h[:, I:]
+    quantised per valid row; h [rows_total, 2I] float32, bfloat16 or float16."""
+    R, I2 = _matrix(h, "h")
+    I = I2 // 2
+    E = counts.numel()
+    _call("moe_act_requant_int8", stream, (h, offsets, counts, q, q_scale, status),
+          _ptr(h, _FLOATS, "h", (R, 2 * I)), _type(h, "h"),
+          _ptr(offsets, _I32, "offsets", (E + 1,)), _ptr(counts, _I32, "counts", (E,)), E, R, I,
+          _ptr(q, _I8, "q", (R, I)), _ptr(q_scale, _F32, "q_scale", (R,)),
+          _ptr(status, _I32, "status", (1,)))
+
+
 def moe_ceiling_copy(src, dst, stream=None):
     """Copy src to dst (same byte size) with the library's plain copy kernel
     (a measurement helper: HBM ceiling)."""

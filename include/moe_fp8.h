@@ -487,6 +487,72 @@ moe_status_t moe_combine_rows_grad(const void* dout, const void* y, int dtype, i
                                    int32_t* status_dev, void* stream);
 
 /*
+ * Products in 8-bit integers with one scale per token and one per output
+ * channel: the layer's expert products and the linears outside it for
+ * weights kept in int8 (the counterparts of moe_quantize_fp8, moe_gemm_fp8,
+ * moe_grouped_gemm_fp8[_gather] and moe_act_requant).
+ *
+ *   moe_quantize_int8   per row m of x [rows, cols] (a token; or, on
+ *                       weights [E*N, K], an output channel):
+ *                         s = fp32(max_j |x[m, j]| / 127); 1 for a row of
+ *                             zeros; at least 2^-126
+ *                         q[m, j] = the integer nearest x[m, j] / s, ties to
+ *                             even (decided exactly, in [-127, 127])
+ *                       A row with an infinity or a NaN gets the scale NaN
+ *                       and zero codes: what is computed from it is NaN.
+ *   moe_gemm_int8       c[m, n] = round((a_scale[m] * w_scale[n]) *
+ *                                       sum_k a[m, k] * w[n, k])
+ *   moe_grouped_gemm_int8  the same with expert e's weights for the valid
+ *                       rows of segment e; other rows are not written
+ *   moe_grouped_gemm_int8_gather  with row r of the buffer read from
+ *                       x[row_src[r]] and its scale from
+ *                       x_scale[row_src[r]]; a valid row with row_src < 0 or
+ *                       >= T gives 0
+ *   moe_act_requant_int8  v[m, j] = silu(h[m, j]) * h[m, I + j] in fp32 (exp
+ *                       and reciprocal from the hardware, ~1 ulp each),
+ *                       quantised per valid row as moe_quantize_int8
+ *   moe_linear_int8     moe_quantize_int8 of x, then moe_gemm_int8
+ *
+ * The sum is exact (32-bit integers; codes may be any of [-128, 127]); the
+ * scales multiply it in fp32 and the result is rounded once to c's type, to
+ * nearest even.
+ *
+ *   a, q [rows, K] int8, a_scale, q_scale [rows] f32
+ *   w    [E, N, K] int8 (dense: [N, K]), w_scale [E, N] f32
+ *   c    [rows, N] of c_type;  x, h of `dtype`
+ *   dtype, c_type  MOE_TYPE_F32, _BF16 or _F16
+ *   workspace  moe_linear_int8_workspace_bytes(M, K) bytes; what the call
+ *              leaves there is unspecified
+ * N, K, I and cols must be multiples of 16, K at most 131056 (so that no sum
+ * overflows), T * K of the gathered call below 0x7ffff000 (one buffer
+ * descriptor): MOE_UNSUPPORTED_SHAPE otherwise.  M, T and rows are arbitrary.
+ * Matrices 16-byte aligned.  offsets / counts / status_dev as for
+ * moe_grouped_gemm_fp8.  Outputs may not overlap inputs.
+ */
+moe_status_t moe_quantize_int8(const void* x, int dtype, int rows, int cols, int8_t* q,
+                               float* scale, void* stream);
+moe_status_t moe_gemm_int8(const int8_t* a, const float* a_scale, const int8_t* w,
+                           const float* w_scale, int M, int N, int K, void* c, int c_type,
+                           void* stream);
+moe_status_t moe_grouped_gemm_int8(const int8_t* a, const float* a_scale, const int8_t* w,
+                                   const float* w_scale, const int32_t* offsets,
+                                   const int32_t* counts, int E, int rows_total, int N, int K,
+                                   void* c, int c_type, int32_t* status_dev, void* stream);
+moe_status_t moe_grouped_gemm_int8_gather(const int8_t* x, const float* x_scale, int T,
+                                          const int32_t* row_src, const int8_t* w,
+                                          const float* w_scale, const int32_t* offsets,
+                                          const int32_t* counts, int E, int rows_total, int N,
+                                          int K, void* c, int c_type, int32_t* status_dev,
+                                          void* stream);
+moe_status_t moe_act_requant_int8(const void* h, int dtype, const int32_t* offsets,
+                                  const int32_t* counts, int E, int rows_total, int I, int8_t* q,
+                                  float* q_scale, int32_t* status_dev, void* stream);
+size_t moe_linear_int8_workspace_bytes(int M, int K);
+moe_status_t moe_linear_int8(const void* x, int dtype, const int8_t* w, const float* w_scale,
+                             int M, int N, int K, void* c, int c_type, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
  * Measurement helpers (not steps of the layer).  They time the two
  * resources the layer's kernels are bound by, so that a kernel can be
  * reported against what the GPU sustains as well as against its published
