@@ -22,37 +22,12 @@
 // lie past the weight descriptor's range in the same way.
 #include <type_traits>
 
-#include "gemm_tiles.hpp"
+#include "product_i8.hpp"
+#include "skinny_i8.hpp"
 
 namespace moe {
 
 constexpr uint32_t kOutOfRange = 0x80000000u;
-
-__device__ __forceinline__ v4i mfma_i8(const v4i& a, const v4i& b, const v4i& c) {
-  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
-}
-
-__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
-  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, (h2){(_Float16)lo, (_Float16)hi});
-}
-
-// The arguments of a product.  offsets == nullptr: dense (one weight matrix,
-// every row of it).  row_src != nullptr: buffer row r is row row_src[r] of a
-// [src_rows, K], its scale a_scale[row_src[r]].
-struct I8Args {
-  const uint8_t* a;
-  const float* a_scale;
-  const uint8_t* w;
-  const float* w_scale;
-  const int32_t* offsets;
-  const int32_t* counts;
-  const int32_t* row_src;
-  int E, rows_total, N, K, src_rows;
-  void* c;
-  int c_type;
-  int32_t* status;
-};
 
 template <int BM, int BN, int WM, int WN, int GM, bool kGather, bool kRagged>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_kernel(I8Args p) {
@@ -396,9 +371,52 @@ static bool big_tiles_i8(long long rows_total, int N, int E) {
   return rows_total >= 256LL * E && (rows_total / 256) * (N / 256) > 128;
 }
 
+template <int MT, int NT>
+static moe_status_t launch_skinny(const I8Args& p, hipStream_t st) {
+  const long long m_tiles = p.offsets ? (long long)p.rows_total / (16 * MT) + p.E
+                                      : ((long long)p.rows_total + 16 * MT - 1) / (16 * MT);
+  const long long blocks = m_tiles * ((p.N + 16 * NT - 1) / (16 * NT));
+  if (blocks * 64 * kSkinnyWaves > 0xffffffffLL) return MOE_UNSUPPORTED_SHAPE;
+  const dim3 grid((unsigned)blocks), block(64 * kSkinnyWaves);
+  if (p.row_src)
+    hipLaunchKernelGGL((skinny_i8_kernel<MT, NT, true>), grid, block, 0, st, p);
+  else
+    hipLaunchKernelGGL((skinny_i8_kernel<MT, NT, false>), grid, block, 0, st, p);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
+}
+
+// Few rows: the kernel that reads the weights once, straight to registers.
+// `rows` is a dense product's, or a segment's on average; `channels` all
+// experts'.  Its tile is as large as leaves 192 workgroups (a CU takes in some
+// 20 bytes a cycle whatever it runs, so the CUs have to share the bytes).
+static moe_status_t few_rows_i8(const I8Args& p, long long rows, long long channels,
+                                hipStream_t st) {
+  const bool many = channels >= 192 * 32;
+  if (rows <= 16) return launch_skinny<1, 1>(p, st);
+  if (rows <= 32) return many ? launch_skinny<2, 2>(p, st) : launch_skinny<2, 1>(p, st);
+  if (rows <= 64) return many ? launch_skinny<4, 2>(p, st) : launch_skinny<2, 2>(p, st);
+  return many ? launch_skinny<8, 2>(p, st) : launch_skinny<4, 2>(p, st);
+}
+
 // Launches the product in tiles chosen from the sizes alone (the same inside
 // graph capture).
 static moe_status_t product_i8(const I8Args& p, hipStream_t st) {
+  const long long rows = ((long long)p.rows_total + p.E - 1) / p.E;
+  const long long channels = (long long)p.E * p.N;
+#ifdef MOE_I8_FORCE
+  switch (MOE_I8_FORCE) {
+    case 64: return launch_i8<64, 128, 32, 64, 4>(p, st);
+    case 128: return launch_i8<128, 128, 64, 64, 4>(p, st);
+    case 256: return launch_i8<256, 256, 128, 64, 2>(p, st);
+    case 320: return launch_i8<320, 256, 160, 64, 2>(p, st);
+    case 192: return launch_i8<192, 256, 96, 64, 2>(p, st);
+    case 1282: return launch_i8<128, 256, 64, 64, 2>(p, st);
+    case 2561: return launch_i8<256, 128, 64, 64, 2>(p, st);
+    case 642: return launch_i8<64, 256, 32, 64, 4>(p, st);
+  }
+#endif
+  if (rows <= 16 || (rows <= 128 && channels < 128 * 192) || (rows <= 32 && p.E == 1))
+    return few_rows_i8(p, rows, channels, st);
   if (big_tiles_i8(p.rows_total, p.N, p.E)) return launch_i8<256, 256, 128, 64, 2>(p, st);
   return launch_i8<128, 128, 64, 64, 4>(p, st);
 }
@@ -463,4 +481,61 @@ extern "C" moe_status_t moe_grouped_gemm_int8_gather(
   const moe_status_t ok = product_args(p, true);
   if (ok != MOE_OK || rows_total == 0) return ok;
   return product_i8(p, reinterpret_cast<hipStream_t>(stream));
+}
+
+// ---- a whole linear: quantise the rows, then the product.  The workspace
+// holds the codes [M, K] and, from the next multiple of 16 bytes, the scales.
+extern "C" size_t moe_linear_int8_workspace_bytes(int M, int K) {
+  if (M < 0 || K <= 0) return 0;
+  const size_t codes = ((size_t)M * (size_t)K + 15) / 16 * 16;
+  return codes + (size_t)M * sizeof(float);
+}
+
+// One launch for at most this many rows.
+static bool one_launch(int M, int K) {
+  return M <= kLinearRows && (long long)M * (K + 16) <= 61440;   // of 64 KB
+}
+
+static moe_status_t linear_in_one(const void* x, int dtype, const int8_t* w, const float* w_scale,
+                                  int M, int N, int K, void* c, int c_type, hipStream_t st) {
+  const dim3 grid((unsigned)((N + 15) / 16)), block(64 * kSkinnyWaves);
+  const size_t lds = (size_t)M * (K + 16);
+  const uint8_t* wb = reinterpret_cast<const uint8_t*>(w);
+  if (dtype == MOE_TYPE_F32)
+    hipLaunchKernelGGL((linear_i8_kernel<MOE_TYPE_F32>), grid, block, lds, st, x, wb, w_scale, M,
+                       N, K, c, c_type);
+  else if (dtype == MOE_TYPE_BF16)
+    hipLaunchKernelGGL((linear_i8_kernel<MOE_TYPE_BF16>), grid, block, lds, st, x, wb, w_scale, M,
+                       N, K, c, c_type);
+  else
+    hipLaunchKernelGGL((linear_i8_kernel<MOE_TYPE_F16>), grid, block, lds, st, x, wb, w_scale, M,
+                       N, K, c, c_type);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
+}
+
+static bool float_type(int dtype) {
+  return dtype == MOE_TYPE_F32 || dtype == MOE_TYPE_BF16 || dtype == MOE_TYPE_F16;
+}
+
+extern "C" moe_status_t moe_linear_int8(const void* x, int dtype, const int8_t* w,
+                                        const float* w_scale, int M, int N, int K, void* c,
+                                        int c_type, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+  if (!float_type(dtype) || !float_type(c_type) || M < 0 || N <= 0 || K <= 0)
+    return MOE_INVALID_ARG;
+  if (N % 16 != 0 || K % 16 != 0 || K > 131056) return MOE_UNSUPPORTED_SHAPE;
+  if (!w || !w_scale) return MOE_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!x || !c || !workspace || workspace_bytes < moe_linear_int8_workspace_bytes(M, K))
+    return MOE_INVALID_ARG;
+  if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)c | (uintptr_t)workspace) & 15)
+    return MOE_UNSUPPORTED_SHAPE;
+  if (one_launch(M, K))
+    return linear_in_one(x, dtype, w, w_scale, M, N, K, c, c_type,
+                         reinterpret_cast<hipStream_t>(stream));
+  int8_t* q = static_cast<int8_t*>(workspace);
+  float* s = reinterpret_cast<float*>(q + ((size_t)M * (size_t)K + 15) / 16 * 16);
+  const moe_status_t ok = moe_quantize_int8(x, dtype, M, K, q, s, stream);
+  if (ok != MOE_OK) return ok;
+  return moe_gemm_int8(q, s, w, w_scale, M, N, K, c, c_type, stream);
 }

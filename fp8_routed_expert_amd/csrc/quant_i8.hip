@@ -10,69 +10,12 @@
 // codes; a longer row's others are read (and the activation computed) again,
 // from the cache.  Reads 2 (or 4) bytes and writes one per value: bound by
 // HBM bandwidth.
-//
-// The codes are decided exactly: rint(v * (1 / s)) is the right integer or
-// off by one where v / s is near a border, and the residual d = v - q s is
-// exact in one fma (q has 8 bits and |d| is at most about s, a multiple of
-// the smaller of the two's last places), so comparing 2d with s moves q to
-// the nearest integer and finds the ties.
-//
-// A row with an infinity or a NaN gets the scale NaN and zero codes, so
-// that whatever is computed from it is NaN.
-#include "device_common.hpp"
+#include "rows_i8.hpp"
 
 namespace moe {
 
 constexpr int kQThreads = 256;
 constexpr int kKeep = 4;
-
-__device__ __forceinline__ void load8_as(int dtype, const void* x, size_t at, float (&v)[8]) {
-  if (dtype == MOE_TYPE_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    return;
-  }
-  const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
-  if (dtype == MOE_TYPE_F16) {
-    typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-    const h8 h = __builtin_bit_cast(h8, a);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
-  } else {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_to_f32(w[i] & 0xffffu);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-}
-
-// A row's scale from the bits of its largest magnitude (a NaN's are above an
-// infinity's).
-__device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
-  if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-  if (amax_bits == 0) return 1.f;
-  return fmaxf(__uint_as_float(amax_bits) / 127.f, 0x1p-126f);
-}
-
-__device__ __forceinline__ uint32_t int8_code(float v, float s, float inv) {
-  float q = rintf(v * inv);
-  const float d = fmaf(-q, s, v);
-  const float d2 = d + d, up = q + 1.f, down = q - 1.f;
-  const bool odd = ((int)q & 1) != 0;
-  q = (d2 > s || (d2 == s && odd)) ? up : (d2 < -s || (d2 == -s && odd)) ? down : q;
-  return (uint32_t)(int)q & 0xffu;
-}
-
-__device__ __forceinline__ uint2 int8_codes(const float (&v)[8], float s, float inv) {
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i >> 2] |= int8_code(v[i], s, inv) << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
-}
 
 // kAct: v = silu(h[j]) * h[cols + j] of a row [2 cols]; else the row itself.
 template <int kType, bool kAct>
@@ -107,17 +50,15 @@ __global__ __launch_bounds__(kQThreads) void quant_int8_kernel(
       const int j = (u * kQThreads + (int)threadIdx.x) * 8;
       if (j < cols) {
         row_slice<kType, kAct>(x, row, cols, j, v[u]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[u][i]) & 0x7fffffffu);
+        top = max_bits(v[u], top);
       }
     }
     for (int j = (kKeep * kQThreads + (int)threadIdx.x) * 8; j < cols; j += kQThreads * 8) {
       float t[8];
       row_slice<kType, kAct>(x, row, cols, j, t);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(t[i]) & 0x7fffffffu);
+      top = max_bits(t, top);
     }
-    for (int o = 32; o >= 1; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    top = wave_max(top);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
     __syncthreads();
 #pragma unroll
@@ -193,33 +134,4 @@ extern "C" moe_status_t moe_act_requant_int8(const void* h, int dtype, const int
   if (((uintptr_t)h | (uintptr_t)q) & 15) return MOE_UNSUPPORTED_SHAPE;
   return quantize_int8<true>(h, dtype, rows_total, I, q, q_scale, offsets, counts, E, status_dev,
                              stream);
-}
-
-// ---- a whole linear: quantise the rows, then the product.  The workspace
-// holds the codes [M, K] and, from the next multiple of 16 bytes, the scales.
-extern "C" size_t moe_linear_int8_workspace_bytes(int M, int K) {
-  if (M < 0 || K <= 0) return 0;
-  const size_t codes = ((size_t)M * (size_t)K + 15) / 16 * 16;
-  return codes + (size_t)M * sizeof(float);
-}
-
-extern "C" moe_status_t moe_linear_int8(const void* x, int dtype, const int8_t* w,
-                                        const float* w_scale, int M, int N, int K, void* c,
-                                        int c_type, void* workspace, size_t workspace_bytes,
-                                        void* stream) {
-  if (!float_type(dtype) || !float_type(c_type) || M < 0 || N <= 0 || K <= 0)
-    return MOE_INVALID_ARG;
-  if (N % 16 != 0 || K % 16 != 0 || K > 131056) return MOE_UNSUPPORTED_SHAPE;
-  if (!w || !w_scale) return MOE_INVALID_ARG;
-  if (M == 0) return MOE_OK;
-  if (!x || !c || !workspace || workspace_bytes < moe_linear_int8_workspace_bytes(M, K))
-    return MOE_INVALID_ARG;
-  if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)c | (uintptr_t)workspace) & 15)
-    return MOE_UNSUPPORTED_SHAPE;
-  int8_t* q = static_cast<int8_t*>(workspace);
-  float* s = reinterpret_cast<float*>(q + ((size_t)M * (size_t)K + 15) / 16 * 16);
-  const moe_status_t ok = quantize_int8<false>(x, dtype, M, K, q, s, nullptr, nullptr, 0, nullptr,
-                                               stream);
-  if (ok != MOE_OK) return ok;
-  return moe_gemm_int8(q, s, w, w_scale, M, N, K, c, c_type, stream);
 }

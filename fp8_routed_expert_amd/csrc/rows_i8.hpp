@@ -1,0 +1,102 @@
+// Rows in 8-bit integers: a row's scale and its values' codes, as the
+// quantiser, the gated activation and the one-launch linear compute them.
+//
+//   s = fp32(max_j |v_j| / 127), 1 for a row of zeros, at least 2^-126
+//   q_j = the integer nearest v_j / s, ties to even
+//
+// The codes are decided exactly: rint(v * (1 / s)) is the right integer or
+// off by one where v / s is near a border, and the residual d = v - q s is
+// exact in one fma (q has 8 bits and |d| is at most about s, a multiple of
+// the smaller of the two's last places), so comparing 2d with s moves q to
+// the nearest integer and finds the ties.
+//
+// A row with an infinity or a NaN gets the scale NaN and zero codes, so
+// that whatever is computed from it is NaN.
+#pragma once
+
+#include "device_common.hpp"
+
+namespace moe {
+
+// Eight consecutive values of type `dtype` from element `at`.
+__device__ __forceinline__ void load8_as(int dtype, const void* x, size_t at, float (&v)[8]) {
+  if (dtype == MOE_TYPE_F32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+    const float4 a = p[0], b = p[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    return;
+  }
+  const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
+  if (dtype == MOE_TYPE_F16) {
+    typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+    const h8 h = __builtin_bit_cast(h8, a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
+  } else {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_to_f32(w[i] & 0xffffu);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+// A row's scale from the bits of its largest magnitude (a NaN's are above an
+// infinity's).
+__device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+  if (amax_bits == 0) return 1.f;
+  return fmaxf(__uint_as_float(amax_bits) / 127.f, 0x1p-126f);
+}
+
+// Eight codes.  v * inv + 1.5 * 2^23 rounds to an integer whose two's
+// complement is in the low bits; only where a residual reaches half a step
+// (rare) is an integer moved.
+__device__ __forceinline__ uint2 int8_codes(const float (&v)[8], float s, float inv) {
+  constexpr float kShift = 12582912.f;
+  float t[8], far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    t[i] = fmaf(v[i], inv, kShift);
+    far = fmaxf(far, fabsf(fmaf(kShift - t[i], s, v[i])));
+  }
+  if (far + far >= s) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = t[i] - kShift;
+      const float d = fmaf(-q, s, v[i]), d2 = d + d;
+      const bool odd = (__float_as_uint(t[i]) & 1u) != 0;
+      if (d2 > s || (d2 == s && odd))
+        t[i] = q + 1.f + kShift;
+      else if (d2 < -s || (d2 == -s && odd))
+        t[i] = q - 1.f + kShift;
+    }
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {   // the low bytes of four
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(t[4 * h + 1]),
+                                              __float_as_uint(t[4 * h]), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(t[4 * h + 3]),
+                                              __float_as_uint(t[4 * h + 2]), 0x04000c0cu);
+    w[h] = lo | hi;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// The largest magnitude among eight values and `top`, as bits.
+__device__ __forceinline__ uint32_t max_bits(const float (&v)[8], uint32_t top) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  return top;
+}
+
+// The largest of a wave's values, in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t top) {
+  for (int o = 32; o >= 1; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  return top;
+}
+
+}  // namespace moe

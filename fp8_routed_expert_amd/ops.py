@@ -387,23 +387,42 @@ def _type(t, name, bytes_too=False):
     return code
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_functions = {}
+
+
+def _arg(t, dtypes, name, shape=None):
+    """_ptr with its checks in the order of their cost: a call on a few rows
+    takes as long as its checks."""
+    if t.is_cuda and t.dtype in dtypes and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
+    return _ptr(t, dtypes, name, shape)   # names what is wrong
+
+
 def _call(name, stream, tensors, *args):
     """Calls library function `name` on the device that the tensors share
     (which need not be the current one), on `stream` or that device's
     current stream."""
-    dev = tensors[0].device
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t.device != dev:
-            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-        raise ValueError(f"{name}: tensors on {dev}, stream on {stream.device}")
-    fn = getattr(load(), name)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, _stream(stream))
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
+    if stream is None:
+        stream = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
+            raise ValueError(f"{name}: tensors on device {dev}, stream on {stream.device}")
+        stream = stream.cuda_stream
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load(), name)
+    if dev == torch.cuda.current_device():
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream))
-    check(st, name)
+            st = fn(*args, stream)
+    if st:
+        check(st, name)
 
 
 def _matrix(t, name):
@@ -422,12 +441,12 @@ def moe_sort_tokens(topk_idx, E, layout, align_m, rows, counts, offsets, slot_of
     rows_total = E * rows if layout == LAYOUT_MASKED else rows
     _call("moe_sort_tokens", stream,
           (topk_idx, counts, offsets, slot_of, row_src, row_expert, workspace, status),
-          _ptr(topk_idx, _I32, "topk_idx"), T, K, E, layout, align_m, rows,
-          _ptr(counts, _I32, "counts", (E,)), _ptr(offsets, _I32, "offsets", (E + 1,)),
-          _ptr(slot_of, _I32, "slot_of", (T, K)), _ptr(row_src, _I32, "row_src", (rows_total,)),
-          _ptr(row_expert, _I32, "row_expert", (rows_total,)),
-          _ptr(workspace, (torch.uint8,), "workspace"), workspace.numel(),
-          _ptr(status, _I32, "status", (1,)))
+          _arg(topk_idx, _I32, "topk_idx"), T, K, E, layout, align_m, rows,
+          _arg(counts, _I32, "counts", (E,)), _arg(offsets, _I32, "offsets", (E + 1,)),
+          _arg(slot_of, _I32, "slot_of", (T, K)), _arg(row_src, _I32, "row_src", (rows_total,)),
+          _arg(row_expert, _I32, "row_expert", (rows_total,)),
+          _arg(workspace, (torch.uint8,), "workspace"), workspace.numel(),
+          _arg(status, _I32, "status", (1,)))
 
 
 def moe_permute_rows(x, slot_of, a, status, row_src=None, stream=None):
@@ -440,10 +459,10 @@ def moe_permute_rows(x, slot_of, a, status, row_src=None, stream=None):
     R = _matrix(a, "a")[0]
     code = _type(x, "x", True)
     ts = (x, slot_of, a, status) + (() if row_src is None else (row_src,))
-    _call("moe_permute_rows", stream, ts, _ptr(x, (x.dtype,), "x"), code, T, K, H,
-          _ptr(slot_of, _I32, "slot_of", (T, K)), R, _ptr(a, (x.dtype,), "a", (R, H)),
-          None if row_src is None else _ptr(row_src, _I32, "row_src", (R,)),
-          _ptr(status, _I32, "status", (1,)))
+    _call("moe_permute_rows", stream, ts, _arg(x, (x.dtype,), "x"), code, T, K, H,
+          _arg(slot_of, _I32, "slot_of", (T, K)), R, _arg(a, (x.dtype,), "a", (R, H)),
+          None if row_src is None else _arg(row_src, _I32, "row_src", (R,)),
+          _arg(status, _I32, "status", (1,)))
 
 
 def moe_permute_rows_grad(da, slot_of, dx, status, stream=None):
@@ -453,8 +472,8 @@ def moe_permute_rows_grad(da, slot_of, dx, status, stream=None):
     T, K = _matrix(slot_of, "slot_of")
     code = _type(da, "da")
     _call("moe_permute_rows_grad", stream, (da, slot_of, dx, status),
-          _ptr(da, (da.dtype,), "da"), code, R, _ptr(slot_of, _I32, "slot_of"), T, K, H,
-          _ptr(dx, (da.dtype,), "dx", (T, H)), _ptr(status, _I32, "status", (1,)))
+          _arg(da, (da.dtype,), "da"), code, R, _arg(slot_of, _I32, "slot_of"), T, K, H,
+          _arg(dx, (da.dtype,), "dx", (T, H)), _arg(status, _I32, "status", (1,)))
 
 
 def moe_combine_rows(y, slot_of, topk_w, out, status, stream=None):
@@ -464,9 +483,9 @@ def moe_combine_rows(y, slot_of, topk_w, out, status, stream=None):
     T, K = _matrix(slot_of, "slot_of")
     code = _type(y, "y")
     _call("moe_combine_rows", stream, (y, slot_of, topk_w, out, status),
-          _ptr(y, (y.dtype,), "y"), code, R, _ptr(slot_of, _I32, "slot_of"),
-          _ptr(topk_w, _F32, "topk_w", (T, K)), T, K, H, _ptr(out, (y.dtype,), "out", (T, H)),
-          _ptr(status, _I32, "status", (1,)))
+          _arg(y, (y.dtype,), "y"), code, R, _arg(slot_of, _I32, "slot_of"),
+          _arg(topk_w, _F32, "topk_w", (T, K)), T, K, H, _arg(out, (y.dtype,), "out", (T, H)),
+          _arg(status, _I32, "status", (1,)))
 
 
 def moe_combine_rows_grad(dout, y, slot_of, topk_w, dy, dtopk_w, status, row_src=None,
@@ -483,12 +502,12 @@ def moe_combine_rows_grad(dout, y, slot_of, topk_w, dy, dtopk_w, status, row_src
         raise ValueError("moe_combine_rows_grad: neither dy nor dtopk_w is given")
     given = [t for t in (dy, dtopk_w, row_src) if t is not None]
     _call("moe_combine_rows_grad", stream, (dout, y, slot_of, topk_w, status, *given),
-          _ptr(dout, (dout.dtype,), "dout"), _ptr(y, (dout.dtype,), "y", (R, H)), code, R,
-          _ptr(slot_of, _I32, "slot_of", (T, K)), _ptr(topk_w, _F32, "topk_w", (T, K)), T, K, H,
-          None if dy is None else _ptr(dy, (dout.dtype,), "dy", (R, H)),
-          None if dtopk_w is None else _ptr(dtopk_w, _F32, "dtopk_w", (T, K)),
-          None if row_src is None else _ptr(row_src, _I32, "row_src", (R,)),
-          _ptr(status, _I32, "status", (1,)))
+          _arg(dout, (dout.dtype,), "dout"), _arg(y, (dout.dtype,), "y", (R, H)), code, R,
+          _arg(slot_of, _I32, "slot_of", (T, K)), _arg(topk_w, _F32, "topk_w", (T, K)), T, K, H,
+          None if dy is None else _arg(dy, (dout.dtype,), "dy", (R, H)),
+          None if dtopk_w is None else _arg(dtopk_w, _F32, "dtopk_w", (T, K)),
+          None if row_src is None else _arg(row_src, _I32, "row_src", (R,)),
+          _arg(status, _I32, "status", (1,)))
 
 
 # ---- products in 8-bit integers, one scale per token and one per channel
@@ -502,8 +521,8 @@ def moe_quantize_int8(x, q, scale, stream=None):
     channels of weights [N, K] or [E, N, K] (scale then [E, N])."""
     cols = x.shape[-1]
     rows = x.numel() // cols if cols else 0
-    _call("moe_quantize_int8", stream, (x, q, scale), _ptr(x, _FLOATS, "x"), _type(x, "x"), rows,
-          cols, _ptr(q, _I8, "q", x.shape), _ptr(scale, _F32, "scale", x.shape[:-1]))
+    _call("moe_quantize_int8", stream, (x, q, scale), _arg(x, _FLOATS, "x"), _type(x, "x"), rows,
+          cols, _arg(q, _I8, "q", x.shape), _arg(scale, _F32, "scale", x.shape[:-1]))
 
 
 def moe_gemm_int8(a, a_scale, w, w_scale, c, stream=None):
@@ -511,9 +530,9 @@ def moe_gemm_int8(a, a_scale, w, w_scale, c, stream=None):
     int8, scaled by a_scale [M] and w_scale [N]."""
     M, K = _matrix(a, "a")
     N = _matrix(w, "w")[0]
-    _call("moe_gemm_int8", stream, (a, a_scale, w, w_scale, c), _ptr(a, _I8, "a"),
-          _ptr(a_scale, _F32, "a_scale", (M,)), _ptr(w, _I8, "w", (N, K)),
-          _ptr(w_scale, _F32, "w_scale", (N,)), M, N, K, _ptr(c, _FLOATS, "c", (M, N)),
+    _call("moe_gemm_int8", stream, (a, a_scale, w, w_scale, c), _arg(a, _I8, "a"),
+          _arg(a_scale, _F32, "a_scale", (M,)), _arg(w, _I8, "w", (N, K)),
+          _arg(w_scale, _F32, "w_scale", (N,)), M, N, K, _arg(c, _FLOATS, "c", (M, N)),
           _type(c, "c"))
 
 
@@ -527,10 +546,10 @@ def moe_linear_int8(x, w, w_scale, c, workspace, stream=None):
     moe_linear_int8_workspace_bytes(M, K) bytes."""
     M, K = _matrix(x, "x")
     N = _matrix(w, "w")[0]
-    _call("moe_linear_int8", stream, (x, w, w_scale, c, workspace), _ptr(x, _FLOATS, "x"),
-          _type(x, "x"), _ptr(w, _I8, "w", (N, K)), _ptr(w_scale, _F32, "w_scale", (N,)), M, N, K,
-          _ptr(c, _FLOATS, "c", (M, N)), _type(c, "c"),
-          _ptr(workspace, (torch.uint8,), "workspace"), workspace.numel())
+    _call("moe_linear_int8", stream, (x, w, w_scale, c, workspace), _arg(x, _FLOATS, "x"),
+          _type(x, "x"), _arg(w, _I8, "w", (N, K)), _arg(w_scale, _F32, "w_scale", (N,)), M, N, K,
+          _arg(c, _FLOATS, "c", (M, N)), _type(c, "c"),
+          _arg(workspace, (torch.uint8,), "workspace"), workspace.numel())
 
 
 def _experts(w):
@@ -545,10 +564,10 @@ def moe_grouped_gemm_int8(a, a_scale, w, w_scale, offsets, counts, c, status, st
     E, N, K = _experts(w)
     R = _matrix(a, "a")[0]
     _call("moe_grouped_gemm_int8", stream, (a, a_scale, w, w_scale, offsets, counts, c, status),
-          _ptr(a, _I8, "a", (R, K)), _ptr(a_scale, _F32, "a_scale", (R,)), _ptr(w, _I8, "w"),
-          _ptr(w_scale, _F32, "w_scale", (E, N)), _ptr(offsets, _I32, "offsets", (E + 1,)),
-          _ptr(counts, _I32, "counts", (E,)), E, R, N, K, _ptr(c, _FLOATS, "c", (R, N)),
-          _type(c, "c"), _ptr(status, _I32, "status", (1,)))
+          _arg(a, _I8, "a", (R, K)), _arg(a_scale, _F32, "a_scale", (R,)), _arg(w, _I8, "w"),
+          _arg(w_scale, _F32, "w_scale", (E, N)), _arg(offsets, _I32, "offsets", (E + 1,)),
+          _arg(counts, _I32, "counts", (E,)), E, R, N, K, _arg(c, _FLOATS, "c", (R, N)),
+          _type(c, "c"), _arg(status, _I32, "status", (1,)))
 
 
 def moe_grouped_gemm_int8_gather(x, x_scale, row_src, w, w_scale, offsets, counts, c, status,
@@ -560,11 +579,11 @@ def moe_grouped_gemm_int8_gather(x, x_scale, row_src, w, w_scale, offsets, count
     R = row_src.numel()
     _call("moe_grouped_gemm_int8_gather", stream,
           (x, x_scale, row_src, w, w_scale, offsets, counts, c, status),
-          _ptr(x, _I8, "x", (T, K)), _ptr(x_scale, _F32, "x_scale", (T,)), T,
-          _ptr(row_src, _I32, "row_src", (R,)), _ptr(w, _I8, "w"),
-          _ptr(w_scale, _F32, "w_scale", (E, N)), _ptr(offsets, _I32, "offsets", (E + 1,)),
-          _ptr(counts, _I32, "counts", (E,)), E, R, N, K, _ptr(c, _FLOATS, "c", (R, N)),
-          _type(c, "c"), _ptr(status, _I32, "status", (1,)))
+          _arg(x, _I8, "x", (T, K)), _arg(x_scale, _F32, "x_scale", (T,)), T,
+          _arg(row_src, _I32, "row_src", (R,)), _arg(w, _I8, "w"),
+          _arg(w_scale, _F32, "w_scale", (E, N)), _arg(offsets, _I32, "offsets", (E + 1,)),
+          _arg(counts, _I32, "counts", (E,)), E, R, N, K, _arg(c, _FLOATS, "c", (R, N)),
+          _type(c, "c"), _arg(status, _I32, "status", (1,)))
 
 
 def moe_act_requant_int8(h, offsets, counts, q, q_scale, status, stream=None):
@@ -574,10 +593,10 @@ def moe_act_requant_int8(h, offsets, counts, q, q_scale, status, stream=None):
     I = I2 // 2
     E = counts.numel()
     _call("moe_act_requant_int8", stream, (h, offsets, counts, q, q_scale, status),
-          _ptr(h, _FLOATS, "h", (R, 2 * I)), _type(h, "h"),
-          _ptr(offsets, _I32, "offsets", (E + 1,)), _ptr(counts, _I32, "counts", (E,)), E, R, I,
-          _ptr(q, _I8, "q", (R, I)), _ptr(q_scale, _F32, "q_scale", (R,)),
-          _ptr(status, _I32, "status", (1,)))
+          _arg(h, _FLOATS, "h", (R, 2 * I)), _type(h, "h"),
+          _arg(offsets, _I32, "offsets", (E + 1,)), _arg(counts, _I32, "counts", (E,)), E, R, I,
+          _arg(q, _I8, "q", (R, I)), _arg(q_scale, _F32, "q_scale", (R,)),
+          _arg(status, _I32, "status", (1,)))
 
 
 def moe_ceiling_copy(src, dst, stream=None):

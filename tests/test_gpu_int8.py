@@ -272,7 +272,8 @@ def test_act_corrupt_table(gpu):
 
 # ------------------------------------------------------------- linear
 LINEAR = [(1, 16, 16), (1, 4096, 7168), (2, 256, 128), (4, 272, 400), (5, 144, 2064), (8, 512, 7168), (16, 1040, 1040),
-          (17, 64, 64), (40, 7168, 2048), (96, 528, 2048), (300, 272, 1040), (1, 48, 20000), (3, 32, 131056)]
+          (17, 64, 64), (40, 7168, 2048), (96, 528, 2048), (300, 272, 1040), (1, 48, 20000), (3, 32, 131056),
+          (4, 16, 15344), (1, 32, 61424), (1, 32, 61440), (3, 272, 208)]
 
 
 @pytest.mark.parametrize("dt", list(TYPES))
