@@ -29,7 +29,32 @@ namespace moe {
 
 constexpr uint32_t kOutOfRange = 0x80000000u;
 
-template <int BM, int BN, int WM, int WN, int GM, bool kGather, bool kRagged>
+template <int i>
+using Int = std::integral_constant<int, i>;
+
+// f(Int<a>), ..., f(Int<b - 1>)
+template <int a, int b, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (a < b) {
+    f(Int<a>());
+    each<a + 1, b>(f);
+  }
+}
+
+// Stage i of an operand: an LDS object of its own, so that accesses to one
+// are known not to touch another.
+template <int kBytes, int kOperand, int i>
+struct Stage {
+  __device__ __forceinline__ static uint8_t* get() {
+    __shared__ __attribute__((aligned(1024))) uint8_t s[kBytes];
+    return s;
+  }
+};
+
+// kDeep: 0, or the number of stages of both operands for launches of few
+// tiles: with one workgroup to a CU at most, nothing else hides the latency of
+// a step's loads, so they are issued kDeep - 1 steps ahead.
+template <int BM, int BN, int WM, int WN, int GM, int kDeep, bool kGather, bool kRagged>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_kernel(I8Args p) {
   constexpr int NWM = BM / WM;
   constexpr int NWN = BN / WN;
@@ -41,15 +66,12 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "chunks must split evenly");
   static_assert(MI >= 2, "the late loads need a subtile row before the barrier");
   constexpr int SA_B = BM * kBK, SB_B = BN * kBK;
-  constexpr int NSA = 3 * SA_B + 2 * SB_B <= kLdsBytes ? 3 : 2;
-  static_assert(NSA * SA_B + 2 * SB_B <= kLdsBytes, "tile stages exceed the LDS");
-  __shared__ __attribute__((aligned(1024))) uint8_t sA0[SA_B];
-  __shared__ __attribute__((aligned(1024))) uint8_t sA1[SA_B];
-  uint8_t* const sA2 = ThirdStage<NSA == 3 ? SA_B : 0>::get();
-  __shared__ __attribute__((aligned(1024))) uint8_t sB0[SB_B];
-  __shared__ __attribute__((aligned(1024))) uint8_t sB1[SB_B];
-  auto stA = [&](int i) -> uint8_t* { return i == 0 ? sA0 : i == 1 ? sA1 : sA2; };
-  auto stB = [&](int i) -> uint8_t* { return i == 0 ? sB0 : sB1; };
+  constexpr int NSA = kDeep ? kDeep : 3 * SA_B + 2 * SB_B <= kLdsBytes ? 3 : 2;
+  constexpr int NSB = kDeep ? kDeep : 2;
+  static_assert(NSA * SA_B + NSB * SB_B <= kLdsBytes, "tile stages exceed the LDS");
+  static_assert(6 % NSA == 0 && 6 % NSB == 0, "the K loop is unrolled by 6");
+  auto stA = [&](auto i) { return Stage<SA_B, 0, decltype(i)::value % NSA>::get(); };
+  auto stB = [&](auto i) { return Stage<SB_B, 1, decltype(i)::value % NSB>::get(); };
 
   // ---- which tile (the tile list's order is that of the FP8 products)
   const int N = p.N, K = p.K, rows_total = p.rows_total;
@@ -168,19 +190,21 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
   // the wave's last LDS read of it has landed, and the next step's fragments
   // are read under the last subtile row's multiplications.
   constexpr int kLateRow = MI >= 3 ? 1 : 0;
-  auto step = [&](int kb, auto sa_i, auto sb_i) __attribute__((always_inline)) {
-    constexpr int SAi = decltype(sa_i)::value;
-    constexpr int SBi = decltype(sb_i)::value;
+  // loads that the step's barrier leaves in flight: all issued after the next
+  // step's
+  constexpr int kInFlight = kDeep ? (kDeep - 2) * (CA + CB) : NSA == 3 ? CA : 0;
+  auto step = [&](int kb, auto unrolled) __attribute__((always_inline)) {
+    constexpr int U = decltype(unrolled)::value;
     // formed anew each step, so that no address per stage and subtile is kept
     asm volatile("" : "+v"(fa.lo), "+v"(fa.hi), "+v"(fb.lo), "+v"(fb.hi));
     if (kRagged) asm volatile("" : "+v"(vl[0]), "+v"(vl[1]));
-    const uint8_t* tA = stA(SAi);
-    const uint8_t* tAn = stA((SAi + 1) % NSA);
-    const uint8_t* tBn = stB((SBi + 1) % 2);
-    issue_b(kb + 1, stB((SBi + 1) % 2), kb + 1 < Kb);
+    const uint8_t* tA = stA(Int<U>());
+    const uint8_t* tAn = stA(Int<U + 1>());
+    const uint8_t* tBn = stB(Int<U + 1>());
+    issue_b(kb + NSB - 1, stB(Int<U + NSB - 1>()), kb + NSB - 1 < Kb);
 #pragma unroll
     for (int i = 0; i < MI - 1; ++i) {
-      if (i == kLateRow) issue_a(kb + NSA - 1, stA((SAi + NSA - 1) % NSA), kb + NSA - 1 < Kb);
+      if (i == kLateRow) issue_a(kb + NSA - 1, stA(Int<U + NSA - 1>()), kb + NSA - 1 < Kb);
       const v8i af = af_next;
       af_next = load_frag_at(tA, (i + 1) * 16 * kBK, fa);
       multiply(i, af);
@@ -190,10 +214,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
     for (int i = 0; i < MI - 1; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(acc[i][j]));
-    if constexpr (NSA == 3)
-      wait_vm<CA>();
-    else
-      wait_vm<0>();
+    wait_vm<kInFlight>();
     lds_barrier();
     const v8i af = af_next;
     // (the step's w fragments are replaced one by one, after their last use)
@@ -215,32 +236,29 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
     for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(acc[MI - 1][j]));
   };
 
-  issue_b(0, sB0, true);
-  issue_a(0, sA0, true);
-  if constexpr (NSA == 3) {
-    issue_a(1, sA1, Kb > 1);
-    wait_vm<CA>();
-  } else {
-    wait_vm<0>();
+  issue_b(0, stB(Int<0>()), true);
+  issue_a(0, stA(Int<0>()), true);
+  if constexpr (kDeep != 0) {
+    each<1, kDeep - 1>([&](auto i) {
+      constexpr int k = decltype(i)::value;
+      issue_b(k, stB(i), k < Kb);
+      issue_a(k, stA(i), k < Kb);
+    });
+  } else if constexpr (NSA == 3) {
+    issue_a(1, stA(Int<1>()), Kb > 1);
   }
+  wait_vm<kInFlight>();
   lds_barrier();
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) bf[j] = load_frag_at(sB0, j * 16 * kBK, fb);
-  af_next = load_frag_at(sA0, 0, fa);
-  // unrolled by 6 = lcm(3, 2), so every step names its stages statically
-  auto step_u = [&](int kb, auto u) __attribute__((always_inline)) {
-    constexpr int U = decltype(u)::value;
-    if (U == 0 || kb < Kb)
-      step(kb, std::integral_constant<int, U % NSA>(), std::integral_constant<int, U % 2>());
-  };
-  for (int kb = 0; kb < Kb; kb += 6) {
-    step_u(kb, std::integral_constant<int, 0>());
-    step_u(kb + 1, std::integral_constant<int, 1>());
-    step_u(kb + 2, std::integral_constant<int, 2>());
-    step_u(kb + 3, std::integral_constant<int, 3>());
-    step_u(kb + 4, std::integral_constant<int, 4>());
-    step_u(kb + 5, std::integral_constant<int, 5>());
-  }
+  for (int j = 0; j < NJ; ++j) bf[j] = load_frag_at(stB(Int<0>()), j * 16 * kBK, fb);
+  af_next = load_frag_at(stA(Int<0>()), 0, fa);
+  // unrolled by 6, a multiple of every number of stages, so that every step
+  // names its stages statically
+  for (int kb = 0; kb < Kb; kb += 6)
+    each<0, 6>([&](auto u) __attribute__((always_inline)) {
+      constexpr int U = decltype(u)::value;
+      if (U == 0 || kb + U < Kb) step(kb + U, u);
+    });
   // the last steps' (zero) loads land in stages that the epilogue reuses
   wait_vm<0>();
   lds_barrier();
@@ -291,21 +309,23 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
   static_assert(WN * 2 == 128, "staged rows are 128 bytes");
   constexpr auto fits = [](int parts) {
     const int region = WM / parts * WN * 2;
-    return (SA_B / region) * NSA + (SB_B / region) * 2 >= NW;
+    return (SA_B / region) * NSA + (SB_B / region) * NSB >= NW;
   };
   constexpr int kParts = fits(1) ? 1 : fits(2) ? 2 : 4;
   static_assert(fits(kParts) && MI % kParts == 0, "staging space");
   constexpr int PM = WM / kParts;
   constexpr int kRegion = PM * WN * 2;
   constexpr int kPerA = SA_B / kRegion, kPerB = SB_B / kRegion;
-  uint8_t* region;
-  if (wave < NSA * kPerA) {
-    const int st = wave / kPerA;
-    region = stA(st) + (wave - st * kPerA) * kRegion;
-  } else {
-    const int w = wave - NSA * kPerA;
-    region = w < kPerB ? sB0 + w * kRegion : sB1 + (w - kPerB) * kRegion;
-  }
+  uint8_t* region = nullptr;   // regions fill the A stages, then the B stages
+  each<0, NSA>([&](auto i) {
+    constexpr int k = decltype(i)::value;
+    if (wave >= k * kPerA && wave < (k + 1) * kPerA)
+      region = stA(i) + (wave - k * kPerA) * kRegion;
+  });
+  each<0, NSB>([&](auto i) {
+    constexpr int k = NSA * kPerA + decltype(i)::value * kPerB;
+    if (wave >= k && wave < k + kPerB) region = stB(i) + (wave - k) * kRegion;
+  });
   uint16_t* C = static_cast<uint16_t*>(p.c);
   const int c16 = lane & 7;
 #pragma unroll
@@ -339,7 +359,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
   }
 }
 
-template <int BM, int BN, int WM, int WN, int GM>
+template <int BM, int BN, int WM, int WN, int GM, int kDeep = 0>
 static moe_status_t launch_i8(const I8Args& p, hipStream_t st) {
   const long long m_tiles = p.offsets ? (long long)p.rows_total / BM + p.E
                                       : ((long long)p.rows_total + BM - 1) / BM;
@@ -351,24 +371,20 @@ static moe_status_t launch_i8(const I8Args& p, hipStream_t st) {
   const bool ragged = p.K % kBK != 0;
   if (p.row_src) {
     if (ragged)
-      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, true, true>), grid, block, 0,
+      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, kDeep, true, true>), grid, block, 0,
                          st, p);
     else
-      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, true, false>), grid, block,
+      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, kDeep, true, false>), grid, block,
                          0, st, p);
   } else {
     if (ragged)
-      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, false, true>), grid, block,
+      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, kDeep, false, true>), grid, block,
                          0, st, p);
     else
-      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, false, false>), grid, block,
+      hipLaunchKernelGGL((grouped_gemm_i8_kernel<BM, BN, WM, WN, GM, kDeep, false, false>), grid, block,
                          0, st, p);
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
-}
-
-static bool big_tiles_i8(long long rows_total, int N, int E) {
-  return rows_total >= 256LL * E && (rows_total / 256) * (N / 256) > 128;
 }
 
 template <int MT, int NT>
@@ -385,39 +401,46 @@ static moe_status_t launch_skinny(const I8Args& p, hipStream_t st) {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
 }
 
-// Few rows: the kernel that reads the weights once, straight to registers.
-// `rows` is a dense product's, or a segment's on average; `channels` all
-// experts'.  Its tile is as large as leaves 192 workgroups (a CU takes in some
-// 20 bytes a cycle whatever it runs, so the CUs have to share the bytes).
-static moe_status_t few_rows_i8(const I8Args& p, long long rows, long long channels,
-                                hipStream_t st) {
-  const bool many = channels >= 192 * 32;
-  if (rows <= 16) return launch_skinny<1, 1>(p, st);
-  if (rows <= 32) return many ? launch_skinny<2, 2>(p, st) : launch_skinny<2, 1>(p, st);
-  if (rows <= 64) return many ? launch_skinny<4, 2>(p, st) : launch_skinny<2, 2>(p, st);
-  return many ? launch_skinny<8, 2>(p, st) : launch_skinny<4, 2>(p, st);
-}
-
 // Launches the product in tiles chosen from the sizes alone (the same inside
-// graph capture).
+// graph capture).  `rows` is a dense product's, or a segment's on average.
+// Times are of products whose weights come from HBM, 4096 x 7168 and
+// 7168 x 2048 (N x K), in us.
+//
+//   * Up to 16 rows, and up to 32 where the tiles below would be few: the
+//     kernel that takes the weights straight to registers (1 row: 8.1 and
+//     6.2; as 64 x 128 tiles 46 and 17.  32 rows: 15.2 and 7.9.  Past 32 its
+//     repeated reads of the rows cost more than tiles do: 96 rows 23 and 13
+//     against 18 and 9).
+//   * One round of small tiles, loaded five steps ahead: 64 x 64 (128 rows:
+//     20.4 and 9.6; two and three stages of 64 x 128 tiles 45 and 17), then
+//     128 x 64 (512 and 256 rows: 27 and 11.5; 64 x 64 tiles 41 and 17), then
+//     128 x 128 two steps ahead (1024 rows of 4096 x 7168: 32; without the
+//     third stage of weights 40).  A CU takes in some 20 bytes a cycle
+//     whatever it runs, so as many of them as possible have to share the bytes.
+//   * 256 x 256 once that gives more than half the CUs a tile and segments
+//     have 256 rows: twice the work per byte of two 128 x 128 tiles (prefill
+//     gate/up 3.27 ms against 4.32).  192 x 256 where both fit one round (the
+//     EP72 share's gate/up: 67 against 78).
+//   * else 128 x 128, two workgroups to a CU; 64 x 128 for segments of up to
+//     128 rows where K is short (masked decode, K = 2048: 97 against 107; at
+//     K = 7168 203 against 172).
 static moe_status_t product_i8(const I8Args& p, hipStream_t st) {
   const long long rows = ((long long)p.rows_total + p.E - 1) / p.E;
-  const long long channels = (long long)p.E * p.N;
-#ifdef MOE_I8_FORCE
-  switch (MOE_I8_FORCE) {
-    case 64: return launch_i8<64, 128, 32, 64, 4>(p, st);
-    case 128: return launch_i8<128, 128, 64, 64, 4>(p, st);
-    case 256: return launch_i8<256, 256, 128, 64, 2>(p, st);
-    case 320: return launch_i8<320, 256, 160, 64, 2>(p, st);
-    case 192: return launch_i8<192, 256, 96, 64, 2>(p, st);
-    case 1282: return launch_i8<128, 256, 64, 64, 2>(p, st);
-    case 2561: return launch_i8<256, 128, 64, 64, 2>(p, st);
-    case 642: return launch_i8<64, 256, 32, 64, 4>(p, st);
+  auto tiles = [&](int bm, int bn) {
+    return p.E * ((rows + bm - 1) / bm) * ((p.N + bn - 1) / bn);
+  };
+  if (rows <= 16) return launch_skinny<1, 1>(p, st);
+  if (rows <= 32 && (p.E == 1 || tiles(64, 64) <= 240))
+    return (long long)p.E * p.N >= 192 * 32 ? launch_skinny<2, 2>(p, st)
+                                            : launch_skinny<2, 1>(p, st);
+  if (tiles(64, 64) <= 240) return launch_i8<64, 64, 32, 64, 4, 6>(p, st);
+  if (tiles(128, 64) <= 256) return launch_i8<128, 64, 32, 64, 4, 6>(p, st);
+  if (tiles(128, 128) <= 256) return launch_i8<128, 128, 64, 64, 4, 3>(p, st);
+  if (rows >= 256 && tiles(256, 256) > 128) {
+    if (tiles(192, 256) <= 256) return launch_i8<192, 256, 96, 64, 2>(p, st);
+    return launch_i8<256, 256, 128, 64, 2>(p, st);
   }
-#endif
-  if (rows <= 16 || (rows <= 128 && channels < 128 * 192) || (rows <= 32 && p.E == 1))
-    return few_rows_i8(p, rows, channels, st);
-  if (big_tiles_i8(p.rows_total, p.N, p.E)) return launch_i8<256, 256, 128, 64, 2>(p, st);
+  if (rows <= 128 && p.K <= 4096) return launch_i8<64, 128, 32, 64, 4>(p, st);
   return launch_i8<128, 128, 64, 64, 4>(p, st);
 }
 

@@ -5,11 +5,12 @@
 //   s = fp32(max_j |v_j| / 127), 1 for a row of zeros, at least 2^-126
 //   q_j = the integer nearest v_j / s, ties to even
 //
-// One workgroup per row.  The first kKeep slices of eight values that a
-// thread takes stay in its registers between the row's maximum and the
-// codes; a longer row's others are read (and the activation computed) again,
-// from the cache.  Reads 2 (or 4) bytes and writes one per value: bound by
-// HBM bandwidth.
+// A wave per row of up to 2048 values (no barrier), the four waves of a
+// workgroup per longer row.  The first kKeep slices of eight values that a
+// lane takes stay in its registers between the row's maximum and the codes;
+// the others of a row past 8192 values are read (and the activation computed)
+// again, from the cache.  Reads 2 (or 4) bytes and writes one per value:
+// bound by HBM bandwidth.
 #include "rows_i8.hpp"
 
 namespace moe {
@@ -32,50 +33,60 @@ __device__ __forceinline__ void row_slice(const void* x, size_t row, int cols, i
   }
 }
 
-template <int kType, bool kAct>
+// kWaves: waves per row (1 or 4).
+template <int kType, bool kAct, int kWaves>
 __global__ __launch_bounds__(kQThreads) void quant_int8_kernel(
     const void* __restrict__ x, int rows, int cols, uint8_t* __restrict__ q,
     float* __restrict__ scale, const int32_t* __restrict__ offsets,
     const int32_t* __restrict__ counts, int E, int32_t* __restrict__ status) {
+  constexpr int kRows = kQThreads / 64 / kWaves;   // rows of a workgroup
+  constexpr int kStep = kWaves * 64 * 8;           // values a row's lanes take at once
   __shared__ uint32_t red[kQThreads / 64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (kAct && blockIdx.x == 0 && threadIdx.x < 64 && status &&
       segments_bad(offsets, counts, E, threadIdx.x) && threadIdx.x == 0)
     atomicOr(status, MOE_ERR_BAD_INDEX);
-  for (int row = blockIdx.x; row < rows; row += gridDim.x) {
-    if (kAct && !row_valid(offsets, counts, E, rows, row)) continue;   // uniform
+  const int j0 = kWaves == 1 ? (threadIdx.x & 63) * 8 : threadIdx.x * 8;
+  for (int row = blockIdx.x * kRows + (kWaves == 1 ? wave : 0); row < rows;
+       row += gridDim.x * kRows) {
+    // all loads first (lanes past the row read its first slice again); the
+    // search for the row's segment runs while they are in flight
     float v[kKeep][8];
-    uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < kKeep; ++u) {
-      const int j = (u * kQThreads + (int)threadIdx.x) * 8;
-      if (j < cols) {
-        row_slice<kType, kAct>(x, row, cols, j, v[u]);
-        top = max_bits(v[u], top);
-      }
+      const int j = u * kStep + j0;
+      if (u * kStep < cols) row_slice<kType, kAct>(x, row, cols, j < cols ? j : 0, v[u]);
     }
-    for (int j = (kKeep * kQThreads + (int)threadIdx.x) * 8; j < cols; j += kQThreads * 8) {
+    if (kAct && !row_valid(offsets, counts, E, rows, row)) continue;   // the same for the row
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < kKeep; ++u)
+      if (u * kStep < cols) top = max_bits(v[u], top);
+    for (int j = kKeep * kStep + j0; j < cols; j += kStep) {
       float t[8];
       row_slice<kType, kAct>(x, row, cols, j, t);
       top = max_bits(t, top);
     }
     top = wave_max(top);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
-    __syncthreads();
+    if (kWaves > 1) {
+      if ((threadIdx.x & 63) == 0) red[wave] = top;
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kQThreads / 64; ++i) top = max(top, red[i]);
-    __syncthreads();
+      for (int i = 0; i < kWaves; ++i) top = max(top, red[i]);
+      __syncthreads();
+    }
     const float s = int8_scale(top);
     const bool fine = top < 0x7f800000u;
     const float inv = 1.f / s;
-    if (threadIdx.x == 0) scale[row] = s;
+    if (j0 == 0) scale[row] = s;
     uint8_t* out = q + (size_t)row * cols;
 #pragma unroll
     for (int u = 0; u < kKeep; ++u) {
-      const int j = (u * kQThreads + (int)threadIdx.x) * 8;
+      const int j = u * kStep + j0;
       if (j < cols)
         *reinterpret_cast<uint2*>(out + j) = fine ? int8_codes(v[u], s, inv) : make_uint2(0, 0);
     }
-    for (int j = (kKeep * kQThreads + (int)threadIdx.x) * 8; j < cols; j += kQThreads * 8) {
+    for (int j = kKeep * kStep + j0; j < cols; j += kStep) {
       float t[8];
       row_slice<kType, kAct>(x, row, cols, j, t);
       *reinterpret_cast<uint2*>(out + j) = fine ? int8_codes(t, s, inv) : make_uint2(0, 0);
@@ -83,22 +94,33 @@ __global__ __launch_bounds__(kQThreads) void quant_int8_kernel(
   }
 }
 
+template <int kType, bool kAct>
+static void launch_quant(const void* x, int rows, int cols, uint8_t* q, float* scale,
+                         const int32_t* offsets, const int32_t* counts, int E, int32_t* status,
+                         hipStream_t st) {
+  const bool one = cols <= kKeep * 64 * 8;
+  const long long blocks = one ? ((long long)rows + 3) / 4 : rows;
+  const dim3 grid((unsigned)(blocks < (1 << 22) ? blocks : (1 << 22))), block(kQThreads);
+  if (one)
+    hipLaunchKernelGGL((quant_int8_kernel<kType, kAct, 1>), grid, block, 0, st, x, rows, cols, q,
+                       scale, offsets, counts, E, status);
+  else
+    hipLaunchKernelGGL((quant_int8_kernel<kType, kAct, 4>), grid, block, 0, st, x, rows, cols, q,
+                       scale, offsets, counts, E, status);
+}
+
 template <bool kAct>
 static moe_status_t quantize_int8(const void* x, int dtype, int rows, int cols, int8_t* q,
                                   float* scale, const int32_t* offsets, const int32_t* counts,
                                   int E, int32_t* status, void* stream) {
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const dim3 grid((unsigned)(rows < (1 << 22) ? rows : (1 << 22))), block(kQThreads);
   uint8_t* qb = reinterpret_cast<uint8_t*>(q);
   if (dtype == MOE_TYPE_F32)
-    hipLaunchKernelGGL((quant_int8_kernel<MOE_TYPE_F32, kAct>), grid, block, 0, st, x, rows, cols,
-                       qb, scale, offsets, counts, E, status);
+    launch_quant<MOE_TYPE_F32, kAct>(x, rows, cols, qb, scale, offsets, counts, E, status, st);
   else if (dtype == MOE_TYPE_BF16)
-    hipLaunchKernelGGL((quant_int8_kernel<MOE_TYPE_BF16, kAct>), grid, block, 0, st, x, rows,
-                       cols, qb, scale, offsets, counts, E, status);
+    launch_quant<MOE_TYPE_BF16, kAct>(x, rows, cols, qb, scale, offsets, counts, E, status, st);
   else
-    hipLaunchKernelGGL((quant_int8_kernel<MOE_TYPE_F16, kAct>), grid, block, 0, st, x, rows, cols,
-                       qb, scale, offsets, counts, E, status);
+    launch_quant<MOE_TYPE_F16, kAct>(x, rows, cols, qb, scale, offsets, counts, E, status, st);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
 }
 

@@ -52,8 +52,10 @@ __device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
 }
 
 // Eight codes.  v * inv + 1.5 * 2^23 rounds to an integer whose two's
-// complement is in the low bits; only where a residual reaches half a step
-// (rare) is an integer moved.
+// complement is in the low bits.  Where a residual reaches half a step (a tie,
+// or a quotient so near one that inv's rounding shows) an integer may have to
+// move: ties are checked first, as a row whose scale is a power of two has
+// many and they are right already.
 __device__ __forceinline__ uint2 int8_codes(const float (&v)[8], float s, float inv) {
   constexpr float kShift = 12582912.f;
   float t[8], far = 0.f;
@@ -63,15 +65,23 @@ __device__ __forceinline__ uint2 int8_codes(const float (&v)[8], float s, float 
     far = fmaxf(far, fabsf(fmaf(kShift - t[i], s, v[i])));
   }
   if (far + far >= s) {
+    bool wrong = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float q = t[i] - kShift;
-      const float d = fmaf(-q, s, v[i]), d2 = d + d;
-      const bool odd = (__float_as_uint(t[i]) & 1u) != 0;
-      if (d2 > s || (d2 == s && odd))
-        t[i] = q + 1.f + kShift;
-      else if (d2 < -s || (d2 == -s && odd))
-        t[i] = q - 1.f + kShift;
+      const float d = fabsf(fmaf(kShift - t[i], s, v[i]));
+      wrong |= d + d > s || (d + d == s && (__float_as_uint(t[i]) & 1u) != 0);
+    }
+    if (wrong) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float q = t[i] - kShift;
+        const float d = fmaf(-q, s, v[i]), d2 = d + d;
+        const bool odd = (__float_as_uint(t[i]) & 1u) != 0;
+        if (d2 > s || (d2 == s && odd))
+          t[i] = q + 1.f + kShift;
+        else if (d2 < -s || (d2 == -s && odd))
+          t[i] = q - 1.f + kShift;
+      }
     }
   }
   uint32_t w[2];

@@ -120,7 +120,9 @@ def test_quantize_non_finite(gpu, dt):
 # ------------------------------------------------------------- dense
 DENSE = [(1, 16, 16), (1, 128, 128), (2, 4096, 7168), (3, 48, 80), (16, 272, 144), (17, 272, 144),
          (33, 7168, 2048), (64, 144, 4112), (65, 144, 4112), (130, 144, 4112), (300, 256, 256),
-         (257, 528, 1040), (700, 1040, 7168), (1500, 768, 16), (8448, 1296, 272), (8200, 4096, 384)]
+         (257, 528, 1040), (700, 1040, 7168), (1500, 768, 16), (8448, 1296, 272), (8200, 4096, 384),
+         (32, 16400, 48), (31, 6160, 80), (96, 7168, 2048), (200, 7168, 272), (1000, 4096, 400), (2400, 4096, 144),
+         (2048, 4096, 1040), (2048, 4112, 128), (40, 16384, 656), (129, 80, 896)]
 
 
 @pytest.mark.parametrize("shape", DENSE, ids=["x".join(map(str, s)) for s in DENSE])
@@ -156,7 +158,9 @@ def test_gemm_largest_sum(gpu):
 GROUPED = [(1, 16, 16, [1], 0, 0), (4, 128, 256, [3, 0, 130, 1], 5, 7), (3, 272, 1040, [64, 65, 1], 1, 0),
            (8, 4096, 512, [0, 1, 16, 17, 33, 48, 100, 128], 0, 30), (2, 528, 144, [300, 257], 127, 1),
            (70, 64, 48, None, 0, 3), (300, 32, 32, None, 2, 0), (3, 4096, 400, [2900, 1, 2700], 60, 0),
-           (2, 784, 7168, [513, 700], 0, 0)]
+           (2, 784, 7168, [513, 700], 0, 0), (16, 4096, 4112, [40, 0, 64, 65, 128, 1, 17, 90] * 2, 3, 0),
+           (40, 2064, 272, [20, 33, 0, 1, 31] * 8, 0, 0), (4, 4096, 256, [600, 640, 580, 700], 10, 0),
+           (3, 1040, 144, [300, 200, 129], 0, 5)]
 
 
 def segments(shape):
