@@ -102,15 +102,23 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
   const int Kb = (K + kBK - 1) / kBK;
   const int n0 = tile_n * BN;
 
+  // ---- tile rows of w: row 16 j + 4 g + q of a wave's 64 holds channel
+  //   channel(j, g, q) = 32 (j / 2) + 8 g + 4 (j % 2) + q,
+  // so that a lane's sums of two neighbouring subtiles are eight neighbouring
+  // channels and can be stored as they are (staging them through LDS, to
+  // write whole rows, took the memory that the next tile's loads want).
+  //
   // ---- tile loads.  A chunk is 8 rows; the lane's row is lane / 8, its
   // 16-byte piece the one that belongs at place lane % 8 of that row in an
   // even (odd) 8-row half.
   const int piece0 = (lane & 7) ^ (lane >> 3);
-  uint32_t vl[2];
+  uint32_t vl[2], vb[2];
   int lim[2];
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
     vl[o] = (uint32_t)(lane >> 3) * (uint32_t)K + (uint32_t)((piece0 ^ o) << 4);
+    vb[o] = (uint32_t)(8 * (lane >> 5) + ((lane >> 3) & 3)) * (uint32_t)K +
+            (uint32_t)((piece0 ^ o) << 4);
     lim[o] = K - ((piece0 ^ o) << 4);
   }
   const long long a_bytes = kGather ? (long long)p.src_rows * K : (long long)(rows_total - row0) * K;
@@ -161,8 +169,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
     for (int u = 0; u < CB; ++u) {
       const int c = wave * CB + u;
       const int o = CB % 2 == 0 ? (u & 1) : (c & 1);
-      load16(rsrc_b, tB + c * 1024, o ? vl[1] : vl[0],
-             (uint32_t)(c * 8) * (uint32_t)K + (uint32_t)kb * kBK, kb * kBK, o, live);
+      // the chunk's channels (see channel()): the lane's part is in vb
+      const int first = c / 8 * 64 + ((c >> 2) & 1) * 32 + (c & 1) * 16 + ((c >> 1) & 1) * 4;
+      load16(rsrc_b, tB + c * 1024, o ? vb[1] : vb[0],
+             (uint32_t)first * (uint32_t)K + (uint32_t)kb * kBK, kb * kBK, o, live);
     }
   };
 
@@ -197,7 +207,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
     constexpr int U = decltype(unrolled)::value;
     // formed anew each step, so that no address per stage and subtile is kept
     asm volatile("" : "+v"(fa.lo), "+v"(fa.hi), "+v"(fb.lo), "+v"(fb.hi));
-    if (kRagged) asm volatile("" : "+v"(vl[0]), "+v"(vl[1]));
+    if (kRagged) asm volatile("" : "+v"(vl[0]), "+v"(vl[1]), "+v"(vb[0]), "+v"(vb[1]));
     const uint8_t* tA = stA(Int<U>());
     const uint8_t* tAn = stA(Int<U + 1>());
     const uint8_t* tBn = stB(Int<U + 1>());
@@ -259,19 +269,18 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
       constexpr int U = decltype(u)::value;
       if (U == 0 || kb + U < Kb) step(kb + U, u);
     });
-  // the last steps' (zero) loads land in stages that the epilogue reuses
+  // (the last steps' zero loads still land in stages of this workgroup's LDS)
   wait_vm<0>();
-  lds_barrier();
 
-  // ---- epilogue: scales, then 16-bit outputs staged in the stage memory
-  // (each wave its own region, rows of WN * 2 = 128 bytes, 8-byte pieces
-  // XOR-permuted by the row) and stored as 16-byte pieces of whole rows;
-  // fp32 outputs are stored by the lanes that hold them, four channels each.
-  const int wcol = n0 + wn * WN;
+  // ---- epilogue: scales, conversion, and stores straight from the lanes
+  // that hold the sums: sums (i, j, 0..3) and (i, j + 1, 0..3) with j even are
+  // eight neighbouring channels of row r16, 16 bytes in 16 bits, and the four
+  // lanes of a row write 64 bytes together.
+  const int wcol = n0 + wn * WN + 8 * g;
   float sw[NJ][4];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int n = wcol + j * 16 + 4 * g;
+    const int n = wcol + 32 * (j >> 1) + 4 * (j & 1);
     const float* ws = p.w_scale + (size_t)e_sel * N;
 #pragma unroll
     for (int q = 0; q < 4; ++q) sw[j][q] = n + q < N ? ws[n + q] : 0.f;
@@ -287,74 +296,58 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
     }
     sa[i] = at >= 0 ? p.a_scale[at] : 0.f;
   }
-  auto value = [&](int i, int j, int q) -> float {
-    return (float)acc[i][j][q] * (sa[i] * sw[j][q]);
-  };
-  if (p.c_type == MOE_TYPE_F32) {
-    float* C = static_cast<float*>(p.c);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int row = row0 + wm * WM + i * 16 + r16;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int n = wcol + j * 16 + 4 * g;
-        if (row < row_end && n < N)
-          *reinterpret_cast<float4*>(C + (size_t)row * N + n) =
-              make_float4(value(i, j, 0), value(i, j, 1), value(i, j, 2), value(i, j, 3));
-      }
-    }
-    return;
-  }
   const bool half = p.c_type == MOE_TYPE_F16;
-  static_assert(WN * 2 == 128, "staged rows are 128 bytes");
-  constexpr auto fits = [](int parts) {
-    const int region = WM / parts * WN * 2;
-    return (SA_B / region) * NSA + (SB_B / region) * NSB >= NW;
-  };
-  constexpr int kParts = fits(1) ? 1 : fits(2) ? 2 : 4;
-  static_assert(fits(kParts) && MI % kParts == 0, "staging space");
-  constexpr int PM = WM / kParts;
-  constexpr int kRegion = PM * WN * 2;
-  constexpr int kPerA = SA_B / kRegion, kPerB = SB_B / kRegion;
-  uint8_t* region = nullptr;   // regions fill the A stages, then the B stages
-  each<0, NSA>([&](auto i) {
-    constexpr int k = decltype(i)::value;
-    if (wave >= k * kPerA && wave < (k + 1) * kPerA)
-      region = stA(i) + (wave - k * kPerA) * kRegion;
-  });
-  each<0, NSB>([&](auto i) {
-    constexpr int k = NSA * kPerA + decltype(i)::value * kPerB;
-    if (wave >= k && wave < k + kPerB) region = stB(i) + (wave - k) * kRegion;
-  });
-  uint16_t* C = static_cast<uint16_t*>(p.c);
-  const int c16 = lane & 7;
+  static_assert(NJ == 4, "a wave's channels are two pieces of 32");
 #pragma unroll
-  for (int part = 0; part < kParts; ++part) {
+  for (int i = 0; i < MI; ++i) {
+    float v[2][8];
 #pragma unroll
-    for (int i = part * (MI / kParts); i < (part + 1) * (MI / kParts); ++i) {
-      const int r = (i - part * (MI / kParts)) * 16 + r16;
-      const int f = ((r >> 1) & 7) << 1;
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const float v0 = value(i, j, 0), v1 = value(i, j, 1), v2 = value(i, j, 2),
-                    v3 = value(i, j, 3);
-        uint2 o;
-        o.x = half ? pack2_f16(v0, v1) : pack2_bf16(v0, v1);
-        o.y = half ? pack2_f16(v2, v3) : pack2_bf16(v2, v3);
-        *reinterpret_cast<uint2*>(region + r * 128 + (((j * 4 + g) ^ f) << 3)) = o;
+      for (int q = 0; q < 8; ++q)
+        v[s][q] = (float)acc[i][2 * s + (q >> 2)][q & 3] *
+                  (sa[i] * sw[2 * s + (q >> 2)][q & 3]);
+    const int top = row0 + wm * WM + i * 16;
+    if (p.c_type == MOE_TYPE_F32) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int row = top + r16, n = wcol + 32 * s;
+        if (row < row_end && n < N) {
+          float4* c4 = reinterpret_cast<float4*>(static_cast<float*>(p.c) + (size_t)row * N + n);
+          c4[0] = make_float4(v[s][0], v[s][1], v[s][2], v[s][3]);
+          c4[1] = make_float4(v[s][4], v[s][5], v[s][6], v[s][7]);
+        }
       }
+      continue;
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    // lanes of rows 0..7 exchange their second piece for the first piece of
+    // the row 8 further: a store then writes eight rows' whole 128 bytes
+    // (sixteen rows' 64 bytes took 3-7% longer where the stores weigh)
+    const bool low = r16 < 8;
+    u32x4 first, second;
 #pragma unroll
-    for (int rr = 0; rr < PM; rr += 8) {
-      const int r = rr + (lane >> 3);
-      const uint4 v =
-          *reinterpret_cast<const uint4*>(region + r * 128 + ((c16 ^ ((r >> 1) & 7)) << 4));
-      const int row = row0 + wm * WM + part * PM + r;
-      const int n = wcol + c16 * 8;
-      if (row < row_end && n < N)
-        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v),
-                                    reinterpret_cast<u32x4*>(C + (size_t)row * N + n));
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t w0 = half ? pack2_f16(v[0][2 * q], v[0][2 * q + 1])
+                               : pack2_bf16(v[0][2 * q], v[0][2 * q + 1]);
+      const uint32_t w1 = half ? pack2_f16(v[1][2 * q], v[1][2 * q + 1])
+                               : pack2_bf16(v[1][2 * q], v[1][2 * q + 1]);
+      const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(
+          0, (int)(low ? w1 : w0), 0x128, 0xf, 0xf, false);   // row_ror:8
+      first[q] = low ? w0 : got;
+      second[q] = low ? got : w1;
+    }
+    const int n = wcol + (low ? 0 : 32);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int row = top + (r16 & 7) + 8 * s;
+      if (row < row_end && n < N) {
+        u32x4* c4 = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.c) + (size_t)row * N + n);
+#ifdef MOE_PLAIN
+        *c4 = s ? second : first;
+#else
+        __builtin_nontemporal_store(s ? second : first, c4);
+#endif
+      }
     }
   }
 }
