@@ -36,6 +36,7 @@ def test_gemm_refusals():
         assert call(**bad) == 1, bad
     for bad in (dict(N=40), dict(K=40), dict(K=131072), dict(a=ODD), dict(w=ODD), dict(c=ODD)):
         assert call(**bad) == 2, bad
+    assert call(M=0x1ffffc01) == 2 and call(M=0x1ffffc00, a=N) == 1   # row scales past 31 bits
     assert call(M=0, a=N, sa=N, c=N) == 0
 
 
