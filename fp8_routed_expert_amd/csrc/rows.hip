@@ -21,13 +21,15 @@
 // access is wide and none leaves the row.  The overlap writes the same values
 // twice and is left out of dot products.  Rows shorter than 16 bytes are one
 // chunk of single bytes.
+#include <type_traits>
+
 #include "device_common.hpp"
 
 namespace moe {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowWaves = kRowThreads / 64;
-constexpr int kRowChunks = 2;      // 16-byte chunks per lane and piece of a row
+typedef unsigned int row_chunk __attribute__((ext_vector_type(4)));
 
 struct F32 {
   static constexpr int kSize = 4, kN = 4;
@@ -87,12 +89,14 @@ struct RowShape {
 };
 
 // Sixteen bytes at p (all of the row where it is shorter).  kAligned: p is
-// 16-byte aligned and the row a multiple of 16 bytes.
-template <bool kAligned>
+// 16-byte aligned and the row a multiple of 16 bytes.  kStream: past the
+// caches (see streamed()).
+template <bool kAligned, bool kStream = false>
 __device__ __forceinline__ uint4 load_chunk(const uint8_t* p, int row_bytes) {
   uint4 v = make_uint4(0, 0, 0, 0);
   if (kAligned) {
-    v = *reinterpret_cast<const uint4*>(p);
+    const row_chunk* c = reinterpret_cast<const row_chunk*>(p);
+    v = __builtin_bit_cast(uint4, kStream ? __builtin_nontemporal_load(c) : *c);
   } else if (row_bytes >= 16) {
     __builtin_memcpy(&v, p, 16);
   } else {
@@ -103,10 +107,12 @@ __device__ __forceinline__ uint4 load_chunk(const uint8_t* p, int row_bytes) {
   return v;
 }
 
+// Outputs are written past the caches: nothing here reads them again, and a
+// prefill share's permute took 536 us so against 547.
 template <bool kAligned>
 __device__ __forceinline__ void store_chunk(uint8_t* p, int row_bytes, const uint4& v) {
   if (kAligned) {
-    *reinterpret_cast<uint4*>(p) = v;
+    __builtin_nontemporal_store(__builtin_bit_cast(row_chunk, v), reinterpret_cast<row_chunk*>(p));
   } else if (row_bytes >= 16) {
     __builtin_memcpy(p, &v, 16);
   } else {
@@ -115,16 +121,39 @@ __device__ __forceinline__ void store_chunk(uint8_t* p, int row_bytes, const uin
   }
 }
 
-// Lane k of a wave holds pick k's slot (-1: none, or not a row).  Returns
-// the valid picks as a bit mask; `bad` says whether a slot lies past the
-// buffer.
-__device__ __forceinline__ unsigned long long token_slots(const int32_t* slot_of, long long t,
-                                                          int K, int rows_total, int lane,
-                                                          int& s, bool& bad) {
-  s = lane < K ? slot_of[t * K + lane] : -1;
-  bad = __ballot(s >= rows_total) != 0;
-  return __ballot(s >= 0 && s < rows_total);
-}
+// How a row is shared out: a wave (kLanes 64) takes a piece of at most 64
+// kCh chunks, or each of its four groups of 16 lanes a whole short row.
+//
+// The token's picks: lane k of the wave or group holds pick k's slot.  valid
+// is a bit mask of those that are rows; every lane of the group has the same.
+template <int kLanes>
+struct Picks {
+  int s;
+  unsigned long long valid;
+  bool bad;   // a slot past the buffer
+  int base;   // the group's first lane
+  __device__ __forceinline__ Picks(const int32_t* slot_of, long long t, int K, int rows_total,
+                                   bool live) {
+    const int lane = threadIdx.x & 63, at = lane % kLanes;
+    base = lane - at;
+    s = live && at < K ? slot_of[t * K + at] : -1;
+    unsigned long long b = __ballot(s >= rows_total);
+    valid = __ballot(s >= 0 && s < rows_total);
+    if (kLanes < 64) {
+      constexpr unsigned long long kMask = (1ull << (kLanes & 63)) - 1;
+      valid = (valid >> base) & kMask;
+      b = (b >> base) & kMask;
+    }
+    bad = b != 0;
+  }
+  // the value that pick k's lane holds
+  __device__ __forceinline__ int of(int v, int k) const {
+    return kLanes == 64 ? __builtin_amdgcn_readlane(v, k) : __shfl(v, base + k);
+  }
+  __device__ __forceinline__ float of(float v, int k) const {
+    return __int_as_float(of(__float_as_int(v), k));
+  }
+};
 
 // Rows of the buffer that no token goes to are set to zero: one wave per 64
 // rows reads their sources and clears those without one.
@@ -149,42 +178,40 @@ __device__ __forceinline__ void zero_rows(long long w, const int32_t* __restrict
   }
 }
 
-// One wave per piece of a source row (at most 64 kRowChunks chunks).
-template <bool kAligned>
+template <int kLanes, int kCh, bool kAligned>
 __global__ __launch_bounds__(kRowThreads) void permute_rows_kernel(
     const uint8_t* __restrict__ x, const int32_t* __restrict__ slot_of, int T, int K,
     RowShape row, int pieces, int plen, int rows_total, uint8_t* __restrict__ a,
     const int32_t* __restrict__ row_src, long long zero_waves, int32_t* __restrict__ status) {
-  const int lane = threadIdx.x & 63;
-  const long long units = zero_waves + (long long)T * pieces;
+  constexpr int kGroups = 64 / kLanes;   // rows of a wave
+  const int at = threadIdx.x & (kLanes - 1);
+  const long long units = zero_waves + ((long long)T * pieces + kGroups - 1) / kGroups;
   for (long long w = (long long)blockIdx.x * kRowWaves + (threadIdx.x >> 6); w < units;
        w += (long long)gridDim.x * kRowWaves) {
     if (w < zero_waves) {
       zero_rows(w, row_src, rows_total, row.bytes, a);
       continue;
     }
-    const long long u0 = w - zero_waves;
-    const long long t = u0 / pieces;
-    const int c0 = (int)(u0 - t * pieces) * plen;
+    const long long u0 = (w - zero_waves) * kGroups + (threadIdx.x & 63) / kLanes;
+    const bool live = kLanes == 64 || u0 < T;
+    const long long t = live ? u0 / pieces : 0;
+    const int c0 = kLanes == 64 ? (int)(u0 - t * pieces) * plen : 0;
     const int cend = min(c0 + plen, row.chunks);
-    int s;
-    bool bad;
-    unsigned long long m = token_slots(slot_of, t, K, rows_total, lane, s, bad);
-    if (bad && lane == 0 && c0 == 0) atomicOr(status, MOE_ERR_BAD_INDEX);
+    const Picks<kLanes> picks(slot_of, t, K, rows_total, live);
+    if (picks.bad && at == 0 && c0 == 0) atomicOr(status, MOE_ERR_BAD_INDEX);
     const uint8_t* src = x + t * (long long)row.bytes;
-    uint4 v[kRowChunks];
+    uint4 v[kCh];
 #pragma unroll
-    for (int u = 0; u < kRowChunks; ++u) {
-      const int c = c0 + lane + u * 64;
+    for (int u = 0; u < kCh; ++u) {
+      const int c = c0 + at + u * kLanes;
       v[u] = load_chunk<kAligned>(src + row.start(c < cend ? c : c0), row.bytes);
     }
-    while (m) {
+    for (unsigned long long m = picks.valid; m; m &= m - 1) {
       const int k = __ffsll((long long)m) - 1;
-      m &= m - 1;
-      uint8_t* dst = a + (long long)__builtin_amdgcn_readlane(s, k) * row.bytes;
+      uint8_t* dst = a + (long long)picks.of(picks.s, k) * row.bytes;
 #pragma unroll
-      for (int u = 0; u < kRowChunks; ++u) {
-        const int c = c0 + lane + u * 64;
+      for (int u = 0; u < kCh; ++u) {
+        const int c = c0 + at + u * kLanes;
         if (c < cend) store_chunk<kAligned>(dst + row.start(c), row.bytes, v[u]);
       }
     }
@@ -192,129 +219,191 @@ __global__ __launch_bounds__(kRowThreads) void permute_rows_kernel(
 }
 
 // out[t] = sum over the valid picks, in ascending k, of (w[t, k] *) y[slot]:
-// the combine, and (kWeighted false) the gradient of the permute.
-template <typename El, bool kAligned, bool kWeighted>
+// the combine, and (kWeighted false) the gradient of the permute.  Two rows'
+// loads are in flight at a time.
+template <typename El, int kLanes, int kCh, bool kAligned, bool kStream, bool kWeighted>
 __global__ __launch_bounds__(kRowThreads) void gather_sum_kernel(
     const uint8_t* __restrict__ y, int rows_total, const int32_t* __restrict__ slot_of,
     const float* __restrict__ topk_w, int T, int K, RowShape row, int pieces, int plen,
     uint8_t* __restrict__ out, int32_t* __restrict__ status) {
   constexpr int N = El::kN;
-  const int lane = threadIdx.x & 63;
-  const long long units = (long long)T * pieces;
+  constexpr int kGroups = 64 / kLanes;
+  const int at = threadIdx.x & (kLanes - 1);
+  const long long units = ((long long)T * pieces + kGroups - 1) / kGroups;
   for (long long w = (long long)blockIdx.x * kRowWaves + (threadIdx.x >> 6); w < units;
        w += (long long)gridDim.x * kRowWaves) {
-    const long long t = w / pieces;
-    const int c0 = (int)(w - t * pieces) * plen;
+    const long long u0 = w * kGroups + (threadIdx.x & 63) / kLanes;
+    const bool live = kLanes == 64 || u0 < T;
+    const long long t = live ? u0 / pieces : 0;
+    const int c0 = kLanes == 64 ? (int)(u0 - t * pieces) * plen : 0;
     const int cend = min(c0 + plen, row.chunks);
-    int s;
-    bool bad;
-    unsigned long long m = token_slots(slot_of, t, K, rows_total, lane, s, bad);
-    const float wt = kWeighted && lane < K ? topk_w[t * K + lane] : 1.f;
-    if (bad && lane == 0 && c0 == 0) atomicOr(status, MOE_ERR_BAD_INDEX);
-    float acc[kRowChunks][N];
+    const Picks<kLanes> picks(slot_of, t, K, rows_total, live);
+    const float wt = kWeighted && live && at < K ? topk_w[t * K + at] : 1.f;
+    if (picks.bad && at == 0 && c0 == 0) atomicOr(status, MOE_ERR_BAD_INDEX);
+    float acc[kCh][N];
 #pragma unroll
-    for (int u = 0; u < kRowChunks; ++u)
+    for (int u = 0; u < kCh; ++u)
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[u][i] = 0.f;
-    while (m) {
-      const int k = __ffsll((long long)m) - 1;
-      m &= m - 1;
-      const uint8_t* src = y + (long long)__builtin_amdgcn_readlane(s, k) * row.bytes;
-      const float wk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wt), k));
-      uint4 v[kRowChunks];
+    auto load = [&](int k, uint4 (&v)[kCh]) {
+      const uint8_t* src = y + (long long)picks.of(picks.s, k) * row.bytes;
 #pragma unroll
-      for (int u = 0; u < kRowChunks; ++u) {
-        const int c = c0 + lane + u * 64;
-        v[u] = load_chunk<kAligned>(src + row.start(c < cend ? c : c0), row.bytes);
+      for (int u = 0; u < kCh; ++u) {
+        const int c = c0 + at + u * kLanes;
+        v[u] = load_chunk<kAligned, kStream>(src + row.start(c < cend ? c : c0), row.bytes);
       }
+    };
+    auto add = [&](int k, const uint4 (&v)[kCh]) {
+      const float wk = picks.of(wt, k);
 #pragma unroll
-      for (int u = 0; u < kRowChunks; ++u) {
+      for (int u = 0; u < kCh; ++u) {
         float f[N];
         El::unpack(v[u], f);
 #pragma unroll
         for (int i = 0; i < N; ++i)
           acc[u][i] = kWeighted ? fmaf(wk, f[i], acc[u][i]) : acc[u][i] + f[i];
       }
+    };
+    unsigned long long m = picks.valid;
+    while (m) {
+      const int k0 = __ffsll((long long)m) - 1;
+      m &= m - 1;
+      uint4 v0[kCh], v1[kCh];
+      load(k0, v0);
+      if (m) {
+        const int k1 = __ffsll((long long)m) - 1;
+        m &= m - 1;
+        load(k1, v1);
+        add(k0, v0);
+        add(k1, v1);
+      } else {
+        add(k0, v0);
+      }
     }
     uint8_t* dst = out + t * (long long)row.bytes;
 #pragma unroll
-    for (int u = 0; u < kRowChunks; ++u) {
-      const int c = c0 + lane + u * 64;
-      if (c < cend) store_chunk<kAligned>(dst + row.start(c), row.bytes, El::pack(acc[u]));
+    for (int u = 0; u < kCh; ++u) {
+      const int c = c0 + at + u * kLanes;
+      if (c < cend && live) store_chunk<kAligned>(dst + row.start(c), row.bytes, El::pack(acc[u]));
     }
   }
 }
 
-// Gradient of the combine, one workgroup per token: its dout row is read
-// once and kept in registers piece by piece, each of its y rows is read and
-// its dy row written in the same pass.  A wave's partial dot products are
-// summed over its lanes, and the waves' in a fixed order.
-template <typename El, bool kAligned>
-__global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(
+// Sum over the kLanes lanes of a group, in every one of them.
+template <int kLanes>
+__device__ __forceinline__ float group_sum(float d) {
+#pragma unroll
+  for (int o = kLanes / 2; o >= 1; o >>= 1) d += __shfl_xor(d, o);
+  return d;
+}
+
+// Gradient of the combine: a token's dout row is read once and its chunks kept
+// in registers; each of its y rows is read and its dy row written in the same
+// pass.  A lane's products of a row are summed first, then its group's lanes,
+// then (kBlock: the workgroup's waves share a token) the waves in order: no
+// atomics.  Rows longer than the registers hold are walked in parts.
+//
+// Few chunks per lane leave room for many waves, which is what keeps the
+// memory busy (a prefill share, 5.0 GB: 925 us with 512 threads of one chunk,
+// 955 with 256 of two, 1014 with 256 of four; two rows' loads in flight
+// 945-965).  Unaligned rows took 280 us with 256 threads of two chunks against
+// 356.
+constexpr int grad_threads(bool block, bool aligned) { return block && aligned ? 512 : 256; }
+
+template <typename El, int kLanes, bool kBlock, bool kAligned, bool kStream>
+__global__ __launch_bounds__(grad_threads(kBlock, kAligned)) void combine_grad_kernel(
     const uint8_t* __restrict__ dout, const uint8_t* __restrict__ y, int rows_total,
     const int32_t* __restrict__ slot_of, const float* __restrict__ topk_w, int T, int K,
     RowShape row, uint8_t* __restrict__ dy, float* __restrict__ dw,
-    const int32_t* __restrict__ row_src, long long zero_blocks, int32_t* __restrict__ status) {
+    const int32_t* __restrict__ row_src, long long zero_units, int32_t* __restrict__ status) {
   constexpr int N = El::kN;
-  __shared__ float part[kRowWaves][MOE_MAX_TOPK];
-  const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const long long blocks = zero_blocks + T;
-  for (long long b = blockIdx.x; b < blocks; b += gridDim.x) {
-    if (b < zero_blocks) {
-      zero_rows(b * kRowWaves + wave, row_src, rows_total, row.bytes, dy);
+  constexpr int kThreads = grad_threads(kBlock, kAligned), kWaves = kThreads / 64;
+  constexpr int kCh = kThreads == 512 ? 1 : 2;
+  constexpr int kStep = kBlock ? kThreads : kLanes;   // lanes on a row
+  constexpr int kPer = kBlock ? 1 : kRowThreads / kLanes;   // tokens of a workgroup
+  __shared__ float part[kBlock ? kWaves : 1][MOE_MAX_TOPK];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int at = kBlock ? (int)threadIdx.x : (int)threadIdx.x & (kLanes - 1);
+  const long long units = zero_units + ((long long)T + kPer - 1) / kPer;
+  for (long long b = blockIdx.x; b < units; b += gridDim.x) {
+    if (b < zero_units) {
+      zero_rows(b * kWaves + wave, row_src, rows_total, row.bytes, dy);
       continue;
     }
-    const long long t = b - zero_blocks;
-    int s;
-    bool bad;
-    const unsigned long long valid = token_slots(slot_of, t, K, rows_total, lane, s, bad);
-    const float wt = topk_w && lane < K ? topk_w[t * K + lane] : 0.f;
-    if (bad && threadIdx.x == 0) atomicOr(status, MOE_ERR_BAD_INDEX);
-    float dots = 0.f;   // of pick `lane`
-    for (int c0 = wave * 64; c0 < row.chunks; c0 += kRowThreads) {
-      const int c = c0 + lane;
-      const bool in = c < row.chunks;
-      const int at = row.start(in ? c : 0);
-      // elements of this chunk that the chunk before it has too
-      const int skip = kAligned ? 0 : (16 * c - at) / El::kSize;
-      float g[N];
-      El::unpack(load_chunk<kAligned>(dout + t * (long long)row.bytes + at, row.bytes), g);
-      unsigned long long m = valid;
-      while (m) {
-        const int k = __ffsll((long long)m) - 1;
-        m &= m - 1;
-        const long long off = (long long)__builtin_amdgcn_readlane(s, k) * row.bytes + at;
-        const float wk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wt), k));
+    const long long t0 = (b - zero_units) * kPer + (kBlock ? 0 : (int)threadIdx.x / kLanes);
+    const bool live = t0 < T;
+    const long long t = live ? t0 : 0;
+    const Picks<kLanes> picks(slot_of, t, K, rows_total, live);
+    const int pick = lane & (kLanes - 1);
+    const float wt = topk_w && live && pick < K ? topk_w[t * K + pick] : 0.f;
+    if (picks.bad && at == 0) atomicOr(status, MOE_ERR_BAD_INDEX);
+    float dots = 0.f;   // of pick `pick`
+    for (int c0 = 0; c0 < row.chunks; c0 += kStep * kCh) {
+      int off[kCh];
+      uint4 g[kCh];
+#pragma unroll
+      for (int u = 0; u < kCh; ++u) {
+        const int c = c0 + at + u * kStep;
+        off[u] = row.start(c < row.chunks ? c : 0);
+        if (c0 + u * kStep < row.chunks)
+          g[u] = load_chunk<kAligned, kStream>(dout + t * (long long)row.bytes + off[u], row.bytes);
+      }
+      auto load = [&](int k, uint4 (&v)[kCh]) {
+        const uint8_t* src = y + (long long)picks.of(picks.s, k) * row.bytes;
+#pragma unroll
+        for (int u = 0; u < kCh; ++u)
+          if (c0 + u * kStep < row.chunks)
+            v[u] = load_chunk<kAligned, kStream>(src + off[u], row.bytes);
+      };
+      auto finish = [&](int k, const uint4 (&v)[kCh]) {
+        uint8_t* dst = dy + (long long)picks.of(picks.s, k) * row.bytes;
+        const float wk = picks.of(wt, k);
+        float d = 0.f;
+#pragma unroll
+        for (int u = 0; u < kCh; ++u) {
+          const int c = c0 + at + u * kStep;
+          if (c >= row.chunks) continue;
+          float f[N], e[N];
+          El::unpack(g[u], f);
+          if (dw) {
+            El::unpack(v[u], e);
+            // elements of this chunk that the chunk before it has too
+            const int skip = kAligned ? 0 : (16 * c - off[u]) / El::kSize;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (kAligned || i >= skip) d = fmaf(f[i], e[i], d);
+          }
+          if (dy) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] *= wk;
+            store_chunk<kAligned>(dst + off[u], row.bytes, El::pack(f));
+          }
+        }
         if (dw) {
-          float f[N];
-          El::unpack(load_chunk<kAligned>(y + off, row.bytes), f);
-          float d = 0.f;
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (kAligned || i >= skip) d = fmaf(g[i], f[i], d);
-          d = in ? d : 0.f;
-          for (int o = 32; o >= 1; o >>= 1) d += __shfl_xor(d, o);
-          if (lane == k) dots += d;
+          d = group_sum<kLanes>(d);
+          if (pick == k) dots += d;
         }
-        if (dy && in) {
-          float f[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i) f[i] = wk * g[i];
-          store_chunk<kAligned>(dy + off, row.bytes, El::pack(f));
-        }
+      };
+      for (unsigned long long m = picks.valid; m; m &= m - 1) {
+        const int k = __ffsll((long long)m) - 1;
+        uint4 v[kCh];
+        if (dw) load(k, v);
+        finish(k, v);
       }
     }
-    if (dw) {
+    if (!dw) continue;
+    if constexpr (kBlock) {
       part[wave][lane] = dots;
       __syncthreads();
       if (threadIdx.x < K) {
         float d = 0.f;
 #pragma unroll
-        for (int i = 0; i < kRowWaves; ++i) d += part[i][threadIdx.x];
+        for (int i = 0; i < kWaves; ++i) d += part[i][threadIdx.x];
         dw[t * K + threadIdx.x] = d;
       }
       __syncthreads();
+    } else if (live && pick < K) {
+      dw[t * K + pick] = dots;
     }
   }
 }
@@ -338,8 +427,20 @@ static unsigned grid_for(long long units, int per) {
 
 // Pieces of a row for one wave each, and their length in chunks.
 static void cut(const RowShape& row, int& pieces, int& plen) {
-  pieces = (row.chunks + 64 * kRowChunks - 1) / (64 * kRowChunks);
+  pieces = (row.chunks + 63) / 64;
   plen = (row.chunks + pieces - 1) / pieces;
+}
+
+// Groups of 16 lanes for rows of up to 512 bytes, where a wave would be half
+// idle (60,000 tokens of 130 bf16: combine 32 us with a wave each).
+static bool short_rows(const RowShape& row, int K) { return row.chunks <= 32 && K <= 16; }
+
+// Reading past the caches pays where the rows are more than the memory-side
+// cache holds (256 MB): combine of 2.8 GB 506 us against 534, but of 32 MB
+// 7.1 against 5.9 and of 147 MB 26 against 25, as there the caches may hold
+// what the caller has just written.
+static bool streamed(long long rows_total, const RowShape& row) {
+  return rows_total * row.bytes > (512LL << 20);
 }
 
 // The checks that the four calls share.  Sizes first, then (by the caller)
@@ -368,17 +469,32 @@ template <typename El, bool kWeighted>
 static moe_status_t gather_sum(const void* y, int rows_total, const int32_t* slot_of,
                                const float* topk_w, int T, int K, const RowShape& row, void* out,
                                int32_t* status, hipStream_t st) {
-  int pieces, plen;
-  cut(row, pieces, plen);
-  const dim3 grid(grid_for((long long)T * pieces, kRowWaves)), block(kRowThreads);
+  const dim3 block(kRowThreads);
   const uint8_t* yb = static_cast<const uint8_t*>(y);
   uint8_t* ob = static_cast<uint8_t*>(out);
-  if (wide(row, (uintptr_t)y | (uintptr_t)out))
-    hipLaunchKernelGGL((gather_sum_kernel<El, true, kWeighted>), grid, block, 0, st, yb,
-                       rows_total, slot_of, topk_w, T, K, row, pieces, plen, ob, status);
+  const bool al = wide(row, (uintptr_t)y | (uintptr_t)out);
+  if (short_rows(row, K)) {
+    const dim3 grid(grid_for(T, 4 * kRowWaves));
+    if (al)
+      hipLaunchKernelGGL((gather_sum_kernel<El, 16, 2, true, false, kWeighted>), grid, block, 0,
+                         st, yb, rows_total, slot_of, topk_w, T, K, row, 1, 32, ob, status);
+    else
+      hipLaunchKernelGGL((gather_sum_kernel<El, 16, 2, false, false, kWeighted>), grid, block, 0,
+                         st, yb, rows_total, slot_of, topk_w, T, K, row, 1, 32, ob, status);
+    return launched();
+  }
+  int pieces, plen;
+  cut(row, pieces, plen);
+  const dim3 grid(grid_for((long long)T * pieces, kRowWaves));
+  if (al && streamed(rows_total, row))
+    hipLaunchKernelGGL((gather_sum_kernel<El, 64, 1, true, true, kWeighted>), grid, block, 0, st,
+                       yb, rows_total, slot_of, topk_w, T, K, row, pieces, plen, ob, status);
+  else if (al)
+    hipLaunchKernelGGL((gather_sum_kernel<El, 64, 1, true, false, kWeighted>), grid, block, 0, st,
+                       yb, rows_total, slot_of, topk_w, T, K, row, pieces, plen, ob, status);
   else
-    hipLaunchKernelGGL((gather_sum_kernel<El, false, kWeighted>), grid, block, 0, st, yb,
-                       rows_total, slot_of, topk_w, T, K, row, pieces, plen, ob, status);
+    hipLaunchKernelGGL((gather_sum_kernel<El, 64, 1, false, false, kWeighted>), grid, block, 0, st,
+                       yb, rows_total, slot_of, topk_w, T, K, row, pieces, plen, ob, status);
   return launched();
 }
 
@@ -396,24 +512,50 @@ static moe_status_t gather_sum_any(int dtype, const void* y, int rows_total,
   return gather_sum<F16, kWeighted>(y, rows_total, slot_of, topk_w, T, K, row, out, status, st);
 }
 
+template <typename El, int kLanes, bool kBlock>
+static void launch_combine_grad(bool al, bool stream, const uint8_t* dout, const uint8_t* y,
+                                int rows_total, const int32_t* slot_of, const float* topk_w,
+                                int T, int K, const RowShape& row, uint8_t* dy, float* dw,
+                                const int32_t* row_src, int32_t* status, hipStream_t st) {
+  const int per = kBlock ? 1 : kRowThreads / kLanes;
+  const long long tokens = ((long long)T + per - 1) / per;
+  auto run = [&](auto aligned, auto past) {
+    constexpr int kThreads = grad_threads(kBlock, aligned.value);
+    const long long zero = row_src && dy ? ((long long)rows_total + kThreads - 1) / kThreads : 0;
+    hipLaunchKernelGGL((combine_grad_kernel<El, kLanes, kBlock, aligned.value, past.value>),
+                       dim3(grid_for(zero + tokens, 1)), dim3(kThreads), 0, st, dout, y,
+                       rows_total, slot_of, topk_w, T, K, row, dy, dw, row_src, zero, status);
+  };
+  if (al && stream)
+    run(std::true_type(), std::true_type());
+  else if (al)
+    run(std::true_type(), std::false_type());
+  else
+    run(std::false_type(), std::false_type());
+}
+
+// A workgroup per token for rows past 256 chunks (4 KB), else a wave, or 16
+// lanes for short rows.
 template <typename El>
 static moe_status_t combine_grad(const void* dout, const void* y, int rows_total,
                                  const int32_t* slot_of, const float* topk_w, int T, int K,
                                  const RowShape& row, void* dy, float* dw,
                                  const int32_t* row_src, int32_t* status, void* stream) {
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const long long zero = row_src && dy ? ((long long)rows_total + 64 * kRowWaves - 1) /
-                                             (64 * kRowWaves) : 0;
-  const dim3 grid(grid_for(zero + T, 1)), block(kRowThreads);
   const uint8_t* db = static_cast<const uint8_t*>(dout);
   const uint8_t* yb = static_cast<const uint8_t*>(y);
   uint8_t* gb = static_cast<uint8_t*>(dy);
-  if (wide(row, (uintptr_t)dout | (uintptr_t)y | (uintptr_t)dy))
-    hipLaunchKernelGGL((combine_grad_kernel<El, true>), grid, block, 0, st, db, yb, rows_total,
-                       slot_of, topk_w, T, K, row, gb, dw, row_src, zero, status);
+  const bool al = wide(row, (uintptr_t)dout | (uintptr_t)y | (uintptr_t)dy);
+  const bool past = streamed(rows_total, row);
+  if (short_rows(row, K))
+    launch_combine_grad<El, 16, false>(al, false, db, yb, rows_total, slot_of, topk_w, T, K, row,
+                                       gb, dw, row_src, status, st);
+  else if (row.chunks <= 256)
+    launch_combine_grad<El, 64, false>(al, past, db, yb, rows_total, slot_of, topk_w, T, K, row,
+                                       gb, dw, row_src, status, st);
   else
-    hipLaunchKernelGGL((combine_grad_kernel<El, false>), grid, block, 0, st, db, yb, rows_total,
-                       slot_of, topk_w, T, K, row, gb, dw, row_src, zero, status);
+    launch_combine_grad<El, 64, true>(al, past, db, yb, rows_total, slot_of, topk_w, T, K, row,
+                                      gb, dw, row_src, status, st);
   return launched();
 }
 
@@ -432,21 +574,29 @@ extern "C" moe_status_t moe_permute_rows(const void* x, int dtype, int T, int K,
   if (!status_dev || (T > 0 && (!x || !slot_of)) || (rows_total > 0 && !a))
     return MOE_INVALID_ARG;
   if (((uintptr_t)x | (uintptr_t)a) & (type_size(dtype) - 1)) return MOE_UNSUPPORTED_SHAPE;
-  int pieces, plen;
-  cut(row, pieces, plen);
+  const bool few = short_rows(row, K);
+  int pieces = 1, plen = 32;
+  if (!few) cut(row, pieces, plen);
   const long long zero = row_src ? ((long long)rows_total + 63) / 64 : 0;
-  const long long units = zero + (long long)T * pieces;
+  const long long units = zero + (few ? ((long long)T + 3) / 4 : (long long)T * pieces);
   if (units == 0) return MOE_OK;
   const dim3 grid(grid_for(units, kRowWaves)), block(kRowThreads);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const uint8_t* xb = static_cast<const uint8_t*>(x);
   uint8_t* ab = static_cast<uint8_t*>(a);
-  if (wide(row, (uintptr_t)x | (uintptr_t)a))
-    hipLaunchKernelGGL((permute_rows_kernel<true>), grid, block, 0, st, xb, slot_of, T, K, row,
-                       pieces, plen, rows_total, ab, row_src, zero, status_dev);
+  const bool al = wide(row, (uintptr_t)x | (uintptr_t)a);
+  if (few && al)
+    hipLaunchKernelGGL((permute_rows_kernel<16, 2, true>), grid, block, 0, st, xb, slot_of, T, K,
+                       row, pieces, plen, rows_total, ab, row_src, zero, status_dev);
+  else if (few)
+    hipLaunchKernelGGL((permute_rows_kernel<16, 2, false>), grid, block, 0, st, xb, slot_of, T, K,
+                       row, pieces, plen, rows_total, ab, row_src, zero, status_dev);
+  else if (al)
+    hipLaunchKernelGGL((permute_rows_kernel<64, 1, true>), grid, block, 0, st, xb, slot_of, T, K,
+                       row, pieces, plen, rows_total, ab, row_src, zero, status_dev);
   else
-    hipLaunchKernelGGL((permute_rows_kernel<false>), grid, block, 0, st, xb, slot_of, T, K, row,
-                       pieces, plen, rows_total, ab, row_src, zero, status_dev);
+    hipLaunchKernelGGL((permute_rows_kernel<64, 1, false>), grid, block, 0, st, xb, slot_of, T, K,
+                       row, pieces, plen, rows_total, ab, row_src, zero, status_dev);
   return launched();
 }
 

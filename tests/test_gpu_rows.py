@@ -26,7 +26,8 @@ U = 2.0 ** -24
 SHAPES = [
     (1, 1, 1, 1, 0, 128), (1, 8, 8, 7168, 0, 1024), (3, 2, 2, 5, 0, 256), (64, 2, 4, 256, 0, 636),
     (77, 3, 5, 509, 0, 900), (200, 4, 6, 1000, 1, 40), (33, 8, 9, 7168, 0, 1500),
-    (5, 64, 70, 130, 0, 9100), (130, 5, 300, 9, 1, 3), (19, 2, 3, 4099, 0, 30), (0, 3, 4, 64, 0, 16),
+    (5, 64, 70, 130, 0, 9100), (77, 16, 40, 130, 0, 6000), (78, 17, 40, 40, 0, 6000), (301, 4, 6, 2048, 0, 2000),
+    (20, 3, 4, 18000, 0, 600), (130, 5, 300, 9, 1, 3), (19, 2, 3, 4099, 0, 30), (0, 3, 4, 64, 0, 16),
 ]
 IDS = ["x".join(map(str, s)) for s in SHAPES]
 
@@ -206,8 +207,10 @@ def test_rows(gpu, shape, dt, offset):
     near(dy.cpu()[live], ref, ref.abs(), 1, t, "dy")
     assert dy.cpu()[empty].isnan().all()
     dots, mag = (g64[:, None] * rows64).sum(-1), (g64[:, None] * rows64).abs().sum(-1)
-    # a lane's chunk (at most 8 products), 6 levels of lanes, passes, 4 waves
-    near(dw, dots, mag, 8 + 6 + -(-H // 512) + 4, torch.float32, "dw")
+    # a lane's products of one part of a row (at most 2 chunks of 8), 6 levels
+    # of lanes, the parts (a wave's 128 chunks of a row of up to 256, or a
+    # workgroup's 512, of at least 4), 8 waves
+    near(dw, dots, mag, 16 + 6 + 2 + -(-H // 2048) + 8, torch.float32, "dw")
     dy2, dw2 = out(R, H), torch.full((T, K), float("nan"), device="cuda")
     fre.moe_combine_rows_grad(gd, y, slot, wd, dy2, None, st, row_src=srcd)
     fre.moe_combine_rows_grad(gd, y, slot, wd, None, dw2, st)
