@@ -33,6 +33,7 @@ constexpr int kLayoutRounds = 4;
 constexpr int kChunk = kLayoutThreads * kLayoutRounds;   // flat entries per block
 constexpr int kWaves = kLayoutThreads / 64;
 constexpr int kScanThreads = 1024;
+constexpr int kOneRows = 4096;         // rows one block clears beside ranking a chunk
 constexpr long long kFoldMax = 8192;   // chunk x expert counts a rank block sums itself
 
 // Lanes of the wave whose key equals this lane's (ballots over the key bits).
@@ -166,6 +167,11 @@ __global__ __launch_bounds__(kScanThreads) void layout_scan(
 // Each block sums the chunk counts itself -- all of them for the expert
 // totals and segment starts, those of the earlier chunks for its own bases
 // -- and block 0 writes counts and offsets; the values equal layout_scan's.
+//
+// kOne (one chunk, launched as one block, fold != 0): neither is layout_count
+// launched.  The block counts its own entries and clears row_src / row_expert
+// itself, so that a decode step's sort is one launch.
+template <bool kOne>
 __global__ __launch_bounds__(kLayoutThreads) void layout_rank(
     const int32_t* __restrict__ idx, long long F, int K, int E, int key_bits,
     int layout, int rows_total, int cap, int32_t* __restrict__ offsets,
@@ -179,6 +185,13 @@ __global__ __launch_bounds__(kLayoutThreads) void layout_rank(
   int32_t* offs = wcnt + kWaves * E;  // [E] segment starts
   int32_t* tot = offs + E;          // [E] expert totals (fold)
   __shared__ long long wsum[kWaves];
+  int bad = 0;
+  if constexpr (kOne) {
+    for (int i = threadIdx.x; i < rows_total; i += blockDim.x) {
+      row_src[i] = -1;
+      row_expert[i] = -1;
+    }
+  }
   for (int i = threadIdx.x; i < E; i += blockDim.x) {
     if (fold) {
       run[i] = 0;
@@ -190,11 +203,25 @@ __global__ __launch_bounds__(kLayoutThreads) void layout_rank(
     for (int w = 0; w < kWaves; ++w) wcnt[w * E + i] = 0;
   }
   __syncthreads();
+  if constexpr (kOne) {   // layout_count's histogram, of the whole problem
+    const unsigned long long below = (1ull << (threadIdx.x & 63)) - 1ull;
+#pragma unroll
+    for (int r = 0; r < kLayoutRounds; ++r) {
+      const long long f = r * kLayoutThreads + threadIdx.x;
+      const int e = f < F ? idx[f] : -1;
+      const bool valid = e >= 0 && e < E;
+      if (!valid && e != -1) bad = 1;
+      const unsigned long long m = match_key(valid ? e + 1 : 0, key_bits);
+      if (valid && (m & below) == 0) atomicAdd(&tot[e], __popcll(m));
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) atomicOr(status, MOE_ERR_BAD_EXPERT);
+  }
   if (fold) {
     // kLayoutThreads / E threads per expert, each summing a strided share of
     // the chunks in registers, then one LDS add each
     const int tpe = kLayoutThreads / E;
-    if ((int)threadIdx.x < tpe * E) {
+    if (!kOne && (int)threadIdx.x < tpe * E) {
       const int e = threadIdx.x % E;
       int sum = 0, before = 0;
       for (int c = threadIdx.x / E; c < nchunks; c += tpe) {
@@ -453,18 +480,27 @@ static void launch_index(const int32_t* topk_idx, int T, int K, int E, int layou
   int32_t* chunk_base = chunk_counts + (nc < 1 ? 1 : nc) * E;
   const int cap = layout == MOE_LAYOUT_MASKED ? rows : 0;
 
+  const int fold = nc > 0 && E <= kLayoutThreads && nc * (long long)E <= kFoldMax;
+  const size_t rank_lds = (3 + kWaves) * E * sizeof(int32_t);
+  // one chunk, and no more rows to clear than one block does in passing
+  if (nc == 1 && fold && rows_total <= kOneRows) {
+    hipLaunchKernelGGL((layout_rank<true>), dim3(1), dim3(kLayoutThreads), rank_lds, st, topk_idx,
+                       F, K, E, key_bits_for(E), layout, rows_total, cap, offsets, chunk_base,
+                       slot_of, row_src, row_expert, status_dev, fold, chunk_counts, 1, align_m,
+                       counts);
+    return;
+  }
   const int ncl = (int)(nc < 1 ? 1 : nc);   // count always runs: it also clears row_src
   hipLaunchKernelGGL(layout_count, dim3((unsigned)ncl), dim3(kLayoutThreads),
                      E * sizeof(int32_t), st, topk_idx, F, E, key_bits_for(E), chunk_counts,
                      row_src, row_expert, rows_total, status_dev);
   // few chunks: the rank blocks compute the scan themselves (one launch less)
-  const int fold = nc > 0 && E <= kLayoutThreads && nc * (long long)E <= kFoldMax;
   if (!fold)
     hipLaunchKernelGGL(layout_scan, dim3(1), dim3(kScanThreads), 0, st, chunk_counts, ncl, E,
                        scan_group(E), layout, align_m, cap, chunk_base, counts, offsets);
   if (nc > 0)
-    hipLaunchKernelGGL(layout_rank, dim3((unsigned)nc), dim3(kLayoutThreads),
-                       (3 + kWaves) * E * sizeof(int32_t), st, topk_idx, F, K,
+    hipLaunchKernelGGL((layout_rank<false>), dim3((unsigned)nc), dim3(kLayoutThreads),
+                       rank_lds, st, topk_idx, F, K,
                        E, key_bits_for(E), layout, rows_total, cap,
                        offsets, chunk_base, slot_of, row_src, row_expert,
                        status_dev, fold, chunk_counts, ncl, align_m, counts);
