@@ -122,7 +122,8 @@ DENSE = [(1, 16, 16), (1, 128, 128), (2, 4096, 7168), (3, 48, 80), (16, 272, 144
          (33, 7168, 2048), (64, 144, 4112), (65, 144, 4112), (130, 144, 4112), (300, 256, 256),
          (257, 528, 1040), (700, 1040, 7168), (1500, 768, 16), (8448, 1296, 272), (8200, 4096, 384),
          (32, 16400, 48), (31, 6160, 80), (96, 7168, 2048), (200, 7168, 272), (1000, 4096, 400), (2400, 4096, 144),
-         (2048, 4096, 1040), (2048, 4112, 128), (40, 16384, 656), (129, 80, 896)]
+         (2048, 4096, 1040), (2048, 4112, 128), (40, 16384, 656), (129, 80, 896), (16640, 4096, 256), (16400, 4112, 128),
+         (12300, 4096, 144)]
 
 
 @pytest.mark.parametrize("shape", DENSE, ids=["x".join(map(str, s)) for s in DENSE])
@@ -160,7 +161,8 @@ GROUPED = [(1, 16, 16, [1], 0, 0), (4, 128, 256, [3, 0, 130, 1], 5, 7), (3, 272,
            (70, 64, 48, None, 0, 3), (300, 32, 32, None, 2, 0), (3, 4096, 400, [2900, 1, 2700], 60, 0),
            (2, 784, 7168, [513, 700], 0, 0), (16, 4096, 4112, [40, 0, 64, 65, 128, 1, 17, 90] * 2, 3, 0),
            (40, 2064, 272, [20, 33, 0, 1, 31] * 8, 0, 0), (4, 4096, 256, [600, 640, 580, 700], 10, 0),
-           (3, 1040, 144, [300, 200, 129], 0, 5)]
+           (3, 1040, 144, [300, 200, 129], 0, 5), (3, 4096, 384, [2900, 1, 2700], 60, 0),
+           (3, 4096, 128, [5900, 0, 6100], 1, 9), (70, 256, 128, [260] * 70, 0, 0)]
 
 
 def segments(shape):
@@ -308,6 +310,54 @@ def test_linear(gpu, shape, dt):
     assert torch.equal(c.cpu()[fine], two.cpu()[fine])
     s64 = exact_scale(x[fine].double().abs().amax(1))
     check(c.cpu()[fine], exact_codes(x[fine].double(), s64), s64, w, sw, f"linear {shape} {dt}")
+
+
+@pytest.mark.parametrize("M", [1, 3, 20, 100, 700])
+def test_linear_captured(gpu, M):
+    """Replayed with other inputs and with eager calls between."""
+    N, K = 528, 1040
+    w = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda")
+    sw = torch.rand(N, device="cuda") / 100
+    x, c = torch.randn(M, K, device="cuda").bfloat16(), torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(fre.moe_linear_int8_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    fre.moe_linear_int8(x, w, sw, c, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fre.moe_linear_int8(x, w, sw, c, ws)
+    for _ in range(4):
+        x.copy_(torch.randn(M, K, device="cuda"))
+        fre.moe_linear_int8(x, w, sw, c, ws)
+        want = c.clone()
+        c.fill_(7)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c, want)
+
+
+def test_two_linears_at_once(gpu):
+    """On two streams, with workspaces of their own, each repeated."""
+    N, K, M = 4096, 2048, 300
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    w = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda")
+    sw = torch.rand(N, device="cuda") / 100
+    xs = [torch.randn(M, K, device="cuda").half() for _ in range(2)]
+    n = fre.moe_linear_int8_workspace_bytes(M, K)
+    wss = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cs = [torch.zeros(6, M, N, dtype=torch.float16, device="cuda") for _ in range(2)]
+    want = []
+    for x, ws in zip(xs, wss):
+        c = torch.zeros(M, N, dtype=torch.float16, device="cuda")
+        fre.moe_linear_int8(x, w, sw, c, ws)
+        want.append(c)
+    torch.cuda.synchronize()
+    for i in range(6):
+        for x, ws, c, s in zip(xs, wss, cs, streams):
+            fre.moe_linear_int8(x, w, sw, c[i], ws, stream=s)
+    torch.cuda.synchronize()
+    for c, v in zip(cs, want):
+        assert all(torch.equal(c[i], v) for i in range(6))
 
 
 # ------------------------------------------------------------- the layer
