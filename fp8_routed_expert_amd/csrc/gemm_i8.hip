@@ -377,7 +377,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
   // short (kLateSw) the channels' only after it, under the next tile's search.
   auto load_sa = [&](const Tile&) __attribute__((always_inline)) {
     const long long rows = kGather ? p.src_rows : rows_total;
-    const Rsrc ra = buffer(p.a_scale, (uint32_t)(rows * 4 > 0x7ffff000LL ? 0x7ffff000LL : rows * 4));
+    const Rsrc ra = buffer(p.a_scale, (uint32_t)(rows * 4));   // (the host bounds the rows)
 #pragma unroll
     for (int i = 0; i < MI; ++i)
       sa[i] = __int_as_float((int)__builtin_amdgcn_raw_buffer_load_b32(
@@ -446,9 +446,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void grouped_gemm_i8_ke
       for (int s = 0; s < 2; ++s) {
         const int row = top + (r16 & 7) + 8 * s;
         if constexpr (kPersist) {
-          const uint32_t at = row < t.row_end && n < N
-                                  ? ((uint32_t)(row - t.row0) * (uint32_t)N + (uint32_t)(n - t.n0)) * 2u
-                                  : kNowhere;
+          const uint32_t in =
+              ((uint32_t)(row - t.row0) * (uint32_t)N + (uint32_t)(n - t.n0)) * 2u;
+          const uint32_t at = row < t.row_end && n < N ? in : kNowhere;
           __builtin_amdgcn_raw_buffer_store_b128(s ? second : first, rc, (int)at, 0, 2);   // nt
         } else if (row < t.row_end && n < N) {
           u32x4* c4 = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.c) + (size_t)row * N + n);
@@ -617,6 +617,7 @@ static moe_status_t product_args(const I8Args& p, bool grouped) {
   if (p.rows_total > 0 && ((!p.a_scale && !(p.row_src && p.src_rows == 0)) || !p.c))
     return MOE_INVALID_ARG;
   if (((uintptr_t)p.a | (uintptr_t)p.w | (uintptr_t)p.c) & 15) return MOE_UNSUPPORTED_SHAPE;
+  if (((uintptr_t)p.a_scale | (uintptr_t)p.w_scale) & 3) return MOE_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }
 

@@ -561,6 +561,7 @@ extern "C" moe_status_t moe_sort_tokens(const int32_t* topk_idx, int T, int K, i
       check_routing(topk_idx, T, K, E, layout, align_m, rows, counts, offsets, slot_of, row_src,
                     row_expert, workspace, workspace_bytes, status_dev, &rows_total);
   if (ok != MOE_OK) return ok;
+  if ((uintptr_t)workspace & 3) return MOE_UNSUPPORTED_SHAPE;
   launch_index(topk_idx, T, K, E, layout, align_m, rows, (int)rows_total, counts, offsets,
                slot_of, row_src, row_expert, workspace, status_dev,
                reinterpret_cast<hipStream_t>(stream));

@@ -5,11 +5,13 @@
 //   s = fp32(max_j |v_j| / 127), 1 for a row of zeros, at least 2^-126
 //   q_j = the integer nearest v_j / s, ties to even
 //
-// A wave per row (no barrier) or the four waves of a workgroup.  The first kKeep slices of eight values that a
-// lane takes stay in its registers between the row's maximum and the codes;
-// the others of a row past 8192 values are read (and the activation computed)
-// again, from the cache.  Reads 2 (or 4) bytes and writes one per value:
-// bound by HBM bandwidth.
+// A wave per row (no barrier) or the four waves of a workgroup.  The first
+// kKeep slices of eight values that a lane takes stay in its registers between
+// the row's maximum and the codes; the others of a longer row are read (and
+// the activation computed) again, from the cache.  Reads 2 (or 4) bytes and
+// writes one per value: bound by HBM bandwidth (65536 rows of 7168 bf16 270 us,
+// 5.2 TB/s; 16384 of 4096 5.6; the activation of 131072 rows of 2 x 2048 250 us,
+// 5.4 TB/s).
 #include "rows_i8.hpp"
 
 namespace moe {

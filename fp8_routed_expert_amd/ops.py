@@ -387,28 +387,29 @@ def _type(t, name, bytes_too=False):
     return code
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# torch's own accessors without their Python layers: a call on a few rows takes
+# as long as its checks
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _functions = {}
 
 
-def _arg(t, dtypes, name, shape=None):
-    """_ptr with its checks in the order of their cost: a call on a few rows
-    takes as long as its checks."""
-    if t.is_cuda and t.dtype in dtypes and t.is_contiguous() and (shape is None or t.shape == shape):
+def _arg(t, dtypes, name, dev, shape=None):
+    """t's pointer, if it is a contiguous tensor of the right type and shape
+    on device `dev`."""
+    if (t.get_device() == dev >= 0 and t.dtype in dtypes and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
         return t.data_ptr()
-    return _ptr(t, dtypes, name, shape)   # names what is wrong
+    _ptr(t, dtypes, name, shape)   # names what is wrong
+    raise ValueError(f"{name}: on {t.device}, the call's first tensor on device {dev}")
 
 
-def _call(name, stream, tensors, *args):
-    """Calls library function `name` on the device that the tensors share
-    (which need not be the current one), on `stream` or that device's
-    current stream."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
+def _call(name, stream, dev, *args):
+    """Calls library function `name` on device `dev` (which need not be the
+    current one), on `stream` or that device's current stream."""
     if stream is None:
-        stream = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+        stream = _raw_stream(dev)
     elif isinstance(stream, torch.cuda.Stream):
         if stream.device.index != dev:
             raise ValueError(f"{name}: tensors on device {dev}, stream on {stream.device}")
@@ -416,7 +417,7 @@ def _call(name, stream, tensors, *args):
     fn = _functions.get(name)
     if fn is None:
         fn = _functions[name] = getattr(load(), name)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -425,10 +426,16 @@ def _call(name, stream, tensors, *args):
         check(st, name)
 
 
+_INT_MAX = 0x7fffffff
+
+
 def _matrix(t, name):
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name}: must have two dimensions, has {t.dim()}")
-    return t.shape
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX:
+        raise ValueError(f"{name}: shape {tuple(shape)} past {_INT_MAX}")
+    return shape
 
 
 def moe_sort_tokens(topk_idx, E, layout, align_m, rows, counts, offsets, slot_of, row_src,
@@ -439,14 +446,15 @@ def moe_sort_tokens(topk_idx, E, layout, align_m, rows, counts, offsets, slot_of
     moe_layout_workspace_bytes(T, K, E) bytes."""
     T, K = _matrix(topk_idx, "topk_idx")
     rows_total = E * rows if layout == LAYOUT_MASKED else rows
-    _call("moe_sort_tokens", stream,
-          (topk_idx, counts, offsets, slot_of, row_src, row_expert, workspace, status),
-          _arg(topk_idx, _I32, "topk_idx"), T, K, E, layout, align_m, rows,
-          _arg(counts, _I32, "counts", (E,)), _arg(offsets, _I32, "offsets", (E + 1,)),
-          _arg(slot_of, _I32, "slot_of", (T, K)), _arg(row_src, _I32, "row_src", (rows_total,)),
-          _arg(row_expert, _I32, "row_expert", (rows_total,)),
-          _arg(workspace, (torch.uint8,), "workspace"), workspace.numel(),
-          _arg(status, _I32, "status", (1,)))
+    dev = topk_idx.get_device()
+    _call("moe_sort_tokens", stream, dev,
+          _arg(topk_idx, _I32, "topk_idx", dev), T, K, E, layout, align_m, rows,
+          _arg(counts, _I32, "counts", dev, (E,)), _arg(offsets, _I32, "offsets", dev, (E + 1,)),
+          _arg(slot_of, _I32, "slot_of", dev, (T, K)),
+          _arg(row_src, _I32, "row_src", dev, (rows_total,)),
+          _arg(row_expert, _I32, "row_expert", dev, (rows_total,)),
+          _arg(workspace, (torch.uint8,), "workspace", dev), workspace.numel(),
+          _arg(status, _I32, "status", dev, (1,)))
 
 
 def moe_permute_rows(x, slot_of, a, status, row_src=None, stream=None):
@@ -458,11 +466,11 @@ def moe_permute_rows(x, slot_of, a, status, row_src=None, stream=None):
     K = _matrix(slot_of, "slot_of")[1]
     R = _matrix(a, "a")[0]
     code = _type(x, "x", True)
-    ts = (x, slot_of, a, status) + (() if row_src is None else (row_src,))
-    _call("moe_permute_rows", stream, ts, _arg(x, (x.dtype,), "x"), code, T, K, H,
-          _arg(slot_of, _I32, "slot_of", (T, K)), R, _arg(a, (x.dtype,), "a", (R, H)),
-          None if row_src is None else _arg(row_src, _I32, "row_src", (R,)),
-          _arg(status, _I32, "status", (1,)))
+    dev = x.get_device()
+    _call("moe_permute_rows", stream, dev, _arg(x, (x.dtype,), "x", dev), code, T, K, H,
+          _arg(slot_of, _I32, "slot_of", dev, (T, K)), R, _arg(a, (x.dtype,), "a", dev, (R, H)),
+          None if row_src is None else _arg(row_src, _I32, "row_src", dev, (R,)),
+          _arg(status, _I32, "status", dev, (1,)))
 
 
 def moe_permute_rows_grad(da, slot_of, dx, status, stream=None):
@@ -471,9 +479,10 @@ def moe_permute_rows_grad(da, slot_of, dx, status, stream=None):
     R, H = _matrix(da, "da")
     T, K = _matrix(slot_of, "slot_of")
     code = _type(da, "da")
-    _call("moe_permute_rows_grad", stream, (da, slot_of, dx, status),
-          _arg(da, (da.dtype,), "da"), code, R, _arg(slot_of, _I32, "slot_of"), T, K, H,
-          _arg(dx, (da.dtype,), "dx", (T, H)), _arg(status, _I32, "status", (1,)))
+    dev = da.get_device()
+    _call("moe_permute_rows_grad", stream, dev,
+          _arg(da, (da.dtype,), "da", dev), code, R, _arg(slot_of, _I32, "slot_of", dev), T, K, H,
+          _arg(dx, (da.dtype,), "dx", dev, (T, H)), _arg(status, _I32, "status", dev, (1,)))
 
 
 def moe_combine_rows(y, slot_of, topk_w, out, status, stream=None):
@@ -482,10 +491,12 @@ def moe_combine_rows(y, slot_of, topk_w, out, status, stream=None):
     R, H = _matrix(y, "y")
     T, K = _matrix(slot_of, "slot_of")
     code = _type(y, "y")
-    _call("moe_combine_rows", stream, (y, slot_of, topk_w, out, status),
-          _arg(y, (y.dtype,), "y"), code, R, _arg(slot_of, _I32, "slot_of"),
-          _arg(topk_w, _F32, "topk_w", (T, K)), T, K, H, _arg(out, (y.dtype,), "out", (T, H)),
-          _arg(status, _I32, "status", (1,)))
+    dev = y.get_device()
+    _call("moe_combine_rows", stream, dev,
+          _arg(y, (y.dtype,), "y", dev), code, R, _arg(slot_of, _I32, "slot_of", dev),
+          _arg(topk_w, _F32, "topk_w", dev, (T, K)), T, K, H,
+          _arg(out, (y.dtype,), "out", dev, (T, H)),
+          _arg(status, _I32, "status", dev, (1,)))
 
 
 def moe_combine_rows_grad(dout, y, slot_of, topk_w, dy, dtopk_w, status, row_src=None,
@@ -500,14 +511,15 @@ def moe_combine_rows_grad(dout, y, slot_of, topk_w, dy, dtopk_w, status, row_src
     code = _type(dout, "dout")
     if dy is None and dtopk_w is None:
         raise ValueError("moe_combine_rows_grad: neither dy nor dtopk_w is given")
-    given = [t for t in (dy, dtopk_w, row_src) if t is not None]
-    _call("moe_combine_rows_grad", stream, (dout, y, slot_of, topk_w, status, *given),
-          _arg(dout, (dout.dtype,), "dout"), _arg(y, (dout.dtype,), "y", (R, H)), code, R,
-          _arg(slot_of, _I32, "slot_of", (T, K)), _arg(topk_w, _F32, "topk_w", (T, K)), T, K, H,
-          None if dy is None else _arg(dy, (dout.dtype,), "dy", (R, H)),
-          None if dtopk_w is None else _arg(dtopk_w, _F32, "dtopk_w", (T, K)),
-          None if row_src is None else _arg(row_src, _I32, "row_src", (R,)),
-          _arg(status, _I32, "status", (1,)))
+    dev = dout.get_device()
+    _call("moe_combine_rows_grad", stream, dev,
+          _arg(dout, (dout.dtype,), "dout", dev), _arg(y, (dout.dtype,), "y", dev, (R, H)),
+          code, R, _arg(slot_of, _I32, "slot_of", dev, (T, K)),
+          _arg(topk_w, _F32, "topk_w", dev, (T, K)), T, K, H,
+          None if dy is None else _arg(dy, (dout.dtype,), "dy", dev, (R, H)),
+          None if dtopk_w is None else _arg(dtopk_w, _F32, "dtopk_w", dev, (T, K)),
+          None if row_src is None else _arg(row_src, _I32, "row_src", dev, (R,)),
+          _arg(status, _I32, "status", dev, (1,)))
 
 
 # ---- products in 8-bit integers, one scale per token and one per channel
@@ -521,8 +533,11 @@ def moe_quantize_int8(x, q, scale, stream=None):
     channels of weights [N, K] or [E, N, K] (scale then [E, N])."""
     cols = x.shape[-1]
     rows = x.numel() // cols if cols else 0
-    _call("moe_quantize_int8", stream, (x, q, scale), _arg(x, _FLOATS, "x"), _type(x, "x"), rows,
-          cols, _arg(q, _I8, "q", x.shape), _arg(scale, _F32, "scale", x.shape[:-1]))
+    if rows > _INT_MAX:
+        raise ValueError(f"moe_quantize_int8: {rows} rows, at most {_INT_MAX}")
+    dev = x.get_device()
+    _call("moe_quantize_int8", stream, dev, _arg(x, _FLOATS, "x", dev), _type(x, "x"), rows,
+          cols, _arg(q, _I8, "q", dev, x.shape), _arg(scale, _F32, "scale", dev, x.shape[:-1]))
 
 
 def moe_gemm_int8(a, a_scale, w, w_scale, c, stream=None):
@@ -530,9 +545,10 @@ def moe_gemm_int8(a, a_scale, w, w_scale, c, stream=None):
     int8, scaled by a_scale [M] and w_scale [N]."""
     M, K = _matrix(a, "a")
     N = _matrix(w, "w")[0]
-    _call("moe_gemm_int8", stream, (a, a_scale, w, w_scale, c), _arg(a, _I8, "a"),
-          _arg(a_scale, _F32, "a_scale", (M,)), _arg(w, _I8, "w", (N, K)),
-          _arg(w_scale, _F32, "w_scale", (N,)), M, N, K, _arg(c, _FLOATS, "c", (M, N)),
+    dev = a.get_device()
+    _call("moe_gemm_int8", stream, dev, _arg(a, _I8, "a", dev),
+          _arg(a_scale, _F32, "a_scale", dev, (M,)), _arg(w, _I8, "w", dev, (N, K)),
+          _arg(w_scale, _F32, "w_scale", dev, (N,)), M, N, K, _arg(c, _FLOATS, "c", dev, (M, N)),
           _type(c, "c"))
 
 
@@ -546,10 +562,12 @@ def moe_linear_int8(x, w, w_scale, c, workspace, stream=None):
     moe_linear_int8_workspace_bytes(M, K) bytes."""
     M, K = _matrix(x, "x")
     N = _matrix(w, "w")[0]
-    _call("moe_linear_int8", stream, (x, w, w_scale, c, workspace), _arg(x, _FLOATS, "x"),
-          _type(x, "x"), _arg(w, _I8, "w", (N, K)), _arg(w_scale, _F32, "w_scale", (N,)), M, N, K,
-          _arg(c, _FLOATS, "c", (M, N)), _type(c, "c"),
-          _arg(workspace, (torch.uint8,), "workspace"), workspace.numel())
+    dev = x.get_device()
+    _call("moe_linear_int8", stream, dev, _arg(x, _FLOATS, "x", dev),
+          _type(x, "x"), _arg(w, _I8, "w", dev, (N, K)),
+          _arg(w_scale, _F32, "w_scale", dev, (N,)), M, N, K,
+          _arg(c, _FLOATS, "c", dev, (M, N)), _type(c, "c"),
+          _arg(workspace, (torch.uint8,), "workspace", dev), workspace.numel())
 
 
 def _experts(w):
@@ -563,11 +581,13 @@ def moe_grouped_gemm_int8(a, a_scale, w, w_scale, offsets, counts, c, status, st
     by a_scale [rows_total] and w_scale [E, N]; c float32, bfloat16 or float16."""
     E, N, K = _experts(w)
     R = _matrix(a, "a")[0]
-    _call("moe_grouped_gemm_int8", stream, (a, a_scale, w, w_scale, offsets, counts, c, status),
-          _arg(a, _I8, "a", (R, K)), _arg(a_scale, _F32, "a_scale", (R,)), _arg(w, _I8, "w"),
-          _arg(w_scale, _F32, "w_scale", (E, N)), _arg(offsets, _I32, "offsets", (E + 1,)),
-          _arg(counts, _I32, "counts", (E,)), E, R, N, K, _arg(c, _FLOATS, "c", (R, N)),
-          _type(c, "c"), _arg(status, _I32, "status", (1,)))
+    dev = a.get_device()
+    _call("moe_grouped_gemm_int8", stream, dev,
+          _arg(a, _I8, "a", dev, (R, K)), _arg(a_scale, _F32, "a_scale", dev, (R,)),
+          _arg(w, _I8, "w", dev), _arg(w_scale, _F32, "w_scale", dev, (E, N)),
+          _arg(offsets, _I32, "offsets", dev, (E + 1,)),
+          _arg(counts, _I32, "counts", dev, (E,)), E, R, N, K, _arg(c, _FLOATS, "c", dev, (R, N)),
+          _type(c, "c"), _arg(status, _I32, "status", dev, (1,)))
 
 
 def moe_grouped_gemm_int8_gather(x, x_scale, row_src, w, w_scale, offsets, counts, c, status,
@@ -577,13 +597,14 @@ def moe_grouped_gemm_int8_gather(x, x_scale, row_src, w, w_scale, offsets, count
     E, N, K = _experts(w)
     T = _matrix(x, "x")[0]
     R = row_src.numel()
-    _call("moe_grouped_gemm_int8_gather", stream,
-          (x, x_scale, row_src, w, w_scale, offsets, counts, c, status),
-          _arg(x, _I8, "x", (T, K)), _arg(x_scale, _F32, "x_scale", (T,)), T,
-          _arg(row_src, _I32, "row_src", (R,)), _arg(w, _I8, "w"),
-          _arg(w_scale, _F32, "w_scale", (E, N)), _arg(offsets, _I32, "offsets", (E + 1,)),
-          _arg(counts, _I32, "counts", (E,)), E, R, N, K, _arg(c, _FLOATS, "c", (R, N)),
-          _type(c, "c"), _arg(status, _I32, "status", (1,)))
+    dev = x.get_device()
+    _call("moe_grouped_gemm_int8_gather", stream, dev,
+          _arg(x, _I8, "x", dev, (T, K)), _arg(x_scale, _F32, "x_scale", dev, (T,)), T,
+          _arg(row_src, _I32, "row_src", dev, (R,)), _arg(w, _I8, "w", dev),
+          _arg(w_scale, _F32, "w_scale", dev, (E, N)),
+          _arg(offsets, _I32, "offsets", dev, (E + 1,)),
+          _arg(counts, _I32, "counts", dev, (E,)), E, R, N, K, _arg(c, _FLOATS, "c", dev, (R, N)),
+          _type(c, "c"), _arg(status, _I32, "status", dev, (1,)))
 
 
 def moe_act_requant_int8(h, offsets, counts, q, q_scale, status, stream=None):
@@ -592,11 +613,13 @@ def moe_act_requant_int8(h, offsets, counts, q, q_scale, status, stream=None):
     R, I2 = _matrix(h, "h")
     I = I2 // 2
     E = counts.numel()
-    _call("moe_act_requant_int8", stream, (h, offsets, counts, q, q_scale, status),
-          _arg(h, _FLOATS, "h", (R, 2 * I)), _type(h, "h"),
-          _arg(offsets, _I32, "offsets", (E + 1,)), _arg(counts, _I32, "counts", (E,)), E, R, I,
-          _arg(q, _I8, "q", (R, I)), _arg(q_scale, _F32, "q_scale", (R,)),
-          _arg(status, _I32, "status", (1,)))
+    dev = h.get_device()
+    _call("moe_act_requant_int8", stream, dev,
+          _arg(h, _FLOATS, "h", dev, (R, 2 * I)), _type(h, "h"),
+          _arg(offsets, _I32, "offsets", dev, (E + 1,)), _arg(counts, _I32, "counts", dev, (E,)),
+          E, R, I,
+          _arg(q, _I8, "q", dev, (R, I)), _arg(q_scale, _F32, "q_scale", dev, (R,)),
+          _arg(status, _I32, "status", dev, (1,)))
 
 
 def moe_ceiling_copy(src, dst, stream=None):

@@ -526,7 +526,8 @@ moe_status_t moe_combine_rows_grad(const void* dout, const void* y, int dtype, i
  * N, K, I and cols must be multiples of 16, K at most 131056 (so that no sum
  * overflows), T * K of the gathered call below 0x7ffff000 (one buffer
  * descriptor), M, T and rows of a product at most 0x1ffffc00:
- * MOE_UNSUPPORTED_SHAPE otherwise.  Matrices 16-byte aligned.  offsets / counts / status_dev as for
+ * MOE_UNSUPPORTED_SHAPE otherwise.  Matrices and the workspace 16-byte
+ * aligned, scales 4-byte.  offsets / counts / status_dev as for
  * moe_grouped_gemm_fp8.  Outputs may not overlap inputs.
  */
 moe_status_t moe_quantize_int8(const void* x, int dtype, int rows, int cols, int8_t* q,

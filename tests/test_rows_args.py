@@ -26,6 +26,7 @@ def test_sort_tokens_refusals():
         assert call(**bad) == 1, bad
     assert call(layout=1, E=1024, rows=1 << 21, wsb=1 << 24) == 2      # rows past 2^31
     assert call(T=1 << 30, K=2, wsb=1 << 62) == 2                      # picks past 2^31
+    assert call(ws=ODD) == 2
 
 
 def test_permute_rows_refusals():
