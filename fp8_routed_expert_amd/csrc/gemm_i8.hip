@@ -575,7 +575,9 @@ static moe_status_t product_i8(const I8Args& p, hipStream_t st) {
   auto tiles = [&](int bm, int bn) {
     return p.E * ((rows + bm - 1) / bm) * ((p.N + bn - 1) / bn);
   };
-  if (rows <= 16) return launch_skinny<1, 1>(p, st);
+  // (a launch holds 2^32 threads: past 2^22 tiles of 16 x 16 larger ones follow)
+  if (rows <= 16 && tiles(16, 16) + (p.N + 15) / 16 * (long long)p.E < (1 << 22))
+    return launch_skinny<1, 1>(p, st);
   if (rows <= 32 && (p.E == 1 || tiles(64, 64) <= 240))
     return (long long)p.E * p.N >= 192 * 32 ? launch_skinny<2, 2>(p, st)
                                             : launch_skinny<2, 1>(p, st);

@@ -48,8 +48,9 @@ __global__ __launch_bounds__(kQThreads) void quant_int8_kernel(
       segments_bad(offsets, counts, E, threadIdx.x) && threadIdx.x == 0)
     atomicOr(status, MOE_ERR_BAD_INDEX);
   const int j0 = kWaves == 1 ? (threadIdx.x & 63) * 8 : threadIdx.x * 8;
-  for (int row = blockIdx.x * kRows + (kWaves == 1 ? wave : 0); row < rows;
-       row += gridDim.x * kRows) {
+  for (long long at = (long long)blockIdx.x * kRows + (kWaves == 1 ? wave : 0); at < rows;
+       at += (long long)gridDim.x * kRows) {
+    const int row = (int)at;
     // all loads first (lanes past the row read its first slice again); the
     // search for the row's segment runs while they are in flight
     float v[kKeep][8];

@@ -93,4 +93,6 @@ def permute_tokens(x, table):
 def combine_tokens(y, topk_w, table):
     """out [T, H] = sum_k topk_w[t, k] * y[slot_of[t, k]]; gradients for y
     (zero in the rows that no token has) and topk_w (float32 [T, K])."""
+    if y.shape[0] != table.rows_total:
+        raise ValueError(f"y: {y.shape[0]} rows, the table's buffer has {table.rows_total}")
     return _Combine.apply(y, topk_w, table)

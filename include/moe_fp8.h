@@ -522,7 +522,8 @@ moe_status_t moe_combine_rows_grad(const void* dout, const void* y, int dtype, i
  *   c    [rows, N] of c_type;  x, h of `dtype`
  *   dtype, c_type  MOE_TYPE_F32, _BF16 or _F16
  *   workspace  moe_linear_int8_workspace_bytes(M, K) bytes; what the call
- *              leaves there is unspecified
+ *              leaves there is unspecified.  Calls (or captured graphs) that
+ *              may run at the same time need one each.
  * N, K, I and cols must be multiples of 16, K at most 131056 (so that no sum
  * overflows), T * K of the gathered call below 0x7ffff000 (one buffer
  * descriptor), M, T and rows of a product at most 0x1ffffc00:

@@ -450,6 +450,33 @@ def test_differentiable_routing(gpu, dt):
     assert ((wd.grad.cpu().double() - w64.grad).abs() <= (1.1 * u + 20 * U) * mag + 1e-7).all()
 
 
+def test_rows_that_are_not_the_tables(gpu):
+    idx = torch.zeros(3, 1, dtype=torch.int32, device="cuda")
+    tab = fre.sort_tokens(idx, 1, 256)
+    with pytest.raises(ValueError, match="256"):
+        fre.combine_tokens(torch.zeros(255, 4, device="cuda"), torch.ones(3, 1, device="cuda"), tab)
+    with pytest.raises(ValueError):
+        fre.permute_tokens(torch.zeros(4, 4, device="cuda"), tab)
+
+
+def test_more_tiles_than_a_launch_holds(gpu):
+    """1024 experts of one row with 131,072 channels: past 2^22 tiles of 16."""
+    E, N, K = 1024, 131072, 16
+    g = np.random.default_rng(9)
+    w = torch.zeros(E, N, K, dtype=torch.int8, device="cuda")
+    a, sa, sw = codes(g, E, K), scales(g, E), scales(g, N)
+    sws = sw.cuda().expand(E, N).contiguous()
+    offs = torch.arange(E + 1, dtype=torch.int32, device="cuda")
+    c, st = torch.full((E, N), 77.0, dtype=torch.bfloat16, device="cuda"), i32(1)
+    picked = {e: codes(g, N, K) for e in (0, 511, 1023)}
+    for e, v in picked.items():
+        w[e] = v.cuda()
+    fre.moe_grouped_gemm_int8(a.cuda(), sa.cuda(), w, sws, offs, torch.ones(E, dtype=torch.int32, device="cuda"), c, st)
+    for e, v in picked.items():
+        check(c[e:e + 1].cpu(), a[e:e + 1], sa[e:e + 1], v, sw, f"expert {e}")
+    assert int((c != 0).any(1).sum()) == 3 and int(st) == 0
+
+
 def test_only_one_gradient(gpu):
     """Weights or rows alone; an expanded gradient; a table sorted in between."""
     idx = torch.tensor([[0, 1], [1, -1], [-1, -1]], dtype=torch.int32, device="cuda")
