@@ -101,9 +101,10 @@ static void launch_quant(const void* x, int rows, int cols, uint8_t* q, float* s
                          const int32_t* offsets, const int32_t* counts, int E, int32_t* status,
                          hipStream_t st) {
   // a wave per row where the lanes of four would idle, or where there are
-  // enough rows to fill the CUs (8191 rows of 2048: 15.4 us against 17.0 with
-  // four waves; 96 rows: 7.1 against 3.9, all latency)
-  const bool one = cols <= 512 || (cols <= kKeep * 64 * 8 && rows > 3072);
+  // enough rows to fill the CUs (bf16, 8191 rows of 2048: 11.5 us against 12.8
+  // with four waves, 2048 rows 4.5 against 5.0; 96 rows 3.7 against 2.9, all
+  // latency; 8191 rows of 1024 6.1 against 10.5, 96 rows 3.0 against 2.9)
+  const bool one = cols <= 1024 || (cols <= kKeep * 64 * 8 && rows > 1536);
   const long long blocks = one ? ((long long)rows + 3) / 4 : rows;
   const dim3 grid((unsigned)(blocks < (1 << 22) ? blocks : (1 << 22))), block(kQThreads);
   if (one)

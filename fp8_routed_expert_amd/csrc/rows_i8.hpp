@@ -53,35 +53,25 @@ __device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
 
 // Eight codes.  v * inv + 1.5 * 2^23 rounds to an integer whose two's
 // complement is in the low bits.  Where a residual reaches half a step (a tie,
-// or a quotient so near one that inv's rounding shows) an integer may have to
-// move: ties are checked first, as a row whose scale is a power of two has
-// many and they are right already.
+// or a quotient so near one that inv's rounding shows) the integer moves
+// towards the residual if twice its magnitude is past s, or is s and the
+// integer odd: as bit patterns of positive floats, |2d| + odd > s.  (bf16
+// rows have ties often: with branches for each kind of move 16384 rows of 1024
+// took 14.8 us against 11.3.)
 __device__ __forceinline__ uint2 int8_codes(const float (&v)[8], float s, float inv) {
   constexpr float kShift = 12582912.f;
-  float t[8], far = 0.f;
+  float t[8], d[8], far = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     t[i] = fmaf(v[i], inv, kShift);
-    far = fmaxf(far, fabsf(fmaf(kShift - t[i], s, v[i])));
+    d[i] = fmaf(kShift - t[i], s, v[i]);
+    far = fmaxf(far, fabsf(d[i]));
   }
   if (far + far >= s) {
-    bool wrong = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float d = fabsf(fmaf(kShift - t[i], s, v[i]));
-      wrong |= d + d > s || (d + d == s && (__float_as_uint(t[i]) & 1u) != 0);
-    }
-    if (wrong) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q = t[i] - kShift;
-        const float d = fmaf(-q, s, v[i]), d2 = d + d;
-        const bool odd = (__float_as_uint(t[i]) & 1u) != 0;
-        if (d2 > s || (d2 == s && odd))
-          t[i] = q + 1.f + kShift;
-        else if (d2 < -s || (d2 == -s && odd))
-          t[i] = q - 1.f + kShift;
-      }
+      const uint32_t d2 = __float_as_uint(fabsf(d[i] + d[i])) + (__float_as_uint(t[i]) & 1u);
+      t[i] += d2 > __float_as_uint(s) ? copysignf(1.f, d[i]) : 0.f;
     }
   }
   uint32_t w[2];
@@ -103,10 +93,18 @@ __device__ __forceinline__ uint32_t max_bits(const float (&v)[8], uint32_t top) 
   return top;
 }
 
-// The largest of a wave's values, in every lane.
+// The largest of a wave's values, in every lane: within rows of 16 lanes by
+// moves that need no LDS, then across the four rows.
 __device__ __forceinline__ uint32_t wave_max(uint32_t top) {
-  for (int o = 32; o >= 1; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-  return top;
+  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xb1, 0xf, 0xf, true));
+  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4e, 0xf, 0xf, true));
+  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x141, 0xf, 0xf, true));
+  top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x140, 0xf, 0xf, true));
+  const uint32_t a = __builtin_amdgcn_readlane((int)top, 0);
+  const uint32_t b = __builtin_amdgcn_readlane((int)top, 16);
+  const uint32_t c = __builtin_amdgcn_readlane((int)top, 32);
+  const uint32_t e = __builtin_amdgcn_readlane((int)top, 48);
+  return max(max(a, b), max(c, e));
 }
 
 }  // namespace moe
