@@ -9,9 +9,11 @@
 // kKeep slices of eight values that a lane takes stay in its registers between
 // the row's maximum and the codes; the others of a longer row are read (and
 // the activation computed) again, from the cache.  Reads 2 (or 4) bytes and
-// writes one per value: bound by HBM bandwidth (65536 rows of 7168 bf16 270 us,
-// 5.2 TB/s; 16384 of 4096 5.6; the activation of 131072 rows of 2 x 2048 250 us,
-// 5.4 TB/s).
+// writes one per value: bound by HBM bandwidth (65536 rows of 7168 bf16 250 us,
+// 5.6 TB/s; 16384 of 4096 5.9; the activation of 131072 rows of 2 x 2048 220 us,
+// 6.1 TB/s).
+#include <type_traits>
+
 #include "rows_i8.hpp"
 
 namespace moe {
@@ -20,22 +22,22 @@ constexpr int kQThreads = 256;
 constexpr int kKeep = 4;
 
 // kAct: v = silu(h[j]) * h[cols + j] of a row [2 cols]; else the row itself.
-template <int kType, bool kAct>
+template <int kType, bool kAct, bool kStream>
 __device__ __forceinline__ void row_slice(const void* x, size_t row, int cols, int j,
                                           float (&v)[8]) {
   if constexpr (kAct) {
     float g[8], u[8];
-    load8_as(kType, x, row * (size_t)(2 * (long long)cols) + j, g);
-    load8_as(kType, x, row * (size_t)(2 * (long long)cols) + cols + j, u);
+    load8_as<kStream>(kType, x, row * (size_t)(2 * (long long)cols) + j, g);
+    load8_as<kStream>(kType, x, row * (size_t)(2 * (long long)cols) + cols + j, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = silu_mul(g[i], u[i]);
   } else {
-    load8_as(kType, x, row * (size_t)cols + j, v);
+    load8_as<kStream>(kType, x, row * (size_t)cols + j, v);
   }
 }
 
-// kWaves: waves per row (1 or 4).
-template <int kType, bool kAct, int kWaves>
+// kWaves: waves per row (1 or 4); kStream: the rows are read past the caches.
+template <int kType, bool kAct, int kWaves, bool kStream>
 __global__ __launch_bounds__(kQThreads) void quant_int8_kernel(
     const void* __restrict__ x, int rows, int cols, uint8_t* __restrict__ q,
     float* __restrict__ scale, const int32_t* __restrict__ offsets,
@@ -57,7 +59,7 @@ __global__ __launch_bounds__(kQThreads) void quant_int8_kernel(
 #pragma unroll
     for (int u = 0; u < kKeep; ++u) {
       const int j = u * kStep + j0;
-      if (u * kStep < cols) row_slice<kType, kAct>(x, row, cols, j < cols ? j : 0, v[u]);
+      if (u * kStep < cols) row_slice<kType, kAct, kStream>(x, row, cols, j < cols ? j : 0, v[u]);
     }
     if (kAct && !row_valid(offsets, counts, E, rows, row)) continue;   // the same for the row
     uint32_t top = 0;
@@ -66,7 +68,7 @@ __global__ __launch_bounds__(kQThreads) void quant_int8_kernel(
       if (u * kStep < cols) top = max_bits(v[u], top);
     for (int j = kKeep * kStep + j0; j < cols; j += kStep) {
       float t[8];
-      row_slice<kType, kAct>(x, row, cols, j, t);
+      row_slice<kType, kAct, kStream>(x, row, cols, j, t);
       top = max_bits(t, top);
     }
     top = wave_max(top);
@@ -90,7 +92,7 @@ __global__ __launch_bounds__(kQThreads) void quant_int8_kernel(
     }
     for (int j = kKeep * kStep + j0; j < cols; j += kStep) {
       float t[8];
-      row_slice<kType, kAct>(x, row, cols, j, t);
+      row_slice<kType, kAct, kStream>(x, row, cols, j, t);
       *reinterpret_cast<uint2*>(out + j) = fine ? int8_codes(t, s, inv) : make_uint2(0, 0);
     }
   }
@@ -107,12 +109,25 @@ static void launch_quant(const void* x, int rows, int cols, uint8_t* q, float* s
   const bool one = cols <= 1024 || (cols <= kKeep * 64 * 8 && rows > 1536);
   const long long blocks = one ? ((long long)rows + 3) / 4 : rows;
   const dim3 grid((unsigned)(blocks < (1 << 22) ? blocks : (1 << 22))), block(kQThreads);
-  if (one)
-    hipLaunchKernelGGL((quant_int8_kernel<kType, kAct, 1>), grid, block, 0, st, x, rows, cols, q,
-                       scale, offsets, counts, E, status);
+  // Past the caches where h is more than the memory-side cache (256 MB) holds:
+  // 131072 rows of 2 x 2048 220 us against 254, but 16384 34 against 31.  (The
+  // plain rows gain nothing: 65536 of 7168 bf16 254 against 248.  Codes stored
+  // past the caches cost the product that reads them next more than they give.)
+  const bool past = kAct && 2LL * rows * cols * (kType == MOE_TYPE_F32 ? 4 : 2) > (512LL << 20);
+  auto run = [&](auto waves, auto stream) {
+    hipLaunchKernelGGL((quant_int8_kernel<kType, kAct, waves.value, stream.value>), grid, block, 0,
+                       st, x, rows, cols, q, scale, offsets, counts, E, status);
+  };
+  using One = std::integral_constant<int, 1>;
+  using Four = std::integral_constant<int, 4>;
+  if (past && one)
+    run(One(), std::integral_constant<bool, kAct>());
+  else if (past)
+    run(Four(), std::integral_constant<bool, kAct>());
+  else if (one)
+    run(One(), std::false_type());
   else
-    hipLaunchKernelGGL((quant_int8_kernel<kType, kAct, 4>), grid, block, 0, st, x, rows, cols, q,
-                       scale, offsets, counts, E, status);
+    run(Four(), std::false_type());
 }
 
 template <bool kAct>

@@ -18,27 +18,35 @@
 
 namespace moe {
 
-// Eight consecutive values of type `dtype` from element `at`.
+// Eight consecutive values of type `dtype` from element `at`; kStream: past the
+// caches.
+template <bool kStream = false>
 __device__ __forceinline__ void load8_as(int dtype, const void* x, size_t at, float (&v)[8]) {
   if (dtype == MOE_TYPE_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    typedef float f4 __attribute__((ext_vector_type(4)));
+    const f4* p = reinterpret_cast<const f4*>(static_cast<const float*>(x) + at);
+    const f4 a = kStream ? __builtin_nontemporal_load(p) : p[0];
+    const f4 b = kStream ? __builtin_nontemporal_load(p + 1) : p[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
     return;
   }
-  const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  const u4* p = reinterpret_cast<const u4*>(static_cast<const uint16_t*>(x) + at);
+  const u4 a = kStream ? __builtin_nontemporal_load(p) : *p;
   if (dtype == MOE_TYPE_F16) {
     typedef _Float16 h8 __attribute__((ext_vector_type(8)));
     const h8 h = __builtin_bit_cast(h8, a);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
   } else {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_to_f32(w[i] & 0xffffu);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      v[2 * i] = bf16_to_f32(a[i] & 0xffffu);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
     }
   }
 }

@@ -276,6 +276,29 @@ def test_act_corrupt_table(gpu):
     assert int(st) == fre.ERR_BAD_INDEX
 
 
+@pytest.mark.parametrize("rows,I,dt", [(66000, 2048, "bf16"), (16500, 8208, "f16"), (66000, 1040, "f32"),
+                                       (8300, 8208, "f32")])
+def test_act_of_many_rows(gpu, rows, I, dt):
+    """An h larger than the caches is read past them, with the same bits as
+    its parts; rows behind the last segment are left as they were."""
+    h = torch.randn(rows, 2 * I, device="cuda").to(TYPES[dt])
+    end = rows - 7
+
+    def act(lo, hi):
+        q = torch.full((hi - lo, I), 99, dtype=torch.int8, device="cuda")
+        s, st = torch.full((hi - lo,), 99.0, device="cuda"), i32(1)
+        fre.moe_act_requant_int8(h[lo:hi], torch.tensor([0, hi - lo], dtype=torch.int32).cuda(),
+                                 torch.tensor([min(hi, end) - lo], dtype=torch.int32).cuda(), q, s, st)
+        assert int(st) == 0
+        return q, s
+
+    q, s = act(0, rows)
+    cuts = [0, rows // 5, rows // 2, rows * 3 // 4, rows]
+    parts = [act(lo, hi) for lo, hi in zip(cuts, cuts[1:])]
+    assert torch.equal(q, torch.cat([p[0] for p in parts])) and torch.equal(s, torch.cat([p[1] for p in parts]))
+    assert (q[end:] == 99).all() and (s[end:] == 99).all()
+
+
 # ------------------------------------------------------------- linear
 LINEAR = [(1, 16, 16), (1, 4096, 7168), (2, 256, 128), (4, 272, 400), (5, 144, 2064), (8, 512, 7168), (16, 1040, 1040),
           (17, 64, 64), (40, 7168, 2048), (96, 528, 2048), (300, 272, 1040), (1, 48, 20000), (3, 32, 131056),
