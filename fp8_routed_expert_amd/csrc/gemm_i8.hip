@@ -549,14 +549,22 @@ static moe_status_t launch_skinny(const I8Args& p, hipStream_t st) {
 
 // Launches the product in tiles chosen from the sizes alone (the same inside
 // graph capture).  `rows` is a dense product's, or a segment's on average.
-// Times are of products whose weights come from HBM, 4096 x 7168 and
-// 7168 x 2048 (N x K), in us.
+// Times are of products whose weights come from HBM, N x K (experts x N x K),
+// in us.
 //
-//   * Up to 16 rows, and up to 32 where the tiles below would be few: the
-//     kernel that takes the weights straight to registers (1 row: 8.1 and
-//     6.2; as 64 x 128 tiles 46 and 17.  32 rows: 15.2 and 7.9.  Past 32 its
-//     repeated reads of the rows cost more than tiles do: 96 rows 23 and 13
-//     against 18 and 9).
+//   * Few rows: the kernel that takes the weights straight to registers, up to
+//     16 rows (1 row of 4096 x 7168 and 7168 x 2048: 8.0 and 6.1; as 64 x 128
+//     tiles 46 and 17), and up to 32 (with more than 8 rows) where the tiles
+//     below would be few (32 rows: 15.2 and 7.9; 8192 x 8192 21.2 both ways, 16384 x
+//     7168 33.0 against 25.3).  Its workgroups take 16 channels, or 32 where
+//     there are enough of them and each has more to do than to stream (search
+//     its segment, read rows, start on a short K): 32 x 4096 x 7168 of 16 rows
+//     177 against 219, 16 rows of 32768 x 4096 31.5 against 36.0; but 1 row
+//     28.0 against 26.4, and 4096 x 7168, too few, 11.5 against 8.0.
+//     Where even those are short-lived and many, 64 x 128 tiles: 32 x 7168 x
+//     2048 of 16 rows 97 against 124, 64 x 7168 x 3584 296 against 388, one
+//     row of 65536 x 1024 15.9 against 17.7; but 32 x 4096 x 4096 132 against
+//     124, one row of 152064 x 2048 65 against 52.
 //   * One round of small tiles, loaded five steps ahead: 64 x 64 (128 rows:
 //     20.4 and 9.6; two and three stages of 64 x 128 tiles 45 and 17), then
 //     128 x 64 (512 and 256 rows: 27 and 11.5; 64 x 64 tiles 41 and 17), then
@@ -567,21 +575,29 @@ static moe_status_t launch_skinny(const I8Args& p, hipStream_t st) {
 //     have 256 rows: twice the work per byte of two 128 x 128 tiles (prefill
 //     gate/up 3.27 ms against 4.32).  192 x 256 where both fit one round (the
 //     EP72 share's gate/up: 67 against 78).
-//   * else 128 x 128, two workgroups to a CU; 64 x 128 for segments of up to
-//     128 rows where K is short (masked decode, K = 2048: 97 against 107; at
-//     K = 7168 203 against 172).
+//   * else 64 x 128 up to 64 rows (32 x 4096 x 7168: 170 against 195, 64 x
+//     7168 x 3584 302 against 337), and 128 x 128, two workgroups to a CU (segments
+//     of 48 to 96 rows, 32 x 7168 x 2048: 111 against 143, as 64 rows do not
+//     hold them; half empty ones 107 against 97).
 static moe_status_t product_i8(const I8Args& p, hipStream_t st) {
   const long long rows = ((long long)p.rows_total + p.E - 1) / p.E;
+  const bool grouped = p.offsets != nullptr;
   auto tiles = [&](int bm, int bn) {
     return p.E * ((rows + bm - 1) / bm) * ((p.N + bn - 1) / bn);
   };
-  // (a launch holds 2^32 threads: past 2^22 tiles of 16 x 16 larger ones follow)
-  if (rows <= 16 && tiles(16, 16) + (p.N + 15) / 16 * (long long)p.E < (1 << 22))
-    return launch_skinny<1, 1>(p, st);
-  if (rows <= 32 && (p.E == 1 || tiles(64, 64) <= 240))
+  const long long slices = (long long)p.E * ((p.N + 15) / 16);   // of 16 channels
+  const long long wide = (long long)p.E * ((p.N + 127) / 128);
+  if (rows <= 16 && wide > 256 &&
+      (p.K <= 1024 || (grouped && (p.K <= 2048 || wide > 1024))))
+    return launch_i8<64, 128, 32, 64, 4>(p, st);
+  // (a launch holds 2^32 threads: past 2^21 slices tiles follow)
+  if (rows <= 16 && slices < (1 << 21) && (rows <= 8 || grouped || tiles(64, 64) <= 128))
+    return slices >= 448 && (grouped || rows > 4 || p.K <= 1024) ? launch_skinny<1, 2>(p, st)
+                                                                 : launch_skinny<1, 1>(p, st);
+  if (rows <= 32 && tiles(64, 64) <= 128)
     return (long long)p.E * p.N >= 192 * 32 ? launch_skinny<2, 2>(p, st)
                                             : launch_skinny<2, 1>(p, st);
-  if (tiles(64, 64) <= 240) return launch_i8<64, 64, 32, 64, 4, 6>(p, st);
+  if (tiles(64, 64) <= 256) return launch_i8<64, 64, 32, 64, 4, 6>(p, st);
   if (tiles(128, 64) <= 256) return launch_i8<128, 64, 32, 64, 4, 6>(p, st);
   if (tiles(128, 128) <= 256) return launch_i8<128, 128, 64, 64, 4, 3>(p, st);
   if (rows >= 256 && tiles(256, 256) > 128) {
@@ -594,7 +610,7 @@ static moe_status_t product_i8(const I8Args& p, hipStream_t st) {
       return launch_i8<256, 256, 128, 64, 2, 0, true>(p, st);
     return launch_i8<256, 256, 128, 64, 2>(p, st);
   }
-  if (rows <= 128 && p.K <= 4096) return launch_i8<64, 128, 32, 64, 4>(p, st);
+  if (rows <= 64) return launch_i8<64, 128, 32, 64, 4>(p, st);
   return launch_i8<128, 128, 64, 64, 4>(p, st);
 }
 
@@ -671,9 +687,14 @@ extern "C" size_t moe_linear_int8_workspace_bytes(int M, int K) {
   return codes + (size_t)M * sizeof(float);
 }
 
-// One launch for at most this many rows.
-static bool one_launch(int M, int K) {
-  return M <= kLinearRows && (long long)M * (K + 16) <= 61440;   // of 64 KB
+// One launch for few rows, and no more channels than three workgroups to a CU
+// have: later workgroups would quantise the rows again with no weights under way
+// (us, weights from HBM, one launch against two; 1 row of 4096 x 7168 (N x K)
+// 8.5 : 11.7, 4 rows 10.6 : 12.7; 12288 x 4096 15.0 : 15.3, 16384 x 4096
+// 19.5 : 18.5, 32768 x 1024 19.4 : 13.8, 152064 x 2048 97 : 54).
+static bool one_launch(int M, int N, int K) {
+  return M <= kLinearRows && N <= 3 * 256 * 16 &&
+         (long long)M * (K + 16) <= 61440;   // of 64 KB
 }
 
 static moe_status_t linear_in_one(const void* x, int dtype, const int8_t* w, const float* w_scale,
@@ -710,7 +731,7 @@ extern "C" moe_status_t moe_linear_int8(const void* x, int dtype, const int8_t* 
     return MOE_INVALID_ARG;
   if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)c | (uintptr_t)workspace) & 15)
     return MOE_UNSUPPORTED_SHAPE;
-  if (one_launch(M, K))
+  if (one_launch(M, N, K))
     return linear_in_one(x, dtype, w, w_scale, M, N, K, c, c_type,
                          reinterpret_cast<hipStream_t>(stream));
   int8_t* q = static_cast<int8_t*>(workspace);

@@ -212,6 +212,27 @@ def test_grouped(gpu, shape, gather):
         assert not (got[written] == 77).all(-1).any()
 
 
+# Few rows with many channels, or of many experts: the tiles' borders.
+FEW = [(9, 7184, 272), (7, 7184, 1040), (3, 16400, 144), (2, 33040, 1040), (16, 16400, 2064), (20, 16384, 144),
+       (5, 40016, 256), (30, 8208, 144), (64, 16400, 144), (100, 33040, 80)]
+
+
+@pytest.mark.parametrize("shape", FEW, ids=["x".join(map(str, s)) for s in FEW])
+def test_gemm_of_few_rows(gpu, shape):
+    test_gemm(gpu, shape)
+
+
+FEW_EACH = [(20, 1040, 144, None, 1, 0), (40, 1040, 144, None, 0, 2), (520, 144, 2064, None, 0, 3),
+            (30, 272, 144, [16, 0, 9] * 10, 0, 0), (24, 272, 2064, [2, 1, 0] * 8, 0, 1), (70, 1040, 144, [64, 33] * 35, 0, 0),
+            (70, 1040, 128, [70, 96] * 35, 1, 0)]
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["plain", "gather"])
+@pytest.mark.parametrize("shape", FEW_EACH, ids=["x".join(map(str, s[:3])) for s in FEW_EACH])
+def test_grouped_of_few_rows(gpu, shape, gather):
+    test_grouped(gpu, shape, gather)
+
+
 @pytest.mark.parametrize("R", [300, 5000])
 def test_grouped_clipped_and_corrupt_tables(gpu, R):
     """Counts past their segment or the buffer are clipped; a table that is
@@ -303,6 +324,13 @@ def test_act_of_many_rows(gpu, rows, I, dt):
 LINEAR = [(1, 16, 16), (1, 4096, 7168), (2, 256, 128), (4, 272, 400), (5, 144, 2064), (8, 512, 7168), (16, 1040, 1040),
           (17, 64, 64), (40, 7168, 2048), (96, 528, 2048), (300, 272, 1040), (1, 48, 20000), (3, 32, 131056),
           (4, 16, 15344), (1, 32, 61424), (1, 32, 61440), (3, 272, 208)]
+
+
+@pytest.mark.parametrize("shape", [(1, 12288, 256), (1, 12304, 256), (3, 40016, 144), (17, 40016, 48)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_linear_of_many_channels(gpu, shape):
+    """Either side of the channels that one launch takes."""
+    test_linear(gpu, shape, "bf16")
 
 
 @pytest.mark.parametrize("dt", list(TYPES))
