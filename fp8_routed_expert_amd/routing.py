@@ -11,7 +11,9 @@ All calls run on the current stream of the tensors' device.  sort_tokens
 allocates its table, so a table that a backward pass still needs is not
 overwritten by the next one.  Nothing is read back: the calls can be captured
 in a graph (table.status then tells, after a replay, of bad ids and dropped
-rows).
+rows).  As with every captured backward pass, free the eager passes over the
+same leaves first: an accumulation that belongs to another stream's pass ends
+the capture and the process.
 """
 
 import torch

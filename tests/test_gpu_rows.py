@@ -369,6 +369,43 @@ def test_captured_step(gpu, dt):
     assert int(st) == 0
 
 
+def test_captured_autograd(gpu):
+    """The differentiable calls, forward and backward in one graph (gradients
+    asked for by name, so that no leaf accumulates), against eager passes."""
+    T, K, E, H = 300, 3, 5, 264
+    R = T * K + 127 * E
+    torch.manual_seed(8)
+    idx = torch.from_numpy(routing(T, K, E, seed=1)[0]).cuda()
+    x = torch.randn(T, H, device="cuda", requires_grad=True)
+    w = torch.rand(T, K, device="cuda", requires_grad=True)
+    g = torch.randn(T, H, device="cuda")
+
+    def step():
+        t = fre.sort_tokens(idx, E, R)
+        out = fre.combine_tokens(fre.permute_tokens(x, t) * 1.5, w, t)
+        return (out.detach(), *torch.autograd.grad(out, (x, w), g), t.status)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for n in range(4):
+        idx.copy_(torch.from_numpy(routing(T, K, E, seed=10 + n)[0]))
+        with torch.no_grad():
+            for v in (x, w, g):
+                v.copy_(torch.randn_like(v))
+        want = [v.clone() for v in step()]
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_two_streams_at_once(gpu):
     """Two calls that share nothing but the library, on two streams."""
     res, keep = [], []
