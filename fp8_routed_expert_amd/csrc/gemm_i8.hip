@@ -556,7 +556,7 @@ static moe_status_t launch_skinny(const I8Args& p, hipStream_t st) {
 //     16 rows (1 row of 4096 x 7168 and 7168 x 2048: 8.0 and 6.1; as 64 x 128
 //     tiles 46 and 17), and up to 32 (with more than 8 rows) where the tiles
 //     below would be few (32 rows: 15.2 and 7.9; 8192 x 8192 21.2 both ways, 16384 x
-//     7168 33.0 against 25.3).  Its workgroups take 16 channels, or 32 where
+//     7168 33.0 against 23.2).  Its workgroups take 16 channels, or 32 where
 //     there are enough of them and each has more to do than to stream (search
 //     its segment, read rows, start on a short K): 32 x 4096 x 7168 of 16 rows
 //     177 against 219, 16 rows of 32768 x 4096 31.5 against 36.0; but 1 row
