@@ -573,8 +573,13 @@ static moe_status_t launch_skinny(const I8Args& p, hipStream_t st) {
 //     whatever it runs, so as many of them as possible have to share the bytes.
 //   * 256 x 256 once that gives more than half the CUs a tile and segments
 //     have 256 rows: twice the work per byte of two 128 x 128 tiles (prefill
-//     gate/up 3.27 ms against 4.32).  192 x 256 where both fit one round (the
-//     EP72 share's gate/up: 67 against 78).
+//     gate/up 3.27 ms against 4.32); and from 128 rows where those would take
+//     more than a round (32 x 4096 x 7168 of 256 rows 329 against 383, 8 x 7168
+//     x 2048 of 200 33.6 against 44.3; masked segments of capacity 192 win a
+//     third when 80% full, 31 against 43, and lose it when 30% full, 30
+//     against 23).  192 x 256 where both fit one round and
+//     K is long (the EP72 share's gate/up: 67 against 78; but 1536 rows of
+//     7168 x 2048 35.9 against 27.8).
 //   * else 64 x 128 up to 64 rows (32 x 4096 x 7168: 170 against 195, 64 x
 //     7168 x 3584 302 against 337), and 128 x 128, two workgroups to a CU (segments
 //     of 48 to 96 rows, 32 x 7168 x 2048: 111 against 143, as 64 rows do not
@@ -597,11 +602,20 @@ static moe_status_t product_i8(const I8Args& p, hipStream_t st) {
   if (rows <= 32 && tiles(64, 64) <= 128)
     return (long long)p.E * p.N >= 192 * 32 ? launch_skinny<2, 2>(p, st)
                                             : launch_skinny<2, 1>(p, st);
-  if (tiles(64, 64) <= 256) return launch_i8<64, 64, 32, 64, 4, 6>(p, st);
-  if (tiles(128, 64) <= 256) return launch_i8<128, 64, 32, 64, 4, 6>(p, st);
-  if (tiles(128, 128) <= 256) return launch_i8<128, 128, 64, 64, 4, 3>(p, st);
-  if (rows >= 256 && tiles(256, 256) > 128) {
-    if (tiles(192, 256) <= 256) return launch_i8<192, 256, 96, 64, 2>(p, st);
+  // (segments differ and end anywhere in a tile: half a tile more each, on
+  // average, once they are nearly as long as one; those of a buffer that is as
+  // many whole tiles per expert are taken to be its parts)
+  auto ragged = [&](int bm, int bn) {
+    return !grouped || 4 * rows <= 3 * bm || p.rows_total % ((long long)p.E * bm) == 0
+               ? tiles(bm, bn)
+               : (p.E * (2 * rows + bm) + 2 * bm - 1) / (2 * bm) * ((p.N + bn - 1) / bn);
+  };
+  if (ragged(64, 64) <= 256) return launch_i8<64, 64, 32, 64, 4, 6>(p, st);
+  if (ragged(128, 64) <= 256) return launch_i8<128, 64, 32, 64, 4, 6>(p, st);
+  if (ragged(128, 128) <= 256) return launch_i8<128, 128, 64, 64, 4, 3>(p, st);
+  if ((rows >= 256 && tiles(256, 256) > 128) ||
+      (grouped && rows > 128 && ragged(128, 128) > 512)) {
+    if (p.K > 4096 && ragged(192, 256) <= 256) return launch_i8<192, 256, 96, 64, 2>(p, st);
     // walked by one workgroup per CU where the kernel's counted loads and
     // stores allow (down products 2.7% faster: 1826 us against 1877, 113
     // against 115; long K 1%)
