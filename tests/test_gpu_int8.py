@@ -224,7 +224,8 @@ def test_gemm_of_few_rows(gpu, shape):
 
 FEW_EACH = [(20, 1040, 144, None, 1, 0), (40, 1040, 144, None, 0, 2), (520, 144, 2064, None, 0, 3),
             (30, 272, 144, [16, 0, 9] * 10, 0, 0), (24, 272, 2064, [2, 1, 0] * 8, 0, 1), (70, 1040, 144, [64, 33] * 35, 0, 0),
-            (70, 1040, 128, [70, 96] * 35, 1, 0)]
+            (70, 1040, 128, [70, 96] * 35, 1, 0), (40, 1040, 144, [150, 190, 129, 0] * 10, 3, 0),
+            (40, 1040, 256, [150, 250, 129, 256] * 10, 0, 9)]
 
 
 @pytest.mark.parametrize("gather", [False, True], ids=["plain", "gather"])
