@@ -156,7 +156,8 @@ using namespace moe;
 extern "C" moe_status_t moe_quantize_int8(const void* x, int dtype, int rows, int cols, int8_t* q,
                                           float* scale, void* stream) {
   if (!float_type(dtype) || rows < 0 || cols <= 0) return MOE_INVALID_ARG;
-  if (cols % 16 != 0) return MOE_UNSUPPORTED_SHAPE;
+  // (the kernel's index into a row goes a step past its end)
+  if (cols % 16 != 0 || cols > 0x7ffff000) return MOE_UNSUPPORTED_SHAPE;
   if (rows == 0) return MOE_OK;
   if (!x || !q || !scale) return MOE_INVALID_ARG;
   if (((uintptr_t)x | (uintptr_t)q) & 15) return MOE_UNSUPPORTED_SHAPE;

@@ -1,0 +1,21 @@
+"""CPU checks of the 8-bit integer calls at their largest sizes: what does not
+fit the kernels' index arithmetic is refused before any launch (there is no
+GPU here, so a call that launches returns the HIP error 3; the pointers are
+never followed)."""
+
+import ctypes
+
+from fp8_routed_expert_amd import _lib
+
+P = ctypes.c_void_p(4096)
+N = None
+
+
+def test_quantize_row_length():
+    """A row is walked with a 31-bit index in steps of 2048 values: it may not
+    come within a step of 2^31."""
+    f = _lib.load().moe_quantize_int8
+    for dtype in (0, 1, 2):
+        for cols in (0x7ffff010, 0x7ffffff0):
+            assert f(P, dtype, 1, cols, P, P, N) == 2, hex(cols)
+        assert f(N, dtype, 1, 0x7ffff000, P, P, N) == 1     # taken: the pointer is what it lacks
