@@ -525,9 +525,9 @@ moe_status_t moe_combine_rows_grad(const void* dout, const void* y, int dtype, i
  *              leaves there is unspecified.  Calls (or captured graphs) that
  *              may run at the same time need one each.
  * N, K, I and cols must be multiples of 16, K at most 131056 (so that no sum
- * overflows), I at most 2^30, cols at most 0x7ffff000, T * K of the gathered
- * call at most 0x7ffff000 (one buffer descriptor), M, T and rows of a product
- * at most 0x1ffffc00: MOE_UNSUPPORTED_SHAPE otherwise.  Matrices and the workspace 16-byte
+ * overflows), N at most 0x7fffff00, I at most 2^30, cols at most 0x7ffff000,
+ * T * K of the gathered call at most 0x7ffff000 (one buffer descriptor), M, T
+ * and rows of a product at most 0x1ffffc00: MOE_UNSUPPORTED_SHAPE otherwise.  Matrices and the workspace 16-byte
  * aligned, scales 4-byte.  offsets / counts / status_dev as for
  * moe_grouped_gemm_fp8.  Outputs may not overlap inputs.
  */

@@ -19,3 +19,17 @@ def test_quantize_row_length():
         for cols in (0x7ffff010, 0x7ffffff0):
             assert f(P, dtype, 1, cols, P, P, N) == 2, hex(cols)
         assert f(N, dtype, 1, 0x7ffff000, P, P, N) == 1     # taken: the pointer is what it lacks
+
+
+def test_product_channels():
+    """The tile counts of a product are formed in 31 bits, with up to 255
+    channels added."""
+    lib = _lib.load()
+    big = 0x7fffff10
+    for n in (big, 0x7ffffff0):
+        for m in (1, 20, 300):
+            assert lib.moe_gemm_int8(P, P, P, P, m, n, 16, P, 1, N) == 2, (m, hex(n))
+            assert lib.moe_linear_int8(P, 1, P, P, m, n, 16, P, 1, P, 1 << 20, N) == 2, (m, hex(n))
+            assert lib.moe_grouped_gemm_int8(P, P, P, P, P, P, 1, m, n, 16, P, 1, P, N) == 2
+            assert lib.moe_grouped_gemm_int8_gather(P, P, 9, P, P, P, P, P, 1, m, n, 16, P, 1, P, N) == 2
+    assert lib.moe_gemm_int8(N, P, P, P, 1, 0x7fffff00, 16, P, 1, N) == 1    # taken so far
