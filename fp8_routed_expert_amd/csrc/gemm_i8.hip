@@ -629,6 +629,7 @@ static moe_status_t product_i8(const I8Args& p, hipStream_t st) {
 }
 
 constexpr int kMaxChannels = 0x7fffff00;
+constexpr int kMaxRows = 0x1ffffc00;   // the row scales are addressed with 32-bit byte offsets
 
 // The checks that every product shares: sizes, then pointers.
 static moe_status_t product_args(const I8Args& p, bool grouped) {
@@ -639,8 +640,7 @@ static moe_status_t product_args(const I8Args& p, bool grouped) {
   // 128 * 128 * K stays below 2^31, and so does N with a tile's channels added
   if (p.N % 16 != 0 || p.K % 16 != 0 || p.K > 131056 || p.N > kMaxChannels)
     return MOE_UNSUPPORTED_SHAPE;
-  // the row scales are addressed with 32-bit byte offsets
-  if (p.rows_total > 0x1ffffc00 || p.src_rows > 0x1ffffc00) return MOE_UNSUPPORTED_SHAPE;
+  if (p.rows_total > kMaxRows || p.src_rows > kMaxRows) return MOE_UNSUPPORTED_SHAPE;
   if (grouped && (!p.offsets || !p.counts)) return MOE_INVALID_ARG;
   if (!p.w || !p.w_scale) return MOE_INVALID_ARG;
   if (p.row_src) {
@@ -741,7 +741,8 @@ extern "C" moe_status_t moe_linear_int8(const void* x, int dtype, const int8_t* 
                                         void* stream) {
   if (!float_type(dtype) || !float_type(c_type) || M < 0 || N <= 0 || K <= 0)
     return MOE_INVALID_ARG;
-  if (N % 16 != 0 || K % 16 != 0 || K > 131056 || N > kMaxChannels) return MOE_UNSUPPORTED_SHAPE;
+  if (N % 16 != 0 || K % 16 != 0 || K > 131056 || N > kMaxChannels || M > kMaxRows)
+    return MOE_UNSUPPORTED_SHAPE;
   if (!w || !w_scale) return MOE_INVALID_ARG;
   if (M == 0) return MOE_OK;
   if (!x || !c || !workspace || workspace_bytes < moe_linear_int8_workspace_bytes(M, K))

@@ -33,3 +33,12 @@ def test_product_channels():
             assert lib.moe_grouped_gemm_int8(P, P, P, P, P, P, 1, m, n, 16, P, 1, P, N) == 2
             assert lib.moe_grouped_gemm_int8_gather(P, P, 9, P, P, P, P, P, 1, m, n, 16, P, 1, P, N) == 2
     assert lib.moe_gemm_int8(N, P, P, P, 1, 0x7fffff00, 16, P, 1, N) == 1    # taken so far
+
+
+def test_linear_refuses_before_it_quantises():
+    """A row count that the product cannot take is refused before the rows'
+    quantisation is launched into the workspace."""
+    f = _lib.load().moe_linear_int8
+    m = 0x1ffffc01
+    assert f(P, 1, P, P, m, 16, 16, P, 1, P, m * 20, N) == 2
+    assert f(N, 1, P, P, m - 1, 16, 16, P, 1, P, m * 20, N) == 1
