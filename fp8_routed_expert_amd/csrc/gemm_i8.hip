@@ -747,7 +747,8 @@ extern "C" moe_status_t moe_linear_int8(const void* x, int dtype, const int8_t* 
   if (M == 0) return MOE_OK;
   if (!x || !c || !workspace || workspace_bytes < moe_linear_int8_workspace_bytes(M, K))
     return MOE_INVALID_ARG;
-  if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)c | (uintptr_t)workspace) & 15)
+  if ((((uintptr_t)x | (uintptr_t)w | (uintptr_t)c | (uintptr_t)workspace) & 15) ||
+      ((uintptr_t)w_scale & 3))
     return MOE_UNSUPPORTED_SHAPE;
   if (one_launch(M, N, K))
     return linear_in_one(x, dtype, w, w_scale, M, N, K, c, c_type,

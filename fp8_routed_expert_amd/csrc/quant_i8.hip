@@ -160,7 +160,7 @@ extern "C" moe_status_t moe_quantize_int8(const void* x, int dtype, int rows, in
   if (cols % 16 != 0 || cols > 0x7ffff000) return MOE_UNSUPPORTED_SHAPE;
   if (rows == 0) return MOE_OK;
   if (!x || !q || !scale) return MOE_INVALID_ARG;
-  if (((uintptr_t)x | (uintptr_t)q) & 15) return MOE_UNSUPPORTED_SHAPE;
+  if ((((uintptr_t)x | (uintptr_t)q) & 15) || ((uintptr_t)scale & 3)) return MOE_UNSUPPORTED_SHAPE;
   return quantize_int8<false>(x, dtype, rows, cols, q, scale, nullptr, nullptr, 0, nullptr,
                               stream);
 }
@@ -175,7 +175,7 @@ extern "C" moe_status_t moe_act_requant_int8(const void* h, int dtype, const int
   if (!offsets || !counts) return MOE_INVALID_ARG;
   if (rows_total == 0) return MOE_OK;
   if (!h || !q || !q_scale) return MOE_INVALID_ARG;
-  if (((uintptr_t)h | (uintptr_t)q) & 15) return MOE_UNSUPPORTED_SHAPE;
+  if ((((uintptr_t)h | (uintptr_t)q) & 15) || ((uintptr_t)q_scale & 3)) return MOE_UNSUPPORTED_SHAPE;
   return quantize_int8<true>(h, dtype, rows_total, I, q, q_scale, offsets, counts, E, status_dev,
                              stream);
 }

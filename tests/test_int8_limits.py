@@ -42,3 +42,15 @@ def test_linear_refuses_before_it_quantises():
     m = 0x1ffffc01
     assert f(P, 1, P, P, m, 16, 16, P, 1, P, m * 20, N) == 2
     assert f(N, 1, P, P, m - 1, 16, 16, P, 1, P, m * 20, N) == 1
+
+
+def test_scales_are_aligned():
+    """Scales are 4-byte aligned, as the header asks, in every call."""
+    lib = _lib.load()
+    odd = ctypes.c_void_p(4098)
+    assert lib.moe_quantize_int8(P, 1, 4, 48, P, odd, N) == 2
+    assert lib.moe_act_requant_int8(P, 1, P, P, 4, 64, 48, P, odd, P, N) == 2
+    for m, wsb in ((1, 64), (40, 4096)):     # one launch, two launches
+        assert lib.moe_linear_int8(P, 1, P, odd, m, 32, 48, P, 1, P, wsb, N) == 2
+    assert lib.moe_gemm_int8(P, odd, P, P, 4, 32, 48, P, 1, N) == 2
+    assert lib.moe_gemm_int8(P, P, P, odd, 4, 32, 48, P, 1, N) == 2
