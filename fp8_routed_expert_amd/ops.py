@@ -445,6 +445,8 @@ def moe_sort_tokens(topk_idx, E, layout, align_m, rows, counts, offsets, slot_of
     (contiguous) or the per-expert capacity C (masked); workspace holds
     moe_layout_workspace_bytes(T, K, E) bytes."""
     T, K = _matrix(topk_idx, "topk_idx")
+    if max(E, rows, align_m) > _INT_MAX:
+        raise ValueError(f"moe_sort_tokens: E {E}, rows {rows}, align_m {align_m}, at most {_INT_MAX}")
     rows_total = E * rows if layout == LAYOUT_MASKED else rows
     dev = topk_idx.get_device()
     _call("moe_sort_tokens", stream, dev,
@@ -533,8 +535,8 @@ def moe_quantize_int8(x, q, scale, stream=None):
     channels of weights [N, K] or [E, N, K] (scale then [E, N])."""
     cols = x.shape[-1]
     rows = x.numel() // cols if cols else 0
-    if rows > _INT_MAX:
-        raise ValueError(f"moe_quantize_int8: {rows} rows, at most {_INT_MAX}")
+    if rows > _INT_MAX or cols > _INT_MAX:
+        raise ValueError(f"moe_quantize_int8: {rows} rows of {cols}, at most {_INT_MAX}")
     dev = x.get_device()
     _call("moe_quantize_int8", stream, dev, _arg(x, _FLOATS, "x", dev), _type(x, "x"), rows,
           cols, _arg(q, _I8, "q", dev, x.shape), _arg(scale, _F32, "scale", dev, x.shape[:-1]))
@@ -571,9 +573,19 @@ def moe_linear_int8(x, w, w_scale, c, workspace, stream=None):
 
 
 def _experts(w):
-    if w.dim() != 3:
+    shape = w.shape
+    if len(shape) != 3:
         raise ValueError(f"w: must have three dimensions, has {w.dim()}")
-    return w.shape
+    if max(shape) > _INT_MAX:
+        raise ValueError(f"w: shape {tuple(shape)} past {_INT_MAX}")
+    return shape
+
+
+def _count(t, name):
+    n = t.numel()
+    if n > _INT_MAX:
+        raise ValueError(f"{name}: {n} elements, at most {_INT_MAX}")
+    return n
 
 
 def moe_grouped_gemm_int8(a, a_scale, w, w_scale, offsets, counts, c, status, stream=None):
@@ -596,7 +608,7 @@ def moe_grouped_gemm_int8_gather(x, x_scale, row_src, w, w_scale, offsets, count
     int8, x_scale [T])."""
     E, N, K = _experts(w)
     T = _matrix(x, "x")[0]
-    R = row_src.numel()
+    R = _count(row_src, "row_src")
     dev = x.get_device()
     _call("moe_grouped_gemm_int8_gather", stream, dev,
           _arg(x, _I8, "x", dev, (T, K)), _arg(x_scale, _F32, "x_scale", dev, (T,)), T,
@@ -612,7 +624,7 @@ def moe_act_requant_int8(h, offsets, counts, q, q_scale, status, stream=None):
     quantised per valid row; h [rows_total, 2I] float32, bfloat16 or float16."""
     R, I2 = _matrix(h, "h")
     I = I2 // 2
-    E = counts.numel()
+    E = _count(counts, "counts")
     dev = h.get_device()
     _call("moe_act_requant_int8", stream, dev,
           _arg(h, _FLOATS, "h", dev, (R, 2 * I)), _type(h, "h"),
