@@ -50,6 +50,8 @@ __device__ __forceinline__ v4i make_rsrc(const void* base, uint32_t bytes) {
 // compiler cannot then hoist one offset register per chunk (or per parity)
 // out of the K loop (the address is read when the load issues, so the
 // temporary is free right after).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // (the m0 clobber is meant)
 __device__ __forceinline__ void dma16_split(v4i rsrc, uint8_t* lds, uint32_t vlane,
                                             uint32_t sxor, uint32_t suni) {
   const uint32_t m = (uint32_t)(uintptr_t)(lds_void*)lds;
