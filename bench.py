@@ -36,6 +36,7 @@ HBM_PEAK_GBS = 8000.0         # MI355X HBM3E
 METRIC = "MoE-layer FP8 TFLOP/s + % of MFMA peak; routed token-rows/s per GPU"
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "gemm1_act_ep32_prefill_traffic.json")
 GEMM_SRC = os.path.join(ROOT, "fp8_routed_expert_amd", "csrc", "gemm.hip")
+GEMM_HEADERS = ("gemm_tiles.hpp", "device_common.hpp")   # what gemm.hip includes, beside it
 
 
 def log(msg):
@@ -43,7 +44,11 @@ def log(msg):
 
 
 def gemm_source_hash():
-    return hashlib.sha256(open(GEMM_SRC, "rb").read()).hexdigest()[:16]
+    """Of every source that the GEMM kernels are compiled from."""
+    h = hashlib.sha256()
+    for path in (GEMM_SRC, *(os.path.join(os.path.dirname(GEMM_SRC), n) for n in GEMM_HEADERS)):
+        h.update(open(path, "rb").read())
+    return h.hexdigest()[:16]
 
 
 def stored_traffic(launch_key):
