@@ -505,19 +505,23 @@ def moe_combine_rows_grad(dout, y, slot_of, topk_w, dy, dtopk_w, status, row_src
                           stream=None):
     """Gradients of moe_combine_rows: dy[slot_of[t, k]] = topk_w[t, k] * dout[t]
     and dtopk_w[t, k] = <dout[t], y[slot_of[t, k]]> (float32; 0 without a
-    row).  dy or dtopk_w may be None.  Rows of dy that no token has are left
-    as they are, or set to zero if row_src is given."""
+    row).  dy or dtopk_w may be None; without dtopk_w so may y, and without dy
+    topk_w (what is then not read).  Rows of dy that no token has are left as
+    they are, or set to zero if row_src is given."""
     T, H = _matrix(dout, "dout")
     K = _matrix(slot_of, "slot_of")[1]
-    R = _matrix(y, "y")[0]
     code = _type(dout, "dout")
     if dy is None and dtopk_w is None:
         raise ValueError("moe_combine_rows_grad: neither dy nor dtopk_w is given")
+    if y is None and dtopk_w is not None or topk_w is None and dy is not None:
+        raise ValueError("moe_combine_rows_grad: dtopk_w needs y, and dy needs topk_w")
+    R = _matrix(dy, "dy")[0] if y is None else _matrix(y, "y")[0]
     dev = dout.get_device()
     _call("moe_combine_rows_grad", stream, dev,
-          _arg(dout, (dout.dtype,), "dout", dev), _arg(y, (dout.dtype,), "y", dev, (R, H)),
+          _arg(dout, (dout.dtype,), "dout", dev),
+          None if y is None else _arg(y, (dout.dtype,), "y", dev, (R, H)),
           code, R, _arg(slot_of, _I32, "slot_of", dev, (T, K)),
-          _arg(topk_w, _F32, "topk_w", dev, (T, K)), T, K, H,
+          None if topk_w is None else _arg(topk_w, _F32, "topk_w", dev, (T, K)), T, K, H,
           None if dy is None else _arg(dy, (dout.dtype,), "dy", dev, (R, H)),
           None if dtopk_w is None else _arg(dtopk_w, _F32, "dtopk_w", dev, (T, K)),
           None if row_src is None else _arg(row_src, _I32, "row_src", dev, (R,)),

@@ -70,7 +70,9 @@ class _Combine(torch.autograd.Function):
     def forward(ctx, y, topk_w, table):
         y, topk_w = y.contiguous(), topk_w.contiguous()
         ctx.table = table
-        ctx.save_for_backward(y, topk_w)
+        # y's gradient reads the weights, the weights' y: nothing else is kept
+        needs_y, needs_w = ctx.needs_input_grad[:2]
+        ctx.save_for_backward(y if needs_w else None, topk_w if needs_y else None)
         out = y.new_empty(table.T, y.shape[1])
         ops.moe_combine_rows(y, table.slot_of, topk_w, out, table.status)
         return out
@@ -80,8 +82,8 @@ class _Combine(torch.autograd.Function):
     def backward(ctx, dout):
         t = ctx.table
         y, w = ctx.saved_tensors
-        dy = torch.empty_like(y) if ctx.needs_input_grad[0] else None
-        dw = torch.empty_like(w) if ctx.needs_input_grad[1] else None
+        dy = dout.new_empty(t.rows_total, dout.shape[1]) if ctx.needs_input_grad[0] else None
+        dw = dout.new_empty(t.T, t.K, dtype=torch.float32) if ctx.needs_input_grad[1] else None
         ops.moe_combine_rows_grad(dout.contiguous(), y, t.slot_of, w, dy, dw, t.status, t.row_src)
         return dy, dw, None
 
