@@ -313,7 +313,7 @@ def _own(s):
     if op == "sort":
         fre.moe_sort_tokens(s["topk_idx"], c["E"], c["layout"], 128, _rows(c), s["counts"], s["offsets"],
                             s["slot_of"], s["row_src"], s["row_expert"], s["workspace"], s["status"])
-        fre.moe_permute_rows(s["x"], s["slot_of"], s["a"], s["status"])
+        fre.moe_permute_rows(s["x"], s["slot_of"], s["a"], s["status"], s["row_src"])
         return {"a": s["a"], "table": (s["counts"], s["offsets"], s["slot_of"], s["row_src"], s["row_expert"])}
     if op == "sort_grad":
         fre.moe_permute_rows_grad(s["da"], s["slot_of"], s["dx"], s["status"])
@@ -322,7 +322,8 @@ def _own(s):
         fre.moe_combine_rows(s["y"], s["slot_of"], s["topk_w"], s["out"], s["status"])
         return s["out"]
     if op == "combine_grad":
-        fre.moe_combine_rows_grad(s["dout"], s["y"], s["slot_of"], s["topk_w"], s["dy"], s["dw"], s["status"])
+        fre.moe_combine_rows_grad(s["dout"], s["y"], s["slot_of"], s["topk_w"], s["dy"], s["dw"], s["status"],
+                                  s["row_src"])
         return {"dy": s["dy"], "dw": s["dw"]}
     if op == "gate_up":
         fre.moe_grouped_gemm_int8_gather(s["x"], s["x_scale"], s["row_src"], s["w"], s["w_scale"], s["offsets"],
