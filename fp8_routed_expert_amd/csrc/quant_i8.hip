@@ -9,9 +9,12 @@
 // kKeep slices of eight values that a lane takes stay in its registers between
 // the row's maximum and the codes; the others of a longer row are read (and
 // the activation computed) again, from the cache.  Reads 2 (or 4) bytes and
-// writes one per value: bound by HBM bandwidth (65536 rows of 7168 bf16 250 us,
-// 5.6 TB/s; 16384 of 4096 5.9; the activation of 131072 rows of 2 x 2048 220 us,
-// 6.1 TB/s).
+// writes one per value.  Large inputs are bound by HBM bandwidth (65536 rows of
+// 7168 bf16 250 us, 5.6 TB/s; 16384 of 4096 5.9; the activation of 131072 rows of
+// 2 x 2048 220 us, 6.1 TB/s); a few thousand rows by the chain of a row's slices,
+// one load after the other (8191 rows of 2048 11.5 us, 4.4 TB/s; the activation of
+// 5529 rows of 2 x 2048 15 us, of which the bytes are 9), and the activation of a
+// masked or padded buffer takes as long as that of a full one.
 #include <type_traits>
 
 #include "rows_i8.hpp"
@@ -53,8 +56,11 @@ __global__ __launch_bounds__(kQThreads) void quant_int8_kernel(
   for (long long at = (long long)blockIdx.x * kRows + (kWaves == 1 ? wave : 0); at < rows;
        at += (long long)gridDim.x * kRows) {
     const int row = (int)at;
-    // all loads first (lanes past the row read its first slice again); the
-    // search for the row's segment runs while they are in flight
+    // Slice by slice (lanes past the row read its first one again): each test of
+    // a slice is a branch, so the compiler waits for its load and converts it
+    // (or evaluates the activation) before the next slice's load goes out.  The
+    // row's segment is looked up last, so rows outside the segments are read and
+    // computed like the others, and then dropped.
     float v[kKeep][8];
 #pragma unroll
     for (int u = 0; u < kKeep; ++u) {
@@ -103,7 +109,8 @@ static void launch_quant(const void* x, int rows, int cols, uint8_t* q, float* s
                          const int32_t* offsets, const int32_t* counts, int E, int32_t* status,
                          hipStream_t st) {
   // a wave per row where the lanes of four would idle, or where there are
-  // enough rows to fill the CUs (bf16, 8191 rows of 2048: 11.5 us against 12.8
+  // enough rows to fill the CUs, with a row's slices loaded one after the other
+  // as they are (bf16, 8191 rows of 2048: 11.5 us against 12.8
   // with four waves, 2048 rows 4.5 against 5.0; 96 rows 3.7 against 2.9, all
   // latency; 8191 rows of 1024 6.1 against 10.5, 96 rows 3.0 against 2.9)
   const bool one = cols <= 1024 || (cols <= kKeep * 64 * 8 && rows > 1536);
@@ -175,7 +182,8 @@ extern "C" moe_status_t moe_act_requant_int8(const void* h, int dtype, const int
   if (!offsets || !counts) return MOE_INVALID_ARG;
   if (rows_total == 0) return MOE_OK;
   if (!h || !q || !q_scale) return MOE_INVALID_ARG;
-  if ((((uintptr_t)h | (uintptr_t)q) & 15) || ((uintptr_t)q_scale & 3)) return MOE_UNSUPPORTED_SHAPE;
+  if ((((uintptr_t)h | (uintptr_t)q) & 15) || ((uintptr_t)q_scale & 3))
+    return MOE_UNSUPPORTED_SHAPE;
   return quantize_int8<true>(h, dtype, rows_total, I, q, q_scale, offsets, counts, E, status_dev,
                              stream);
 }
