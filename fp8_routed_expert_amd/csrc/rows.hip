@@ -219,8 +219,11 @@ __global__ __launch_bounds__(kRowThreads) void permute_rows_kernel(
 }
 
 // out[t] = sum over the valid picks, in ascending k, of (w[t, k] *) y[slot]:
-// the combine, and (kWeighted false) the gradient of the permute.  Two rows'
-// loads are in flight at a time.
+// the combine, and (kWeighted false) the gradient of the permute.  Rows are
+// taken in pairs, but only the combine in fp16 and fp32 (aligned rows, a wave
+// each) has both rows' loads in flight: in bf16, and in the permute's gradient
+// in every type, the compiler moves the first row's conversion (fp32: its
+// addition) ahead of the second load, and so waits for one row at a time.
 template <typename El, int kLanes, int kCh, bool kAligned, bool kStream, bool kWeighted>
 __global__ __launch_bounds__(kRowThreads) void gather_sum_kernel(
     const uint8_t* __restrict__ y, int rows_total, const int32_t* __restrict__ slot_of,
