@@ -548,7 +548,13 @@ static moe_status_t launch_skinny(const I8Args& p, hipStream_t st) {
 }
 
 // Launches the product in tiles chosen from the sizes alone (the same inside
-// graph capture).  `rows` is a dense product's, or a segment's on average.
+// graph capture).  `rows` is a dense product's, or a segment's on average: of
+// the buffer, whose rows the host knows, not of the tokens.  The capacity of
+// masked segments and the padding between contiguous ones (up to 127 rows of
+// an expert) count as rows, so few tokens in a contiguous buffer run in the
+// tiles of a hundred or more.  Dense products of 9 to 64 rows go from 64 x 64
+// to 128 x 128 tiles past 16384 channels (one round of the former is full), which
+// leaves CUs without a tile up to some 32768 channels.
 // Times are of products whose weights come from HBM, N x K (experts x N x K),
 // in us.
 //
@@ -559,12 +565,15 @@ static moe_status_t launch_skinny(const I8Args& p, hipStream_t st) {
 //     7168 33.0 against 23.2).  Its workgroups take 16 channels, or 32 where
 //     there are enough of them and each has more to do than to stream (search
 //     its segment, read rows, start on a short K): 32 x 4096 x 7168 of 16 rows
-//     177 against 219, 16 rows of 32768 x 4096 31.5 against 36.0; but 1 row
+//     177 against 219, one expert's 16 rows of 32768 x 4096 31.5 against 36.0 (a
+//     dense product of that many channels has tiles from 9 rows on); but 1 row
 //     28.0 against 26.4, and 4096 x 7168, too few, 11.5 against 8.0.
 //     Where even those are short-lived and many, 64 x 128 tiles: 32 x 7168 x
 //     2048 of 16 rows 97 against 124, 64 x 7168 x 3584 296 against 388, one
 //     row of 65536 x 1024 15.9 against 17.7; but 32 x 4096 x 4096 132 against
-//     124, one row of 152064 x 2048 65 against 52.
+//     124, one row of 152064 x 2048 65 against 52.  With one row of each of few
+//     experts and K <= 2048 the rule loses: 6 x 7168 x 2048 18.7 against 14.1, 8 x
+//     7168 x 2048 (half of them empty) 13.4 against 12.1.
 //   * One round of small tiles, loaded five steps ahead: 64 x 64 (128 rows:
 //     20.4 and 9.6; two and three stages of 64 x 128 tiles 45 and 17), then
 //     128 x 64 (512 and 256 rows: 27 and 11.5; 64 x 64 tiles 41 and 17), then
@@ -708,7 +717,10 @@ extern "C" size_t moe_linear_int8_workspace_bytes(int M, int K) {
 // have: later workgroups would quantise the rows again with no weights under way
 // (us, weights from HBM, one launch against two; 1 row of 4096 x 7168 (N x K)
 // 8.5 : 11.7, 4 rows 10.6 : 12.7; 12288 x 4096 15.0 : 15.3, 16384 x 4096
-// 19.5 : 18.5, 32768 x 1024 19.4 : 13.8, 152064 x 2048 97 : 54).
+// 19.5 : 18.5, 32768 x 1024 19.4 : 13.8, 152064 x 2048 97 : 54).  Past K = 8192,
+// where a wave asks for its weights one load at a time, the two come out even:
+// 8192 x 14336 1 row 26.5 : 31.0, 4 rows 34.1 : 33.1; 8192 x 28672 53.1 : 57.7,
+// 2 rows 60.6 : 60.8; but 4096 x 28672 35.9 : 35.4, 2 rows 39.4 : 35.8.
 static bool one_launch(int M, int N, int K) {
   return M <= kLinearRows && N <= 3 * 256 * 16 &&
          (long long)M * (K + 16) <= 61440;   // of 64 KB

@@ -262,6 +262,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void linear_i8_kernel(
 #pragma unroll
   for (int u = 0; u < kLinearAhead; ++u)
     if (first + u < last) acc[0][0] = mfma_i8(wf[u], row(first + u), acc[0][0]);
+  // (past K = 8192: one load at a time, each waited for before the next; times
+  // at one_launch)
   for (int sl = first + kLinearAhead; sl < last; ++sl)
     acc[0][0] = mfma_i8(weights(sl), row(sl), acc[0][0]);
   add_sums<1, 1>(sums, acc, lane);
