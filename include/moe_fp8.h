@@ -507,15 +507,18 @@ moe_status_t moe_combine_rows_grad(const void* dout, const void* y, int dtype, i
  *   moe_grouped_gemm_int8_gather  with row r of the buffer read from
  *                       x[row_src[r]] and its scale from
  *                       x_scale[row_src[r]]; a valid row with row_src < 0 or
- *                       >= T gives 0
+ *                       >= T is a row of zeros with the scale 0: it gives 0,
+ *                       and NaN in a channel whose scale is not finite
  *   moe_act_requant_int8  v[m, j] = silu(h[m, j]) * h[m, I + j] in fp32 (exp
  *                       and reciprocal from the hardware, ~1 ulp each),
  *                       quantised per valid row as moe_quantize_int8
  *   moe_linear_int8     moe_quantize_int8 of x, then moe_gemm_int8
  *
- * The sum is exact (32-bit integers; codes may be any of [-128, 127]); the
- * scales multiply it in fp32 and the result is rounded once to c's type, to
- * nearest even.
+ * The sum is exact (32-bit integers; codes may be any of [-128, 127]).  It is
+ * then rounded to fp32 (sums past 2^24 lose their last bits), multiplied by
+ * the fp32 product of the two scales, and the result rounded to c's type; each
+ * of these roundings is to nearest even.  A product of scales that overflows
+ * gives infinities, and NaN where the sum is 0.
  *
  *   a, q [rows, K] int8, a_scale, q_scale [rows] f32
  *   w    [E, N, K] int8 (dense: [N, K]), w_scale [E, N] f32
@@ -527,9 +530,9 @@ moe_status_t moe_combine_rows_grad(const void* dout, const void* y, int dtype, i
  * N, K, I and cols must be multiples of 16, K at most 131056 (so that no sum
  * overflows), N at most 0x7fffff00, I at most 2^30, cols at most 0x7ffff000,
  * T * K of the gathered call at most 0x7ffff000 (one buffer descriptor), M, T
- * and rows of a product at most 0x1ffffc00: MOE_UNSUPPORTED_SHAPE otherwise.  Matrices and the workspace 16-byte
- * aligned, scales 4-byte.  offsets / counts / status_dev as for
- * moe_grouped_gemm_fp8.  Outputs may not overlap inputs.
+ * and rows of a product at most 0x1ffffc00; matrices and the workspace 16-byte
+ * aligned, scales 4-byte: MOE_UNSUPPORTED_SHAPE otherwise.  offsets / counts /
+ * status_dev as for moe_grouped_gemm_fp8.  Outputs may not overlap inputs.
  */
 moe_status_t moe_quantize_int8(const void* x, int dtype, int rows, int cols, int8_t* q,
                                float* scale, void* stream);

@@ -132,3 +132,30 @@ def test_quantize_longest_row(gpu):
         v = x[0, b:b + (1 << 27)].double().div_(want.double().cuda()).round_()
         assert torch.equal(q[0, b:b + (1 << 27)], v.to(torch.int8)), b
     assert (buf[:64] == 99).all() and (buf[-64:] == 99).all()
+
+
+@pytest.mark.parametrize("K", [128, 144])
+@pytest.mark.parametrize("shape", FAR, ids=["x".join(map(str, s[2])) for s in FAR])
+def test_gather_with_non_finite_scales(gpu, shape, K):
+    """A row without a source is a row of zeros with the scale 0: NaN in a
+    channel whose scale is not finite, 0 in all others.  Other rows take the
+    channel's NaN, or its infinity times their sum."""
+    E, N, counts = shape
+    torch.manual_seed(K + N)
+    T, R = 60, sum(counts)
+    x, sx = torch.randint(1, 128, (T, K), dtype=torch.int8, device="cuda"), torch.rand(T, device="cuda") + 0.5
+    w, sw = torch.randint(1, 128, (E, N, K), dtype=torch.int8, device="cuda"), torch.rand(E, N, device="cuda") + 0.5
+    sw[:, 3], sw[:, N - 1] = float("nan"), float("inf")
+    src = torch.randint(-1, T, (R,), device="cuda")
+    src[0], src[R - 1], src[R // 2] = -1, T, 5
+    known = (src >= 0) & (src < T)
+    offsets = torch.tensor([sum(counts[:e]) for e in range(E + 1)], dtype=torch.int32).cuda()
+    finite = torch.ones(N, dtype=torch.bool, device="cuda")
+    finite[3], finite[N - 1] = False, False
+    for name, t in TYPES.items():
+        c, st = torch.full((R, N), 77.0, dtype=t, device="cuda"), i32(1)
+        fre.moe_grouped_gemm_int8_gather(x, sx, src.int(), w, sw, offsets,
+                                         torch.tensor(counts, dtype=torch.int32).cuda(), c, st)
+        assert c[:, 3].isnan().all() and c[~known][:, N - 1].isnan().all()
+        assert (c[known][:, N - 1] == float("inf")).all()
+        assert (c[~known][:, finite] == 0).all() and (c[known][:, finite] > 0).all() and int(st) == 0
