@@ -156,7 +156,9 @@ struct Picks {
 };
 
 // Rows of the buffer that no token goes to are set to zero: one wave per 64
-// rows reads their sources and clears those without one.
+// rows reads their sources and clears those without one, row after row (12-17 us
+// where nearly all 64 are empty: 777 x 3 picks of 509 fp32, the gradient with
+// the clearing 22.0 us, without 5.4).
 __device__ __forceinline__ void zero_rows(long long w, const int32_t* __restrict__ row_src,
                                           int rows_total, long long row_bytes, uint8_t* a) {
   const int lane = threadIdx.x & 63;
