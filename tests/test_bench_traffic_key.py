@@ -36,6 +36,13 @@ def test_key_covers_the_kernel_and_its_headers(tmp_path, monkeypatch):
     assert bench.gemm_source_hash() == key
 
 
-def test_stored_record_is_of_these_sources():
+def test_record_of_other_sources_is_not_used(tmp_path, monkeypatch):
     rec = json.load(open(bench.TRAFFIC_FILE))
-    assert bench.stored_traffic(rec["launch"]) == rec["hbm_bytes_per_launch"] > 0
+    assert {"gemm_source_sha", "launch", "hbm_bytes_per_launch"} <= set(rec)
+    path = tmp_path / "record.json"
+    monkeypatch.setattr(bench, "TRAFFIC_FILE", str(path))
+    assert bench.stored_traffic(rec["launch"]) is None
+    for key, want in ((bench.gemm_source_hash(), rec["hbm_bytes_per_launch"]), ("0" * 16, None)):
+        path.write_text(json.dumps({**rec, "gemm_source_sha": key}))
+        assert bench.stored_traffic(rec["launch"]) == want
+        assert bench.stored_traffic("another launch") is None
