@@ -510,8 +510,11 @@ moe_status_t moe_combine_rows_grad(const void* dout, const void* y, int dtype, i
  *                       >= T is a row of zeros with the scale 0: it gives 0,
  *                       and NaN in a channel whose scale is not finite
  *   moe_act_requant_int8  v[m, j] = silu(h[m, j]) * h[m, I + j] in fp32 (exp
- *                       and reciprocal from the hardware, ~1 ulp each),
- *                       quantised per valid row as moe_quantize_int8
+ *                       and reciprocal from the hardware, ~1 ulp each; the
+ *                       reciprocal has no subnormals, so a gate below -87.3
+ *                       gives 0, as moe_act_requant has it, and one of
+ *                       -infinity NaN), quantised per valid row as
+ *                       moe_quantize_int8
  *   moe_linear_int8     moe_quantize_int8 of x, then moe_gemm_int8
  *
  * The sum is exact (32-bit integers; codes may be any of [-128, 127]).  It is

@@ -159,3 +159,23 @@ def test_gather_with_non_finite_scales(gpu, shape, K):
         assert c[:, 3].isnan().all() and c[~known][:, N - 1].isnan().all()
         assert (c[known][:, N - 1] == float("inf")).all()
         assert (c[~known][:, finite] == 0).all() and (c[known][:, finite] > 0).all() and int(st) == 0
+
+
+def test_act_of_far_gates(gpu):
+    """Down to -87.3 as accurate as any gate ((|g| + 6) 2^-23, as in the
+    activation's other test), below that 0; infinite values make the row NaN."""
+    gates = torch.tensor([-80.0, -86, -87, -87.25, -87.5, -89, -104, -1e30, 88, 1e4, float("-inf"), float("inf")])
+    n, I = gates.numel(), 16
+    h = torch.cat([gates[:, None].expand(n, I), torch.full((n, I), 1e30)], dim=1).contiguous()
+    q, s, st = torch.full((n, I), 99, dtype=torch.int8, device="cuda"), torch.zeros(n, device="cuda"), i32(1)
+    fre.moe_act_requant_int8(h.cuda(), torch.tensor([0, n], dtype=torch.int32).cuda(),
+                             torch.tensor([n], dtype=torch.int32).cuda(), q, s, st)
+    q, s, g = q.cpu().double(), s.cpu().double(), gates.double()
+    near = (g > -87.3) & (g < 1e5)
+    v = (g / (1 + torch.exp(-g)) * 1e30)[near]
+    rel = (g[near].abs() + 6) * 2.0 ** -23
+    assert (q[near] == 127 * v.sign()[:, None]).all()
+    assert ((s[near] - v.abs() / 127).abs() <= 2 * rel * s[near]).all()
+    far = (g <= -87.3) & g.isfinite()
+    assert (q[far] == 0).all() and (s[far] == 1).all()
+    assert s[g.isinf()].isnan().all() and (q[g.isinf()] == 0).all() and int(st) == 0
