@@ -12,7 +12,7 @@ from fp8_routed_expert_amd import build as lib_build
 KERNEL = r"""
 #include "gemm_tiles.hpp"
 __global__ void loads(const uint8_t* p, uint8_t* out) {
-  __shared__ __attribute__((aligned(1024))) uint8_t s[3072];
+  __shared__ __attribute__((aligned(1024))) uint8_t s[3 * 1024];
   const moe::v4i r = moe::make_rsrc(p, 4096);
   moe::dma16(r, s, threadIdx.x * 16);
   moe::dma16_add(r, s + 1024, threadIdx.x * 16, 1024);
