@@ -16,8 +16,16 @@ from .ops import (moe_layout_workspace_bytes, moe_gemm_large_tiles, moe_gemm_til
                   moe_quantize_int8, moe_gemm_int8, moe_linear_int8,
                   moe_linear_int8_workspace_bytes, moe_grouped_gemm_int8,
                   moe_grouped_gemm_int8_gather, moe_act_requant_int8,
+                  moe_route_tokens, moe_route_tokens_grad,
+                  moe_layer_norm, moe_layer_norm_grad, moe_layer_norm_workspace_bytes,
+                  moe_grouped_gemm_float, moe_grouped_gemm_float_grad_rows,
+                  moe_grouped_gemm_float_grad_weights, moe_grouped_gemm_float_workspace_bytes,
+                  moe_gated_act, moe_gated_act_grad,
                   moe_ceiling_copy, moe_ceiling_mfma_fp8,
                   LAYOUT_CONTIGUOUS, LAYOUT_MASKED,
-                  ERR_BAD_EXPERT, ERR_OVERFLOW, ERR_BAD_INDEX)
+                  SCORE_SOFTMAX, SCORE_SIGMOID,
+                  ERR_BAD_EXPERT, ERR_OVERFLOW, ERR_BAD_INDEX, ERR_NAN)
 from .layer import MoELayer, contiguous_rows  # noqa: F401
 from .routing import SortedTokens, sort_tokens, permute_tokens, combine_tokens  # noqa: F401
+from .experts import (RoutedExperts, layer_norm, route_tokens, grouped_linear,  # noqa: F401
+                      gated_act)

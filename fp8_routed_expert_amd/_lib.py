@@ -17,6 +17,7 @@ _c_int = ctypes.c_int
 _i32p = ctypes.c_void_p
 _vp = ctypes.c_void_p
 _size = ctypes.c_size_t
+_f32 = ctypes.c_float
 
 # name -> (restype, argtypes), mirroring include/moe_fp8.h
 SIGNATURES = {
@@ -90,11 +91,33 @@ SIGNATURES = {
     "moe_linear_int8_workspace_bytes": (_size, [_c_int, _c_int]),
     "moe_linear_int8": (ctypes.c_int32, [
         _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _size, _vp]),
+    "moe_route_tokens": (ctypes.c_int32, [
+        _vp, _c_int, _c_int, _c_int, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _f32,
+        _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_route_tokens_grad": (ctypes.c_int32, [
+        _vp, _c_int, _c_int, _c_int, _vp, _c_int, _c_int, _c_int, _f32, _vp, _vp, _vp, _vp, _vp]),
+    "moe_layer_norm": (ctypes.c_int32, [
+        _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _f32, _vp, _vp, _vp, _vp]),
+    "moe_layer_norm_workspace_bytes": (_size, [_c_int, _c_int]),
+    "moe_layer_norm_grad": (ctypes.c_int32, [
+        _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _size, _vp]),
+    "moe_grouped_gemm_float": (ctypes.c_int32, [
+        _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp]),
+    "moe_grouped_gemm_float_grad_rows": (ctypes.c_int32, [
+        _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp]),
+    "moe_grouped_gemm_float_workspace_bytes": (_size, [_c_int, _c_int, _c_int, _c_int]),
+    "moe_grouped_gemm_float_grad_weights": (ctypes.c_int32, [
+        _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _size, _vp,
+        _vp]),
+    "moe_gated_act": (ctypes.c_int32, [
+        _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp]),
+    "moe_gated_act_grad": (ctypes.c_int32, [
+        _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp]),
     "moe_ceiling_copy": (ctypes.c_int32, [_vp, _vp, _size, _vp]),
     "moe_ceiling_mfma_fp8": (ctypes.c_int32, [_c_int, _c_int, _vp, _vp, _vp]),
 }
 
-ABI_VERSION = 10
+ABI_VERSION = 11
 
 _lib = None
 

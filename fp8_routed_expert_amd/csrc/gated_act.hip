@@ -1,0 +1,133 @@
+// The gated activation between the experts' two products, and its gradient,
+// in fp32, bf16 and fp16, for the valid rows of the expert segments.
+//
+//   q = silu(g) u,  silu(g) = g s,  s = 1 / (1 + exp(-g))
+//   dg = dq u s (1 + g (1 - s)),  du = dq g s
+//
+// h [rows, 2I] holds g in its first I columns and u in the others.  Every value
+// is read and written once: bound by HBM bandwidth.
+#include "row_chunks.hpp"
+
+namespace moe {
+
+struct ActArgs {
+  const uint8_t* h;
+  const uint8_t* dq;
+  const int32_t* offsets;
+  const int32_t* counts;
+  int E, rows, I;
+  uint8_t* out;      // q, or dh
+  int zero_rest;
+  int32_t* status;
+};
+
+// sigmoid(g) and 1 - sigmoid(g), both without cancellation, from
+// e = exp(-|g|): 1 / (1 + e) and e / (1 + e), the larger one sigmoid of |g|.
+// |g| log2(e) is kept in two parts (the exponential would scale its rounding
+// up by |g|) and the base-2 exponential taken of its half and squared, so that
+// e may be subnormal, which the hardware's instruction flushes.  The hardware's
+// exponential and reciprocal are good to about 1 ulp each.
+__device__ __forceinline__ void sigmoid(float g, float& s, float& rest) {
+  constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.9259629911266175e-8f;
+  const float a = fminf(fabsf(g), 256.f);
+  const float t = a * kLog2e;
+  const float low = fmaf(a, kLog2e, -t) + a * kLog2eLow;
+  const float h = __builtin_amdgcn_exp2f(-0.5f * t);
+  const float e = h * (h * fmaf(low, -0.693147182464599609375f, 1.f));
+  const float big = __builtin_amdgcn_rcpf(1.f + e);
+  const float small = e * big;
+  s = g < 0.f ? small : big;
+  rest = g < 0.f ? big : small;
+}
+
+// A workgroup takes 256 chunks (16 bytes of each operand) of a row.
+template <typename El, bool kGrad>
+__global__ __launch_bounds__(256) void gated_act_kernel(ActArgs p) {
+  constexpr int N = El::kN;
+  const int per_row = p.I / N;
+  if (blockIdx.x == 0 && threadIdx.x < 64 && p.status &&
+      segments_bad(p.offsets, p.counts, p.E, threadIdx.x) && threadIdx.x == 0)
+    atomicOr(p.status, MOE_ERR_BAD_INDEX);
+  const int strips = (per_row + 255) / 256;
+  for (long long u = blockIdx.x; u < (long long)p.rows * strips; u += gridDim.x) {
+    const int m = (int)(u / strips);
+    const int c = (int)(u - (long long)m * strips) * 256 + threadIdx.x;
+    const bool valid = row_valid(p.offsets, p.counts, p.E, p.rows, m);
+    if (c >= per_row || (!valid && !p.zero_rest)) continue;
+    const size_t row = (size_t)p.I * El::kSize, at = (size_t)c * 16;
+    uint8_t* out = p.out + m * (kGrad ? 2 * row : row) + at;
+    if (!valid) {
+      *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
+      if (kGrad) *reinterpret_cast<uint4*>(out + row) = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint8_t* h = p.h + m * 2 * row + at;
+    float g[N], v[N], d[N];
+    El::unpack(load_chunk<true>(h, 16), g);
+    El::unpack(load_chunk<true>(h + row, 16), v);
+    if (kGrad) {
+      El::unpack(load_chunk<true>(p.dq + m * row + at, 16), d);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float s, rest;
+        sigmoid(g[i], s, rest);
+        const float gate = d[i] * v[i] * s * fmaf(g[i], rest, 1.f);
+        v[i] = d[i] * g[i] * s;
+        g[i] = gate;
+      }
+      store_chunk<true>(out, 16, El::pack(g));
+      store_chunk<true>(out + row, 16, El::pack(v));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float s, rest;
+        sigmoid(g[i], s, rest);
+        g[i] = g[i] * s * v[i];
+      }
+      store_chunk<true>(out, 16, El::pack(g));
+    }
+  }
+}
+
+template <bool kGrad>
+static moe_status_t gated_act(const ActArgs& p, int dtype, hipStream_t st) {
+  if ((dtype != MOE_TYPE_F32 && dtype != MOE_TYPE_BF16 && dtype != MOE_TYPE_F16) || p.E <= 0 ||
+      p.E > MOE_MAX_EXPERTS || p.rows < 0 || p.I <= 0)
+    return MOE_INVALID_ARG;
+  if (p.I % 8 != 0 || p.I > (1 << 28)) return MOE_UNSUPPORTED_SHAPE;
+  if (!p.offsets || !p.counts) return MOE_INVALID_ARG;
+  if (p.rows == 0) return MOE_OK;
+  if (!p.h || !p.out || (kGrad && !p.dq)) return MOE_INVALID_ARG;
+  if (((uintptr_t)p.h | (uintptr_t)p.dq | (uintptr_t)p.out) & 15) return MOE_UNSUPPORTED_SHAPE;
+  const int n = dtype == MOE_TYPE_F32 ? 4 : 8;
+  const long long units = (long long)p.rows * ((p.I / n + 255) / 256);
+  const dim3 grid((unsigned)(units < (1 << 22) ? units : (1 << 22))), block(256);
+  if (dtype == MOE_TYPE_F32)
+    hipLaunchKernelGGL((gated_act_kernel<F32, kGrad>), grid, block, 0, st, p);
+  else if (dtype == MOE_TYPE_BF16)
+    hipLaunchKernelGGL((gated_act_kernel<BF16, kGrad>), grid, block, 0, st, p);
+  else
+    hipLaunchKernelGGL((gated_act_kernel<F16, kGrad>), grid, block, 0, st, p);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status_t moe_gated_act(const void* h, int dtype, const int32_t* offsets,
+                                      const int32_t* counts, int E, int rows_total, int I, void* q,
+                                      int zero_rest, int32_t* status_dev, void* stream) {
+  const ActArgs p{static_cast<const uint8_t*>(h), nullptr, offsets, counts, E, rows_total, I,
+                  static_cast<uint8_t*>(q), zero_rest, status_dev};
+  return gated_act<false>(p, dtype, reinterpret_cast<hipStream_t>(stream));
+}
+
+extern "C" moe_status_t moe_gated_act_grad(const void* dq, const void* h, int dtype,
+                                           const int32_t* offsets, const int32_t* counts, int E,
+                                           int rows_total, int I, void* dh, int zero_rest,
+                                           int32_t* status_dev, void* stream) {
+  const ActArgs p{static_cast<const uint8_t*>(h), static_cast<const uint8_t*>(dq), offsets, counts,
+                  E, rows_total, I, static_cast<uint8_t*>(dh), zero_rest, status_dev};
+  return gated_act<true>(p, dtype, reinterpret_cast<hipStream_t>(stream));
+}

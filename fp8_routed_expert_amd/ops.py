@@ -16,6 +16,9 @@ LAYOUT_MASKED = 1
 ERR_BAD_EXPERT = 1
 ERR_OVERFLOW = 2
 ERR_BAD_INDEX = 4
+ERR_NAN = 8
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
 
 
 def _stream(stream):
@@ -635,6 +638,178 @@ def moe_act_requant_int8(h, offsets, counts, q, q_scale, status, stream=None):
           _arg(offsets, _I32, "offsets", dev, (E + 1,)), _arg(counts, _I32, "counts", dev, (E,)),
           E, R, I,
           _arg(q, _I8, "q", dev, (R, I)), _arg(q_scale, _F32, "q_scale", dev, (R,)),
+          _arg(status, _I32, "status", dev, (1,)))
+
+
+# ---- the router, the layer norm in front of it, and the experts' products and
+# activation in 32 and 16 bits, with their gradients
+def _opt(t, dtypes, name, dev, shape=None):
+    return None if t is None else _arg(t, dtypes, name, dev, shape)
+
+
+def moe_route_tokens(logits, topk_idx, topk_w, status, bias=None, score=SCORE_SOFTMAX, groups=1,
+                     top_groups=1, group_best=1, renorm=True, scale=1.0, scores=None,
+                     local_idx=None, first_expert=0, local_experts=None, stream=None):
+    """Picks topk_idx [T, K] (int32, -1: none) and weights topk_w [T, K]
+    (float32) of logits [T, E] (float32, bfloat16 or float16): the K experts
+    with the highest score + bias (float32 [E]) in the top_groups of `groups`
+    groups with the highest sum of their group_best best.  The weights are the
+    picks' scores (softmax or sigmoid), divided by their sum (renorm) and times
+    scale.  scores [T, E] float32: all scores; local_idx [T, K]: the picks
+    among experts [first_expert, first_expert + local_experts), from 0, the
+    others -1 (local_experts None: up to the last expert)."""
+    T, E = _matrix(logits, "logits")
+    K = _matrix(topk_idx, "topk_idx")[1]
+    dev = logits.get_device()
+    _call("moe_route_tokens", stream, dev, _arg(logits, _FLOATS, "logits", dev),
+          _type(logits, "logits"), T, E, _opt(bias, _F32, "bias", dev, (E,)), score, groups,
+          top_groups, group_best, K, bool(renorm), scale, first_expert,
+          E - first_expert if local_experts is None else local_experts,
+          _arg(topk_idx, _I32, "topk_idx", dev, (T, K)),
+          _opt(local_idx, _I32, "local_idx", dev, (T, K)),
+          _arg(topk_w, _F32, "topk_w", dev, (T, K)), _opt(scores, _F32, "scores", dev, (T, E)),
+          _arg(status, _I32, "status", dev, (1,)))
+
+
+def moe_route_tokens_grad(logits, topk_idx, dtopk_w, dlogits, status, score=SCORE_SOFTMAX,
+                          renorm=True, scale=1.0, dscores=None, stream=None):
+    """dlogits [T, E] (logits' dtype) from the gradients of moe_route_tokens'
+    weights (float32 [T, K]) and, where given, scores (float32 [T, E])."""
+    T, E = _matrix(logits, "logits")
+    K = _matrix(topk_idx, "topk_idx")[1]
+    dev = logits.get_device()
+    _call("moe_route_tokens_grad", stream, dev, _arg(logits, _FLOATS, "logits", dev),
+          _type(logits, "logits"), T, E, _arg(topk_idx, _I32, "topk_idx", dev, (T, K)), K, score,
+          bool(renorm), scale, _arg(dtopk_w, _F32, "dtopk_w", dev, (T, K)),
+          _opt(dscores, _F32, "dscores", dev, (T, E)),
+          _arg(dlogits, (logits.dtype,), "dlogits", dev, (T, E)),
+          _arg(status, _I32, "status", dev, (1,)))
+
+
+def _param_type(x, *params):
+    """The one type of the weights, biases and their gradients that are given
+    (x's, or float32)."""
+    types = {t.dtype for t in params if t is not None}
+    if len(types) > 1:
+        raise TypeError(f"weight and bias of different types: {types}")
+    dt = types.pop() if types else x.dtype
+    if dt not in (x.dtype, torch.float32):
+        raise TypeError(f"weight: dtype {dt}, must be x's or float32")
+    return dt
+
+
+def moe_layer_norm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
+    """y [T, H] = (x - mean) * rstd * weight + bias per row of x (float32,
+    bfloat16 or float16); weight, bias [H] of x's type or float32, or None.
+    mean, rstd [T] float32: what the gradient reads."""
+    T, H = _matrix(x, "x")
+    code = _type(x, "x")
+    wt = _param_type(x, weight, bias)
+    dev = x.get_device()
+    _call("moe_layer_norm", stream, dev, _arg(x, _FLOATS, "x", dev), code, T, H,
+          _opt(weight, (wt,), "weight", dev, (H,)), _opt(bias, (wt,), "bias", dev, (H,)),
+          _TYPES[wt], eps, _arg(y, (x.dtype,), "y", dev, (T, H)),
+          _opt(mean, _F32, "mean", dev, (T,)), _opt(rstd, _F32, "rstd", dev, (T,)))
+
+
+def moe_layer_norm_workspace_bytes(T, H):
+    return int(load().moe_layer_norm_workspace_bytes(int(T), int(H)))
+
+
+def moe_layer_norm_grad(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, stream=None):
+    """Gradients of moe_layer_norm: dx [T, H], dweight and dbias [H] (of the
+    weight's type), each None where it is not wanted; workspace (uint8) holds
+    moe_layer_norm_workspace_bytes(T, H) bytes."""
+    T, H = _matrix(x, "x")
+    code = _type(x, "x")
+    wt = _param_type(x, weight, dweight, dbias)
+    dev = x.get_device()
+    if dx is None and dweight is None and dbias is None:
+        raise ValueError("moe_layer_norm_grad: none of dx, dweight and dbias is given")
+    _call("moe_layer_norm_grad", stream, dev, _arg(dy, (x.dtype,), "dy", dev, (T, H)),
+          _arg(x, _FLOATS, "x", dev), code, T, H, _opt(weight, (wt,), "weight", dev, (H,)),
+          _TYPES[wt], _arg(mean, _F32, "mean", dev, (T,)), _arg(rstd, _F32, "rstd", dev, (T,)),
+          _opt(dx, (x.dtype,), "dx", dev, (T, H)), _opt(dweight, (wt,), "dweight", dev, (H,)),
+          _opt(dbias, (wt,), "dbias", dev, (H,)), _arg(workspace, (torch.uint8,), "workspace", dev),
+          workspace.numel())
+
+
+def moe_grouped_gemm_float(a, w, offsets, counts, c, status, zero_rest=False, stream=None):
+    """c[valid rows] = a [rows_total, K] with w[expert] [N, K] in float32,
+    bfloat16 or float16; other rows of c are left as they are, or set to zero."""
+    E, N, K = _experts(w)
+    R = _matrix(a, "a")[0]
+    code = _type(a, "a")
+    dev = a.get_device()
+    _call("moe_grouped_gemm_float", stream, dev, _arg(a, (a.dtype,), "a", dev, (R, K)),
+          _arg(w, (a.dtype,), "w", dev), code, _arg(offsets, _I32, "offsets", dev, (E + 1,)),
+          _arg(counts, _I32, "counts", dev, (E,)), E, R, N, K,
+          _arg(c, (a.dtype,), "c", dev, (R, N)), bool(zero_rest),
+          _arg(status, _I32, "status", dev, (1,)))
+
+
+def moe_grouped_gemm_float_grad_rows(dc, w, offsets, counts, da, status, zero_rest=False,
+                                     stream=None):
+    """da[valid rows] = dc [rows_total, N] with w[expert] [N, K] over N: the
+    gradient of moe_grouped_gemm_float with respect to a."""
+    E, N, K = _experts(w)
+    R = _matrix(dc, "dc")[0]
+    code = _type(dc, "dc")
+    dev = dc.get_device()
+    _call("moe_grouped_gemm_float_grad_rows", stream, dev,
+          _arg(dc, (dc.dtype,), "dc", dev, (R, N)), _arg(w, (dc.dtype,), "w", dev), code,
+          _arg(offsets, _I32, "offsets", dev, (E + 1,)), _arg(counts, _I32, "counts", dev, (E,)),
+          E, R, N, K, _arg(da, (dc.dtype,), "da", dev, (R, K)), bool(zero_rest),
+          _arg(status, _I32, "status", dev, (1,)))
+
+
+def moe_grouped_gemm_float_workspace_bytes(E, rows_total, N, K):
+    return int(load().moe_grouped_gemm_float_workspace_bytes(int(E), int(rows_total), int(N),
+                                                             int(K)))
+
+
+def moe_grouped_gemm_float_grad_weights(dc, a, offsets, counts, dw, workspace, status,
+                                        stream=None):
+    """dw [E, N, K] (a's type or float32) = the sums over each expert's valid
+    rows of dc [rows_total, N] times a [rows_total, K]: the gradient of
+    moe_grouped_gemm_float with respect to w; workspace (uint8) holds
+    moe_grouped_gemm_float_workspace_bytes(E, rows_total, N, K) bytes."""
+    E, N, K = _experts(dw)
+    R = _matrix(a, "a")[0]
+    code = _type(a, "a")
+    dev = a.get_device()
+    _call("moe_grouped_gemm_float_grad_weights", stream, dev,
+          _arg(dc, (a.dtype,), "dc", dev, (R, N)), _arg(a, (a.dtype,), "a", dev, (R, K)), code,
+          _arg(offsets, _I32, "offsets", dev, (E + 1,)), _arg(counts, _I32, "counts", dev, (E,)),
+          E, R, N, K, _arg(dw, (a.dtype, torch.float32), "dw", dev), _type(dw, "dw"),
+          _arg(workspace, (torch.uint8,), "workspace", dev), workspace.numel(),
+          _arg(status, _I32, "status", dev, (1,)))
+
+
+def moe_gated_act(h, offsets, counts, q, status, zero_rest=False, stream=None):
+    """q [rows_total, I] = silu(h[:, :I]) * h[:, I:] for the valid rows of
+    h [rows_total, 2I] (float32, bfloat16 or float16)."""
+    R, I = _matrix(q, "q")
+    E = _count(counts, "counts")
+    code = _type(h, "h")
+    dev = h.get_device()
+    _call("moe_gated_act", stream, dev, _arg(h, (h.dtype,), "h", dev, (R, 2 * I)), code,
+          _arg(offsets, _I32, "offsets", dev, (E + 1,)), _arg(counts, _I32, "counts", dev), E, R,
+          I, _arg(q, (h.dtype,), "q", dev), bool(zero_rest),
+          _arg(status, _I32, "status", dev, (1,)))
+
+
+def moe_gated_act_grad(dq, h, offsets, counts, dh, status, zero_rest=False, stream=None):
+    """dh [rows_total, 2I] from dq [rows_total, I]: the gradient of
+    moe_gated_act."""
+    R, I = _matrix(dq, "dq")
+    E = _count(counts, "counts")
+    code = _type(h, "h")
+    dev = h.get_device()
+    _call("moe_gated_act_grad", stream, dev, _arg(dq, (h.dtype,), "dq", dev),
+          _arg(h, (h.dtype,), "h", dev, (R, 2 * I)), code,
+          _arg(offsets, _I32, "offsets", dev, (E + 1,)), _arg(counts, _I32, "counts", dev), E, R,
+          I, _arg(dh, (h.dtype,), "dh", dev, (R, 2 * I)), bool(zero_rest),
           _arg(status, _I32, "status", dev, (1,)))
 
 

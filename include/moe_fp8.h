@@ -80,6 +80,11 @@ typedef int32_t moe_status_t;
 #define MOE_ERR_BAD_EXPERT 1 /* topk id outside [-1, E): entry skipped     */
 #define MOE_ERR_OVERFLOW 2   /* row did not fit: dropped in stable order  */
 #define MOE_ERR_BAD_INDEX 4  /* slot / offset outside a buffer: skipped   */
+#define MOE_ERR_NAN 8        /* a logit or bias is NaN: expert not picked */
+
+/* the router's scores */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
 
 #define MOE_MAX_EXPERTS 1024
 #define MOE_MAX_TOPK 64
@@ -559,6 +564,151 @@ size_t moe_linear_int8_workspace_bytes(int M, int K);
 moe_status_t moe_linear_int8(const void* x, int dtype, const int8_t* w, const float* w_scale,
                              int M, int N, int K, void* c, int c_type, void* workspace,
                              size_t workspace_bytes, void* stream);
+
+/*
+ * The router [H100-EP 基于 DeepEP 的专家并行: tokens are shuffled to the experts
+ * that their router picked]: a token's logits l [E] (type dtype) to the K
+ * experts it goes to and their weights, as moe_sort_tokens and
+ * moe_combine_rows take them.
+ *
+ *   scores   softmax  s_e = exp(l_e) / sum_f exp(l_f)
+ *            sigmoid  s_e = 1 / (1 + exp(-l_e))
+ *   keys     s_e + bias_e (f32 [E], NULL: 0): the bias balances the load, it
+ *            does not enter the weights
+ *   groups   the experts are `groups` runs of E / groups; a group's score is
+ *            the sum of its group_best (1 or 2) highest keys; the top_groups
+ *            groups with the highest score are kept (groups = top_groups = 1:
+ *            all)
+ *   picks    the K highest keys in the kept groups, in descending order; on a
+ *            tie, of groups as of experts, the lowest index comes first
+ *   weights  w_k = scale * s_k, with renorm != 0 divided by
+ *            max(sum_j s_j, 2^-64)
+ *
+ * An expert whose logit is -infinity (a masked expert; all of them: a padding
+ * token) has the score 0 and is not picked, and neither is one whose bias is
+ * -infinity (its key is -infinity, in its group's score too); a logit or bias
+ * of NaN counts as -infinity and sets MOE_ERR_NAN.  A logit of +infinity
+ * counts as the largest fp32 number.  Where fewer than K experts are left the
+ * other picks are -1 with the weight 0.  Keys are compared in 64 bits; scores
+ * and weights are rounded to fp32 once.
+ *
+ *   topk_idx  [T, K] int32  picks, as indices of all E experts
+ *   local_idx [T, K] int32 or NULL: pick - first_expert for picks in
+ *             [first_expert, first_expert + local_experts), -1 for others:
+ *             what moe_sort_tokens takes where a GPU holds those experts
+ *   topk_w    [T, K] f32
+ *   scores    [T, E] f32 or NULL: s, for a loss that balances the load
+ *
+ * moe_route_tokens_grad gives dlogits [T, E] (of dtype, rounded once) from the
+ * gradients of the weights (dtopk_w [T, K] f32; not read where the pick is -1)
+ * and of the scores (dscores [T, E] f32 or NULL), through the weights'
+ * normalisation and the scores; picks are constants.  It is 0 for logits of
+ * -infinity and NaN.  A pick outside [-1, E) is skipped and sets
+ * MOE_ERR_BAD_EXPERT; one that a token names twice counts twice.
+ *
+ * E <= MOE_MAX_EXPERTS and a multiple of groups, K <= MOE_MAX_TOPK and <= E.
+ */
+moe_status_t moe_route_tokens(const void* logits, int dtype, int T, int E, const float* bias,
+                              int score, int groups, int top_groups, int group_best, int K,
+                              int renorm, float scale, int first_expert, int local_experts,
+                              int32_t* topk_idx, int32_t* local_idx, float* topk_w,
+                              float* scores, int32_t* status_dev, void* stream);
+moe_status_t moe_route_tokens_grad(const void* logits, int dtype, int T, int E,
+                                   const int32_t* topk_idx, int K, int score, int renorm,
+                                   float scale, const float* dtopk_w, const float* dscores,
+                                   void* dlogits, int32_t* status_dev, void* stream);
+
+/*
+ * Layer norm of the rows that go into the router and the experts, and its
+ * gradient.  For every row of x [T, H] (any H >= 1):
+ *
+ *   mean = sum_h x_h / H,  rstd = 1 / sqrt(sum_h (x_h - mean)^2 / H + eps)
+ *   y_h = round((x_h - mean) * rstd * weight_h + bias_h)
+ *
+ *   with g_h = dy_h * weight_h and z_h = (x_h - mean) * rstd:
+ *   dx_h = round(rstd * (g_h - sum_j g_j / H - z_h * sum_j g_j z_j / H))
+ *   dweight_h = round(sum_t dy_th z_th),  dbias_h = round(sum_t dy_th)
+ *
+ * Everything is held in fp32 and rounded once, to nearest even; sums have a
+ * fixed order (no atomics: the same call gives the same bits).  T = 0 gives
+ * zero gradients.  A row with an infinity or a NaN gives NaN.
+ *
+ *   x, y, dy, dx [T, H]  of dtype (MOE_TYPE_F32, _BF16 or _F16)
+ *   weight, bias, dweight, dbias [H]  of w_dtype: dtype or MOE_TYPE_F32;
+ *            weight NULL: 1, bias NULL: 0
+ *   mean, rstd [T] f32   written by moe_layer_norm (each may be NULL there),
+ *            read by the gradient
+ *   eps      >= 0
+ *   dx, dweight, dbias   each may be NULL (not computed), not all
+ *   workspace  moe_layer_norm_workspace_bytes(T, H) bytes, 16-byte aligned;
+ *            what the call leaves there is unspecified.  Calls (or captured
+ *            graphs) that may run at the same time need one each.
+ * Buffers are aligned to their element.  Outputs may not overlap inputs.
+ */
+moe_status_t moe_layer_norm(const void* x, int dtype, int T, int H, const void* weight,
+                            const void* bias, int w_dtype, float eps, void* y, float* mean,
+                            float* rstd, void* stream);
+size_t moe_layer_norm_workspace_bytes(int T, int H);
+moe_status_t moe_layer_norm_grad(const void* dy, const void* x, int dtype, int T, int H,
+                                 const void* weight, int w_dtype, const float* mean,
+                                 const float* rstd, void* dx, void* dweight, void* dbias,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The experts' products in 32- and 16-bit types with their gradients, for
+ * experts that are trained or kept in those types (the counterparts of
+ * moe_grouped_gemm_fp8 and _int8), and the gated activation between them.
+ * For the valid rows m of expert e:
+ *
+ *   moe_grouped_gemm_float               c[m, n] = round(sum_k a[m, k] * w[e, n, k])
+ *   moe_grouped_gemm_float_grad_rows     da[m, k] = round(sum_n dc[m, n] * w[e, n, k])
+ *   moe_grouped_gemm_float_grad_weights  dw[e, n, k] = round(sum over the valid rows m
+ *                                                      of e of dc[m, n] * a[m, k])
+ *   moe_gated_act       q[m, j] = round(silu(h[m, j]) * h[m, I + j]),
+ *                       silu(g) = g * s(g), s(g) = 1 / (1 + exp(-g))
+ *   moe_gated_act_grad  dh[m, j] = round(dq[m, j] * h[m, I + j] * s * (1 + g * (1 - s)))
+ *                       dh[m, I + j] = round(dq[m, j] * g * s),  g = h[m, j], s = s(g)
+ *
+ * Sums are fp32 on the matrix cores, rounded once, to nearest even; the
+ * activation is fp32 (exp and reciprocal from the hardware, ~1 ulp each).  The
+ * same call gives the same bits.  Only valid rows are read; other rows of the
+ * outputs are left as they are, or set to zero with zero_rest != 0.  An expert
+ * without valid rows gets dw = 0.
+ *
+ *   a, da [rows_total, K]   c, dc [rows_total, N]   w, dw [E, N, K]
+ *   h, dh [rows_total, 2I]  q, dq [rows_total, I]
+ *   dtype    MOE_TYPE_F32, _BF16 or _F16, of everything but dw
+ *   dw_type  dtype or MOE_TYPE_F32
+ *   workspace  moe_grouped_gemm_float_workspace_bytes(E, rows_total, N, K) bytes
+ *            (may be 0), 16-byte aligned; what the call leaves there is
+ *            unspecified.  Calls (or captured graphs) that may run at the same
+ *            time need one each.
+ * N, K and I must be multiples of 8, N and K at most 2^20, I at most 2^28;
+ * matrices 16-byte aligned; a launch holds 2^32 threads: MOE_UNSUPPORTED_SHAPE
+ * otherwise.  offsets / counts / status_dev as for moe_grouped_gemm_fp8.
+ * Outputs may not overlap inputs.
+ */
+moe_status_t moe_grouped_gemm_float(const void* a, const void* w, int dtype,
+                                    const int32_t* offsets, const int32_t* counts, int E,
+                                    int rows_total, int N, int K, void* c, int zero_rest,
+                                    int32_t* status_dev, void* stream);
+moe_status_t moe_grouped_gemm_float_grad_rows(const void* dc, const void* w, int dtype,
+                                              const int32_t* offsets, const int32_t* counts,
+                                              int E, int rows_total, int N, int K, void* da,
+                                              int zero_rest, int32_t* status_dev, void* stream);
+size_t moe_grouped_gemm_float_workspace_bytes(int E, int rows_total, int N, int K);
+moe_status_t moe_grouped_gemm_float_grad_weights(const void* dc, const void* a, int dtype,
+                                                 const int32_t* offsets, const int32_t* counts,
+                                                 int E, int rows_total, int N, int K, void* dw,
+                                                 int dw_type, void* workspace,
+                                                 size_t workspace_bytes, int32_t* status_dev,
+                                                 void* stream);
+moe_status_t moe_gated_act(const void* h, int dtype, const int32_t* offsets,
+                           const int32_t* counts, int E, int rows_total, int I, void* q,
+                           int zero_rest, int32_t* status_dev, void* stream);
+moe_status_t moe_gated_act_grad(const void* dq, const void* h, int dtype, const int32_t* offsets,
+                                const int32_t* counts, int E, int rows_total, int I, void* dh,
+                                int zero_rest, int32_t* status_dev, void* stream);
 
 /*
  * Measurement helpers (not steps of the layer).  They time the two
