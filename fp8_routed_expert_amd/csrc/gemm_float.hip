@@ -31,35 +31,13 @@ struct FloatArgs {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// sums += 16 x 16 x 32 products of eight elements per lane: lane (g, r) holds
-// elements l = 8 g .. 8 g + 7 of row r of each operand (in fp32 an instruction
-// takes one element of every lane: l = 8 g + i, the same for both operands).
-template <int kType, typename Frag>
-__device__ __forceinline__ v4f multiply8(const Frag& a, const Frag& b, v4f c) {
-  if constexpr (kType == MOE_TYPE_F32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
-    return c;
-  } else if constexpr (kType == MOE_TYPE_BF16) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  } else {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-  }
-}
-
-template <int kType>
-using Elem = std::conditional_t<kType == MOE_TYPE_F32, float, uint16_t>;
-template <int kType>
-using Frag8 = std::conditional_t<kType == MOE_TYPE_F32, float __attribute__((ext_vector_type(8))),
-                                 uint16_t __attribute__((ext_vector_type(8)))>;
-
-// A 64 x 64 tile by four waves of 32 x 32, l advancing 32 a step through LDS.
-template <int kType, int kMode>
+// fp32: a 64 x 64 tile by four waves of 32 x 32, l advancing 32 a step through
+// LDS.  A lane's fragment is eight values of l of one row; an instruction takes
+// one of them from every lane, the same one of both operands.
+template <int kMode>
 __global__ __launch_bounds__(256) void float_tile_kernel(FloatArgs p) {
-  typedef Elem<kType> El;
-  typedef Frag8<kType> Frag;
+  typedef float El;
+  typedef float Frag __attribute__((ext_vector_type(8)));
   constexpr int BM = 64, BN = 64, BL = 32, kPitch = BL + 8;
   __shared__ __attribute__((aligned(16))) El sp[BM][kPitch], sq[BN][kPitch];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -131,7 +109,10 @@ __global__ __launch_bounds__(256) void float_tile_kernel(FloatArgs p) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) acc[u][v] = multiply8<kType>(fq[v], fp[u], acc[u][v]);
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          acc[u][v] = __builtin_amdgcn_mfma_f32_16x16x4f32(fq[v][i], fp[u][i], acc[u][v], 0, 0, 0);
   }
   // sums (u, v) of a lane: row r16 of P, four neighbours 4 g .. 4 g + 3 of Q
 #pragma unroll
@@ -142,21 +123,420 @@ __global__ __launch_bounds__(256) void float_tile_kernel(FloatArgs p) {
       if (i >= i_end || j >= j_end) continue;
       const size_t at = ((kMode == kWeightsGrad ? (size_t)e * p.N : 0) + i) * width + j;
       const v4f s = acc[u][v];
-      if (p.out_type == MOE_TYPE_F32) {
-        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) =
-            make_float4(s[0], s[1], s[2], s[3]);
-      } else {
-        uint2 o;
-        if (kType == MOE_TYPE_F16) {
-          typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-          o.x = __builtin_bit_cast(uint32_t, (h2){(_Float16)s[0], (_Float16)s[1]});
-          o.y = __builtin_bit_cast(uint32_t, (h2){(_Float16)s[2], (_Float16)s[3]});
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) =
+          make_float4(s[0], s[1], s[2], s[3]);
+    }
+}
+
+template <int i>
+using Int = std::integral_constant<int, i>;
+
+// f(Int<a>), ..., f(Int<b - 1>)
+template <int a, int b, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (a < b) {
+    f(Int<a>());
+    each<a + 1, b>(f);
+  }
+}
+
+// Stage i of an operand: an LDS object of its own, so that accesses to one
+// are known not to touch another.
+template <int kBytes, int kOperand, int i>
+struct Stage {
+  __device__ __forceinline__ static uint8_t* get() {
+    __shared__ __attribute__((aligned(1024))) uint8_t s[kBytes];
+    return s;
+  }
+};
+
+constexpr uint32_t kOutOfRange = 0x80000000u;
+
+// An operand of a 16-bit tile, B rows of 64 l (a step) in 128 B bytes of LDS.
+//
+// Contiguous along l (kSlow false): as the 8-bit products have it, a row of
+// the tile is 128 bytes of LDS, its 16-byte pieces permuted (swz), and a lane's
+// fragment is pieces 2 g and 2 g + 1: l = 16 g .. 16 g + 15.
+//
+// Contiguous along the rows (kSlow true): the step's 64 values of l are lines
+// of 2 B bytes.  Line 16 u + 4 t + g of the stage holds l = 16 g + 4 u + t, so
+// that the four lines t of a group of 16 lanes, which ds_read_b64_tr_b16 turns
+// into four l of 16 rows, belong to the same g as the other operand's fragment.
+// Those 16 lanes read 32 bytes of each of the lines t = 0 .. 3, and the group
+// next to them (g + 1) of four others: the 32-byte columns of a line are
+// permuted by 2 t + g % 2 (64-byte-row lines: by t; neighbours then lie in
+// other banks by themselves), so the eight lines lie in different banks.
+template <int B, bool kSlow>
+struct Operand {
+  static constexpr int kLine = 2 * B;             // bytes of a line (slow)
+  static constexpr int kPieces = kLine / 16;      // of a line
+  static constexpr int kReads = kSlow ? 4 : 2;    // LDS reads of a fragment
+  uint32_t vl[2];     // a lane's offset in a chunk's memory, by the chunk's parity
+  int lim[2];         // (along l) l's left behind the lane's piece, in bytes
+  FragLane frag;      // (slow: lo only)
+  // slow: the rest of the matrix, from this step's first line on
+  uint64_t base;
+  long long bytes;
+  long long step;
+  v4i rsrc;
+
+  // pitch: bytes from a row of memory to the next; w0: the wave's first row
+  __device__ __forceinline__ void lanes(int lane, uint32_t pitch, int L, int w0) {
+    const int g = lane >> 4, r16 = lane & 15;
+    if constexpr (!kSlow) {
+      const int piece = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        vl[o] = (uint32_t)(lane >> 3) * pitch + (uint32_t)((piece ^ o) << 4);
+        lim[o] = 2 * L - ((piece ^ o) << 4);
+      }
+      frag = frag_lane(w0, r16, g);
+    } else {
+      const int at = lane % kPieces, line = lane / kPieces;
+      if constexpr (B == 256) {        // lines g % 2
+        vl[0] = vl[1] = (uint32_t)line * 16u * pitch + (uint32_t)((at ^ (2 * line)) << 4);
+      } else if constexpr (B == 128) { // lines g
+        vl[0] = vl[1] = (uint32_t)line * 16u * pitch + (uint32_t)((at ^ (2 * (line & 1))) << 4);
+      } else {                         // lines 4 (t % 2) + g
+        const int tl = line >> 2;
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+          vl[o] = (uint32_t)(line & 3) * 16u * pitch + (uint32_t)tl * pitch +
+                  (uint32_t)((at ^ (2 * (2 * o + tl))) << 4);
+      }
+      const int t = r16 >> 2, q = r16 & 3;
+      const int sl = B >= 128 ? (g & 1) | (t << 1) : t;
+      const uint32_t in = (uint32_t)((4 * t + g) * kLine + sl * 32 + (q >> 1) * 16 + (q & 1) * 8);
+      const int w = w0 / 16;
+      frag.lo = (in ^ (uint32_t)((w & 7) * 32)) + (uint32_t)((w >> 3) * 256);
+      frag.hi = 0;
+    }
+  }
+  // the tile's memory: first element, and the bytes from there to the end of
+  // what may be read
+  __device__ __forceinline__ void tile(const void* p, long long n, uint32_t pitch) {
+    if constexpr (!kSlow) {
+      rsrc = make_rsrc(p, (uint32_t)(n > 0x7ffff000LL ? 0x7ffff000LL : n));
+    } else {
+      base = (uint64_t)(uintptr_t)p;
+      bytes = n;
+      step = 64LL * pitch;
+    }
+  }
+  // chunks [wave * kC, wave * kC + kC) of step kb into its stage; steps are
+  // issued in order
+  template <int kC, bool kRagged>
+  __device__ __forceinline__ void issue(int kb, uint8_t* stage, int wave, uint32_t pitch,
+                                        bool live) {
+    if constexpr (!kSlow) {
+#pragma unroll
+      for (int u = 0; u < kC; ++u) {
+        const int c = wave * kC + u;
+        const int o = kC % 2 == 0 ? (u & 1) : (c & 1);
+        const uint32_t uni = (uint32_t)(c * 8) * pitch + (uint32_t)kb * kBK;
+        if constexpr (kRagged) {
+          const bool in = live && kb * kBK < lim[o];
+          dma16(rsrc, stage + c * 1024, in ? (o ? vl[1] : vl[0]) + uni : kOutOfRange);
         } else {
-          o = make_uint2(pack2_bf16(s[0], s[1]), pack2_bf16(s[2], s[3]));
+          dma16_add(rsrc, stage + c * 1024, o ? vl[1] : vl[0],
+                    __builtin_amdgcn_readfirstlane(live ? uni : kOutOfRange));
         }
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + at) = o;
+      }
+    } else {
+      // (past the last step nothing is left: the loads read zeros)
+      const long long left = bytes < 0 ? 0 : bytes > 0x7ffff000LL ? 0x7ffff000LL : bytes;
+      const v4i r = make_rsrc(reinterpret_cast<const void*>((uintptr_t)base), (uint32_t)left);
+#pragma unroll
+      for (int u = 0; u < kC; ++u) {
+        const int c = wave * kC + u;
+        if constexpr (B == 256) {
+          const uint32_t t = (uint32_t)((c >> 1) & 3);
+          dma16_split(r, stage + c * 1024, vl[0], __builtin_amdgcn_readfirstlane(t * 64u),
+                      __builtin_amdgcn_readfirstlane(
+                          (uint32_t)(32 * (c & 1) + 4 * (c >> 3)) * pitch + t * pitch));
+        } else if constexpr (B == 128) {
+          const uint32_t t = (uint32_t)(c & 3);
+          dma16_split(r, stage + c * 1024, vl[0], __builtin_amdgcn_readfirstlane(t * 64u),
+                      __builtin_amdgcn_readfirstlane((uint32_t)(4 * (c >> 2)) * pitch + t * pitch));
+        } else {
+          dma16_add(r, stage + c * 1024, (kC % 2 == 0 ? u & 1 : c & 1) ? vl[1] : vl[0],
+                    __builtin_amdgcn_readfirstlane((uint32_t)(4 * (c >> 1) + 2 * (c & 1)) * pitch));
+        }
+      }
+      base += (uint64_t)step;
+      bytes -= step;
+    }
+  }
+  // the fragment of the wave's 16-row subtile i
+  __device__ __forceinline__ v8i load(const uint8_t* stage, int i) const {
+    if constexpr (!kSlow) {
+      return load_frag_at(stage, i * 16 * kBK, frag);
+    } else {
+      typedef short s4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) s4 lds_s4;
+      const uint8_t* at = stage + (frag.lo ^ (uint32_t)(i * 32));
+      v8i r;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const s4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s4*)(lds_void*)(at + u * 16 * kLine));
+        const uint2 w = __builtin_bit_cast(uint2, v);
+        r[2 * u] = (int)w.x;
+        r[2 * u + 1] = (int)w.y;
+      }
+      return r;
+    }
+  }
+  __device__ __forceinline__ void fresh() {
+    asm volatile("" : "+v"(frag.lo));
+    if constexpr (!kSlow) asm volatile("" : "+v"(frag.hi));
+  }
+};
+
+template <int kType>
+__device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
+  if constexpr (kType == MOE_TYPE_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, (h2){(_Float16)lo, (_Float16)hi});
+}
+
+// The 16-bit products: a BM x BN tile by waves of WM x WN, l advancing 64 a
+// step.  The operands go from global memory straight into LDS, P's a step
+// further ahead than Q's; the pipeline is that of the 8-bit products (waits and
+// barriers are explained there): the next step's loads go out first, the step's
+// barrier comes once a wave's last LDS read of it has landed, and the next
+// step's fragments are read under the last subtile row's multiplications.
+// kDeep: 0, or the stages of both operands for launches of few tiles.
+template <int kType, int kMode, int BM, int BN, int WM, int WN, int GM, int kDeep, bool kRagged>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void half_tile_kernel(FloatArgs p) {
+  constexpr int NWN = BN / WN;
+  constexpr int NW = BM / WM * NWN;
+  constexpr int MI = WM / 16, NJ = WN / 16;
+  constexpr int CA = BM / 8 / NW, CB = BN / 8 / NW;   // 1 KB chunks of a stage per wave
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "chunks must split evenly");
+  static_assert(MI >= 2 && NJ == 4, "late loads; a wave's stores are whole pieces");
+  constexpr int SA_B = BM * kBK, SB_B = BN * kBK;
+  constexpr int NSA = kDeep ? kDeep : 3 * SA_B + 2 * SB_B <= kLdsBytes ? 3 : 2;
+  constexpr int NSB = kDeep ? kDeep : 2;
+  static_assert(NSA * SA_B + NSB * SB_B <= kLdsBytes, "tile stages exceed the LDS");
+  static_assert(6 % NSA == 0 && 6 % NSB == 0, "the loop over l is unrolled by 6");
+  auto stA = [&](auto i) { return Stage<SA_B, 0, decltype(i)::value % NSA>::get(); };
+  auto stB = [&](auto i) { return Stage<SB_B, 1, decltype(i)::value % NSB>::get(); };
+
+  // ---- which tile: columns within groups of GM row tiles
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int width = kMode == kProduct ? p.N : p.K;
+  if (blockIdx.x == 0 && threadIdx.x < 64 && p.status &&
+      segments_bad(p.offsets, p.counts, p.E, lane) && lane == 0)
+    atomicOr(p.status, MOE_ERR_BAD_INDEX);
+  const int n_tiles = (width + BN - 1) / BN;
+  const int i_tiles = (p.N + BM - 1) / BM;   // of an expert's weights
+  const int total_m = kMode == kWeightsGrad
+                          ? p.E * i_tiles
+                          : total_mtiles<BM>(p.offsets, p.counts, p.E, p.rows, lane);
+  if ((long long)blockIdx.x >= (long long)total_m * n_tiles) return;
+  const int group = (int)blockIdx.x / (GM * n_tiles);
+  const int in_group = (int)blockIdx.x - group * (GM * n_tiles);
+  const int gm_cnt = min(GM, total_m - group * GM);
+  const int tile_n = in_group / gm_cnt;
+  const int tile_m = group * GM + (in_group - tile_n * gm_cnt);
+  const int n0 = tile_n * BN;
+  int e, row0, row_end, L, s0 = 0;   // rows of P and of the output; s0: the segment's first row
+  if (kMode == kWeightsGrad) {
+    int en;
+    e = tile_m / i_tiles;
+    expert_rows(p.offsets, p.counts, e, p.rows, s0, en);
+    s0 = __builtin_amdgcn_readfirstlane(s0);
+    L = __builtin_amdgcn_readfirstlane(en) - s0;
+    row0 = (tile_m - e * i_tiles) * BM;
+    row_end = p.N;
+  } else {
+    find_mtile<BM>(p.offsets, p.counts, p.E, p.rows, tile_m, lane, e, row0, row_end);
+    if (e < 0) return;
+    L = kMode == kProduct ? p.K : p.N;
+  }
+
+  // ---- operands
+  constexpr bool kSlowA = kMode == kWeightsGrad, kSlowB = kMode != kProduct;
+  Operand<BM, kSlowA> A;
+  Operand<BN, kSlowB> B;
+  const uint32_t pitch_a = 2u * (uint32_t)(kMode == kProduct ? p.K : p.N);
+  const uint32_t pitch_b = 2u * (uint32_t)p.K;
+  const int wm = wave / NWN, wn = wave - wm * NWN;
+  A.lanes(lane, pitch_a, L, wm * WM);
+  B.lanes(lane, pitch_b, L, wn * WN);
+  if constexpr (kMode == kWeightsGrad)
+    A.tile(p.p + (size_t)s0 * pitch_a + 2 * row0, (long long)L * pitch_a - 2 * row0, pitch_a);
+  else
+    A.tile(p.p + (size_t)row0 * pitch_a, (long long)(p.rows - row0) * pitch_a, pitch_a);
+  const uint8_t* we = p.q + (size_t)e * p.N * pitch_b;
+  if constexpr (kMode == kProduct)
+    B.tile(we + (size_t)n0 * pitch_b, (long long)min(BN, p.N - n0) * pitch_b, pitch_b);
+  else if constexpr (kMode == kRowsGrad)
+    B.tile(we + 2 * n0, (long long)L * pitch_b - 2 * n0, pitch_b);
+  else
+    B.tile(p.q + (size_t)s0 * pitch_b + 2 * n0, (long long)L * pitch_b - 2 * n0, pitch_b);
+  const int Lb = (L + 63) / 64;
+  auto issue_a = [&](int kb, uint8_t* st) {
+    A.template issue<CA, kRagged>(kb, st, wave, pitch_a, kb < Lb);
+  };
+  auto issue_b = [&](int kb, uint8_t* st) {
+    B.template issue<CB, kRagged>(kb, st, wave, pitch_b, kb < Lb);
+  };
+
+  v4f acc[MI][NJ] = {};
+  v8i bf[NJ];
+  v8i af_next;
+  auto lo = [](const v8i& v) { return (v4i){v[0], v[1], v[2], v[3]}; };
+  auto hi = [](const v8i& v) { return (v4i){v[4], v[5], v[6], v[7]}; };
+  auto subtile = [&](int i, int j, bool hi_first, const v8i& af) __attribute__((always_inline)) {
+    if (hi_first) {
+      acc[i][j] = mfma16<kType>(hi(bf[j]), hi(af), acc[i][j]);
+      acc[i][j] = mfma16<kType>(lo(bf[j]), lo(af), acc[i][j]);
+    } else {
+      acc[i][j] = mfma16<kType>(lo(bf[j]), lo(af), acc[i][j]);
+      acc[i][j] = mfma16<kType>(hi(bf[j]), hi(af), acc[i][j]);
+    }
+  };
+  constexpr int kLateRow = MI >= 3 ? 1 : 0;
+  constexpr int kInFlight = kDeep ? (kDeep - 2) * (CA + CB) : NSA == 3 ? CA : 0;
+  auto step = [&](int kb, auto unrolled) __attribute__((always_inline)) {
+    constexpr int U = decltype(unrolled)::value;
+    A.fresh();
+    B.fresh();
+    const uint8_t* tA = stA(Int<U>());
+    const uint8_t* tAn = stA(Int<U + 1>());
+    const uint8_t* tBn = stB(Int<U + 1>());
+    issue_b(kb + NSB - 1, stB(Int<U + NSB - 1>()));
+#pragma unroll
+    for (int i = 0; i < MI - 1; ++i) {
+      if (i == kLateRow) issue_a(kb + NSA - 1, stA(Int<U + NSA - 1>()));
+      const v8i af = af_next;
+      af_next = A.load(tA, i + 1);
+#pragma unroll
+      for (int jj = 0; jj < NJ; ++jj) {
+        subtile(i, (i & 1) ? NJ - 1 - jj : jj, jj & 1, af);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+#pragma unroll
+    for (int i = 0; i < MI - 1; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(acc[i][j]));
+    wait_vm<kInFlight>();
+    lds_barrier();
+    const v8i af = af_next;
+#pragma unroll
+    for (int jj = 0; jj < NJ; ++jj) {
+      const int j = (MI & 1) ? jj : NJ - 1 - jj;
+      subtile(MI - 1, j, jj & 1, af);
+      bf[j] = B.load(tBn, j);
+    }
+    af_next = A.load(tAn, 0);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, Operand<BN, kSlowB>::kReads, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, Operand<BM, kSlowA>::kReads, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(acc[MI - 1][j]));
+  };
+
+  issue_b(0, stB(Int<0>()));
+  issue_a(0, stA(Int<0>()));
+  if constexpr (kDeep != 0) {
+    each<1, kDeep - 1>([&](auto i) {
+      issue_b(decltype(i)::value, stB(i));
+      issue_a(decltype(i)::value, stA(i));
+    });
+  } else if constexpr (NSA == 3) {
+    issue_a(1, stA(Int<1>()));
+  }
+  wait_vm<kInFlight>();
+  lds_barrier();
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) bf[j] = B.load(stB(Int<0>()), j);
+  af_next = A.load(stA(Int<0>()), 0);
+  for (int kb = 0; kb < Lb; kb += 6)
+    each<0, 6>([&](auto u) __attribute__((always_inline)) {
+      constexpr int U = decltype(u)::value;
+      if (U == 0 || kb + U < Lb) step(kb + U, u);
+    });
+  wait_vm<0>();   // (the loads past the last step)
+
+  // ---- epilogue: sums (i, j) of a lane are four columns 4 g .. 4 g + 3 of row
+  // r16.  In 16 bits two subtiles' halves are exchanged between neighbouring
+  // rows of 16 lanes, so that a lane holds eight columns, then lanes of rows
+  // 0..7 exchange their second piece for the first piece of the row 8 further:
+  // a store writes eight rows' whole 128 bytes.
+  const int g = lane >> 4, r16 = lane & 15;
+  const size_t out0 = kMode == kWeightsGrad ? (size_t)e * p.N : 0;
+  const int top = row0 + wm * WM, left = n0 + wn * WN;
+  if (p.out_type == MOE_TYPE_F32) {
+    float* out = reinterpret_cast<float*>(p.out);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int row = top + 16 * i + r16, col = left + 16 * j + 4 * g;
+        if (row < row_end && col < width)
+          __builtin_nontemporal_store(acc[i][j],
+                                      reinterpret_cast<v4f*>(out + (out0 + row) * width + col));
+      }
+    return;
+  }
+  uint16_t* out = reinterpret_cast<uint16_t*>(p.out);
+  const bool low = r16 < 8;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    u32x4 piece[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint32_t a[2], b[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const v4f& x = acc[i][2 * s];
+        const v4f& y = acc[i][2 * s + 1];
+        a[q] = kType == MOE_TYPE_F16 ? pack2_f16(x[2 * q], x[2 * q + 1])
+                                     : pack2_bf16(x[2 * q], x[2 * q + 1]);
+        b[q] = kType == MOE_TYPE_F16 ? pack2_f16(y[2 * q], y[2 * q + 1])
+                                     : pack2_bf16(y[2 * q], y[2 * q + 1]);
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const auto r = __builtin_amdgcn_permlane16_swap(a[q], b[q], false, false);
+        piece[s][q] = r[0];
+        piece[s][2 + q] = r[1];
+      }
+    }
+    u32x4 first, second;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(
+          0, (int)(low ? piece[1][q] : piece[0][q]), 0x128, 0xf, 0xf, false);   // row_ror:8
+      first[q] = low ? piece[0][q] : got;
+      second[q] = low ? got : piece[1][q];
+    }
+    const int col = left + (low ? 0 : 32) + 16 * (g & 1) + 8 * (g >> 1);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int row = top + 16 * i + (r16 & 7) + 8 * s;
+      if (row < row_end && col < width)
+        __builtin_nontemporal_store(
+            s ? second : first, reinterpret_cast<u32x4*>(out + (out0 + row) * width + col));
+    }
+  }
 }
 
 // Rows that no expert has, set to zero: a wave to a row.
@@ -176,21 +556,52 @@ static bool float_type(int dtype) {
   return dtype == MOE_TYPE_F32 || dtype == MOE_TYPE_BF16 || dtype == MOE_TYPE_F16;
 }
 
+// Tiles of a launch: those of every expert's rows, rounded up.
+template <int kMode>
+static long long tiles_of(const FloatArgs& p, int bm, int bn) {
+  const int width = kMode == kProduct ? p.N : p.K;
+  const long long m = kMode == kWeightsGrad ? (long long)p.E * ((p.N + bm - 1) / bm)
+                                            : (long long)p.rows / bm + p.E;
+  return m * ((width + bn - 1) / bn);
+}
+
+template <int kType, int kMode, int BM, int BN, int WM, int WN, int GM, int kDeep>
+static moe_status_t launch_half(const FloatArgs& p, hipStream_t st) {
+  constexpr int threads = 64 * (BM / WM) * (BN / WN);
+  const long long blocks = tiles_of<kMode>(p, BM, BN);
+  if (blocks * threads > 0xffffffffLL || blocks > 0x7fffffffLL) return MOE_UNSUPPORTED_SHAPE;
+  const dim3 grid((unsigned)blocks), block(threads);
+  // (a weights' gradient ends where its operands' descriptors end)
+  const bool ragged = kMode != kWeightsGrad && (kMode == kProduct ? p.K : p.N) % 64 != 0;
+  if constexpr (kMode != kWeightsGrad) {
+    if (ragged) {
+      hipLaunchKernelGGL((half_tile_kernel<kType, kMode, BM, BN, WM, WN, GM, kDeep, true>), grid,
+                         block, 0, st, p);
+      return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
+    }
+  }
+  hipLaunchKernelGGL((half_tile_kernel<kType, kMode, BM, BN, WM, WN, GM, kDeep, false>), grid,
+                     block, 0, st, p);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
+}
+
+template <int kType, int kMode>
+static moe_status_t launch_half(const FloatArgs& p, hipStream_t st) {
+  const long long rows = kMode == kWeightsGrad ? p.N : ((long long)p.rows + p.E - 1) / p.E;
+  if (tiles_of<kMode>(p, 64, 64) <= 512 || rows <= 64)
+    return launch_half<kType, kMode, 64, 64, 32, 64, 4, 6>(p, st);
+  if (tiles_of<kMode>(p, 256, 256) <= 128 || rows < 256)
+    return launch_half<kType, kMode, 128, 128, 64, 64, 4, 0>(p, st);
+  return launch_half<kType, kMode, 256, 256, 128, 64, 2, 0>(p, st);
+}
+
 template <int kMode>
 static moe_status_t launch_float(const FloatArgs& p, int dtype, hipStream_t st) {
-  const int width = kMode == kProduct ? p.N : p.K;
-  const dim3 block(256);
-  const long long tiles_i =
-      kMode == kWeightsGrad ? (long long)p.E * ((p.N + 63) / 64) : (long long)p.rows / 64 + p.E;
-  const long long tiles = tiles_i * ((width + 63) / 64);
+  if (dtype == MOE_TYPE_BF16) return launch_half<MOE_TYPE_BF16, kMode>(p, st);
+  if (dtype == MOE_TYPE_F16) return launch_half<MOE_TYPE_F16, kMode>(p, st);
+  const long long tiles = tiles_of<kMode>(p, 64, 64);
   if (tiles * 256 > 0xffffffffLL) return MOE_UNSUPPORTED_SHAPE;   // threads of a launch
-  const dim3 grid((unsigned)tiles);
-  if (dtype == MOE_TYPE_F32)
-    hipLaunchKernelGGL((float_tile_kernel<MOE_TYPE_F32, kMode>), grid, block, 0, st, p);
-  else if (dtype == MOE_TYPE_BF16)
-    hipLaunchKernelGGL((float_tile_kernel<MOE_TYPE_BF16, kMode>), grid, block, 0, st, p);
-  else
-    hipLaunchKernelGGL((float_tile_kernel<MOE_TYPE_F16, kMode>), grid, block, 0, st, p);
+  hipLaunchKernelGGL((float_tile_kernel<kMode>), dim3((unsigned)tiles), dim3(256), 0, st, p);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
 }
 
