@@ -75,142 +75,437 @@ __device__ __forceinline__ void wave_best(double& key, int& idx) {
   }
 }
 
-template <typename El, int kPer>
-__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
-  extern __shared__ double shared[];   // [waves][E], only where there are groups
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int size = p.E / p.groups;     // experts of a group
-  double* keys = shared + (size_t)wave * p.E;
-  for (long long t = (long long)blockIdx.x * kRouteWaves + wave; t < p.T;
-       t += (long long)gridDim.x * kRouteWaves) {
-    float l[kPer];
-    bool pick[kPer], nan = false;
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 64 * i;
-      l[i] = e < p.E ? load_one<El>(p.logits, (size_t)t * p.E + e) : -INFINITY;
-      nan |= l[i] != l[i];
-      if (l[i] != l[i]) l[i] = -INFINITY;
-      l[i] = fminf(l[i], 3.402823466e38f);
-      pick[i] = l[i] > -INFINITY;
-      top = fmaxf(top, l[i]);
-    }
-    double s[kPer], key[kPer];
-    if (p.softmax) {
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-      double sum = 0.;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        s[i] = pick[i] ? exp((double)l[i] - (double)top) : 0.;
-        sum += s[i];
-      }
-      sum = wave_add(sum);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) s[i] = pick[i] ? s[i] / sum : 0.;
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) s[i] = pick[i] ? 1. / (1. + exp(-(double)l[i])) : 0.;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 64 * i;
-      const float b = p.bias && e < p.E ? p.bias[e] : 0.f;
-      nan |= b != b;
-      pick[i] = pick[i] && b > -INFINITY;   // (nor a NaN)
-      key[i] = pick[i] ? s[i] + (double)b : -INFINITY;
-      if (p.scores && e < p.E) p.scores[(size_t)t * p.E + e] = (float)s[i];
-    }
-    if (__ballot(nan) && lane == 0) atomicOr(p.status, MOE_ERR_NAN);
+// A logit as the router counts it: NaN as -infinity, +infinity as the largest
+// fp32 number.
+__device__ __forceinline__ float clean(float l, bool& nan) {
+  nan |= l != l;
+  return l == l ? fminf(l, 3.402823466e38f) : -INFINITY;
+}
 
-    if (p.groups > 1) {
+// Pick k of token t: expert e (-1: none) with score s, of picks that sum to sum.
+__device__ __forceinline__ void put_pick(const RouteArgs& p, long long t, int k, int e, double s,
+                                         double sum) {
+  const size_t at = (size_t)t * p.K + k;
+  p.idx[at] = e;
+  if (p.local_idx) {
+    const int here = e - p.first;
+    p.local_idx[at] = e >= 0 && here >= 0 && here < p.local ? here : -1;
+  }
+  if (p.renorm) s /= sum > (double)kLeastSum ? sum : (double)kLeastSum;
+  p.w[at] = e >= 0 ? (float)(s * (double)p.scale) : 0.f;
+}
+
+// ---- the exact form: a token to a wave, lane l on experts l, l + 64, ..., keys
+// in 64 bits throughout, in E doubles of LDS.  It takes the tokens that the
+// fast form below cannot decide, so its loops are short code, not fast.
+template <typename El>
+__device__ __forceinline__ void route_exact(const RouteArgs& p, long long t, double* keys) {
+  const int lane = threadIdx.x & 63;
+  const size_t row = (size_t)t * p.E;
+  bool nan = false;
+  float top = -INFINITY;
+  double all = 0.;
+  if (p.softmax) {
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 64) top = fmaxf(top, clean(load_one<El>(p.logits, row + e), nan));
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (lane + 64 * i < p.E) keys[lane + 64 * i] = key[i];
-      __threadfence_block();
-      // lane g's group (and g + 64's, ...): up to 1024 groups of one
-      uint32_t kept = 0;   // bit j: group lane + 64 j
-      double total[kPer];
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int g = lane + 64 * j;
-        double first = -INFINITY, second = -INFINITY;
-        if (g < p.groups)
-          for (int m = 0; m < size; ++m) {
-            const double k = keys[g * size + m];
-            second = k > first ? first : k > second ? k : second;
-            first = k > first ? k : first;
-          }
-        total[j] = p.group_best > 1 && size > 1 ? first + second : first;
+    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    top = fmaxf(top, -3.402823466e38f);   // (a row of -infinity)
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 64)
+      all += exp((double)clean(load_one<El>(p.logits, row + e), nan) - (double)top);
+    all = wave_add(all);
+    if (!(all > 0.)) all = 1.;
+  }
+  auto score = [&](int e, bool& pick) {
+    const float l = clean(load_one<El>(p.logits, row + e), nan);
+    pick = l > -INFINITY;
+    const double x = exp(p.softmax ? (double)l - (double)top : -(double)l);
+    return !pick ? 0. : p.softmax ? x / all : 1. / (1. + x);
+  };
+#pragma unroll 1
+  for (int e = lane; e < p.E; e += 64) {
+    bool pick;
+    const double s = score(e, pick);
+    const float b = p.bias ? p.bias[e] : 0.f;
+    nan |= b != b;
+    keys[e] = pick && b > -INFINITY ? s + (double)b : -INFINITY;   // (nor a NaN)
+    if (p.scores) p.scores[row + e] = (float)s;
+  }
+  if (__ballot(nan) && lane == 0) atomicOr(p.status, MOE_ERR_NAN);
+  __threadfence_block();
+
+  if (p.groups > 1) {
+    const int size = p.E / p.groups;
+    // lane g has groups g, g + 64, ...; bit j of kept: group lane + 64 j
+    auto total = [&](int g) {
+      double first = -INFINITY, second = -INFINITY;
+#pragma unroll 1
+      for (int m = 0; m < size; ++m) {
+        const double k = keys[g * size + m];
+        second = k > first ? first : k > second ? k : second;
+        first = k > first ? k : first;
       }
-      for (int n = 0; n < p.top_groups; ++n) {
-        double k = 0.;
-        int g = -1;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int at = lane + 64 * j;
-          if (at < p.groups && !(kept >> j & 1) && (g < 0 || total[j] > k)) {
-            k = total[j];
+      return p.group_best > 1 && size > 1 ? first + second : first;
+    };
+    uint32_t kept = 0;
+#pragma unroll 1
+    for (int n = 0; n < p.top_groups; ++n) {
+      double k = 0.;
+      int g = -1;
+#pragma unroll 1
+      for (int at = lane; at < p.groups; at += 64)
+        if (!(kept >> (at >> 6) & 1)) {
+          const double o = total(at);
+          if (g < 0 || o > k) {
+            k = o;
             g = at;
           }
         }
-        wave_best(k, g);
-        if (g >= 0 && (g & 63) == lane) kept |= 1u << (g >> 6);
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int g = min(lane + 64 * i, p.E - 1) / size;
-        const uint32_t bits = (uint32_t)__shfl((int)kept, g & 63);
-        pick[i] = pick[i] && (bits >> (g >> 6) & 1);
-      }
-      __threadfence_block();
+      wave_best(k, g);
+      if (g >= 0 && (g & 63) == lane) kept |= 1u << (g >> 6);
     }
-
-    int mine = -1;      // lane k: pick k and its score
-    double mine_s = 0.;
-    for (int k = 0; k < p.K; ++k) {
-      double best = 0.;
-      int e = -1;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (pick[i] && (e < 0 || key[i] > best)) {
-          best = key[i];
-          e = lane + 64 * i;
-        }
-      wave_best(best, e);
-      if (e < 0) break;
-      double got = 0.;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (e == lane + 64 * i) {
-          got = s[i];
-          pick[i] = false;
-        }
-      got = __shfl(got, e & 63);
-      if (lane == k) {
-        mine = e;
-        mine_s = got;
-      }
-    }
-    double w = mine_s;
-    if (p.renorm) {
-      double sum = 0.;
-      for (int k = 0; k < p.K; ++k) sum += __shfl(mine_s, k);
-      w /= sum > (double)kLeastSum ? sum : (double)kLeastSum;
-    }
-    if (lane < p.K) {
-      const size_t at = (size_t)t * p.K + lane;
-      p.idx[at] = mine;
-      if (p.local_idx) {
-        const int here = mine - p.first;
-        p.local_idx[at] = mine >= 0 && here >= 0 && here < p.local ? here : -1;
-      }
-      p.w[at] = mine >= 0 ? (float)(w * (double)p.scale) : 0.f;
-    }
+    __threadfence_block();
+#pragma unroll 1
+    for (int g = lane; g < p.groups; g += 64)
+      if (!(kept >> (g >> 6) & 1))
+        for (int m = 0; m < size; ++m) keys[g * size + m] = -INFINITY;
+    __threadfence_block();
   }
+
+  int mine = -1;      // lane k: pick k and its score
+  double mine_s = 0.;
+#pragma unroll 1
+  for (int k = 0; k < p.K; ++k) {
+    double best = -INFINITY;
+    int e = -1;
+#pragma unroll 1
+    for (int at = lane; at < p.E; at += 64)
+      if (keys[at] > best) {
+        best = keys[at];
+        e = at;
+      }
+    wave_best(best, e);
+    if (e < 0) break;
+    if (lane == k) mine = e;
+    if (lane == 0) keys[e] = -INFINITY;
+    __threadfence_block();
+  }
+  bool pick;
+  if (mine >= 0) mine_s = score(mine, pick);
+  const double sum = wave_add(mine_s);
+  if (lane < p.K) put_pick(p, t, lane, mine, mine_s, sum);
+  __threadfence_block();
 }
 
+template <typename El>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_exact_kernel(RouteArgs p) {
+  extern __shared__ double shared[];   // [waves][E]
+  const int wave = threadIdx.x >> 6;
+  for (long long t = (long long)blockIdx.x * kRouteWaves + wave; t < p.T;
+       t += (long long)gridDim.x * kRouteWaves)
+    route_exact<El>(p, t, shared + (size_t)wave * p.E);
+}
+
+// ---- the fast form: kLanes lanes to a token, each holding up to kN
+// neighbouring experts of one group.
+//
+// Keys are fp32 here, and only narrow the choice down: the K highest of every
+// lane's two best keys bound the K-th highest key from below, and the experts
+// above that bound (less the keys' error) are candidates, hardly more than K
+// of them.  The candidates' keys are then formed in 64 bits, a candidate to a
+// lane, and ranked by counting the higher ones.  What 32 bits cannot decide goes
+// to route_exact: groups whose scores are closer than their error, more
+// candidates than fit, and, for the softmax with a bias, whose sum is fp32,
+// candidates closer than that sum's error.
+constexpr float kU = 0x1p-24f;
+
+// Maximum over the aligned group of kLanes lanes, in all of them.
+template <int kLanes>
+__device__ __forceinline__ float lanes_max(float v) {
+  v = fmaxf(v, dpp_row<0xb1>(v));
+  v = fmaxf(v, dpp_row<0x4e>(v));
+  v = fmaxf(v, dpp_row<0x141>(v));
+  v = fmaxf(v, dpp_row<0x140>(v));
+  if constexpr (kLanes == 64) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    v = fmaxf(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+
+template <int kLanes>
+__device__ __forceinline__ float lanes_add(float v) {
+  v += dpp_row<0xb1>(v);
+  v += dpp_row<0x4e>(v);
+  v += dpp_row<0x141>(v);
+  v += dpp_row<0x140>(v);
+  if constexpr (kLanes == 64) {
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+  }
+  return v;
+}
+
+// exp(x) for x <= 0, within 2 ulp down to 2^-126, 0 below: x log2(e) in two
+// parts, since the exponential would scale the rounding of one up by |x|.
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.9259629911266175e-8f;
+  x = fmaxf(x, -1000.f);
+  const float t = x * kLog2e;
+  const float low = fmaf(x, kLog2e, -t) + x * kLog2eLow;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, low * 0.693147182464599609375f, e);
+}
+
+// 1 / x for x in [1, 2^12].
+__device__ __forceinline__ float inverse(float x) {
+  const float y = __builtin_amdgcn_rcpf(x);
+  return fmaf(fmaf(-x, y, 1.f), y, y);
+}
+
+__device__ __forceinline__ float sigmoid32(float l) {
+  const float e = exp_neg(-fabsf(l));
+  const float r = inverse(1.f + e);
+  return l < 0.f ? e * r : r;
+}
+
+struct Candidate {
+  double key;
+  int e;
+};
+
+template <typename El, int kLanes, int kN, bool kWide>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, int lanes_per_group,
+                                                                 int per_lane) {
+  constexpr int kTokens = 64 / kLanes;          // of a wave
+  constexpr int kCap = kLanes == 16 ? 32 : 64;  // candidates of a token
+  __shared__ Candidate cand[kRouteWaves][kTokens][kCap];
+  extern __shared__ double shared[];   // [waves][E], of route_exact
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int at = lane % kLanes, seg = lane / kLanes;
+  const int size = p.E / p.groups;
+  const int group = at / lanes_per_group, sub = at - group * lanes_per_group;
+  const int first = group * size + sub * per_lane;   // the lane's experts
+  const int mine = group < p.groups ? max(0, min(per_lane, size - sub * per_lane)) : 0;
+  Candidate* list = cand[wave][seg];
+
+  float bias[kN], reach = 0.f;   // reach: the largest finite bias in magnitude
+  bool bias_nan = false;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    bias[i] = 0.f;
+    if (i < mine && p.bias) {
+      const float b = p.bias[first + i];
+      bias_nan |= b != b;
+      bias[i] = b == b ? b : -INFINITY;
+      if (fabsf(b) < INFINITY) reach = fmaxf(reach, fabsf(b));
+    }
+  }
+  reach = lanes_max<kLanes>(reach);
+
+  for (long long t0 = ((long long)blockIdx.x * kRouteWaves + wave) * kTokens; t0 < p.T;
+       t0 += (long long)gridDim.x * kRouteWaves * kTokens) {
+    const long long t = t0 + seg;
+    const bool live = t < p.T;
+    const size_t row = (size_t)(live ? t : t0) * p.E;
+    // ---- logits
+    float key[kN];
+    bool nan = bias_nan;
+    if constexpr (kWide) {
+      constexpr int kChunks = kN * El::kSize / 16;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        float f[El::kN];
+        const uint8_t* src = p.logits + (row + first) * El::kSize + 16 * c;
+        El::unpack(*reinterpret_cast<const uint4*>(mine > 0 ? src : p.logits), f);
+#pragma unroll
+        for (int i = 0; i < El::kN; ++i) key[c * El::kN + i] = f[i];
+      }
+#pragma unroll
+      for (int i = 0; i < kN; ++i) key[i] = mine > 0 ? clean(key[i], nan) : -INFINITY;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        key[i] = i < mine ? load_one<El>(p.logits, row + first + i) : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) key[i] = clean(key[i], nan);
+    }
+    // ---- scores and keys
+    float top = 0.f, inv = 1.f;
+    if (p.softmax) {
+      top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) top = fmaxf(top, key[i]);
+      top = lanes_max<kLanes>(top);
+      top = fmaxf(top, -3.402823466e38f);   // (a row of -infinity)
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) sum += exp_neg(key[i] - top);
+      sum = lanes_add<kLanes>(sum);
+      inv = 1.f / fmaxf(sum, 1.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const bool pick = key[i] > -INFINITY;
+      const float s = p.softmax ? exp_neg(key[i] - top) * inv : sigmoid32(key[i]);
+      if (p.scores && i < mine && live) p.scores[row + first + i] = pick ? s : 0.f;
+      key[i] = pick ? s + bias[i] : -INFINITY;
+    }
+    // a key's error: s within 16 roundings (softmax: the argument's too, which
+    // is the logit's distance from the largest, at most -ln s), the sum one
+    const float off = p.softmax ? (112 + kN) * kU : 16.f * kU;
+
+    // ---- the lane's two best, and its group's
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      b = __builtin_amdgcn_fmed3f(a, b, key[i]);
+      a = fmaxf(a, key[i]);
+    }
+    bool slow = false;
+    if (p.groups > 1) {
+      float ga = a, gb = b;
+      for (int d = 1; d < lanes_per_group; ++d) {
+        const int s2 = sub + d < lanes_per_group ? sub + d : sub + d - lanes_per_group;
+        const int from = lane - at + group * lanes_per_group + s2;
+        const float oa = __shfl(a, from), ob = __shfl(b, from);
+        gb = fmaxf(fminf(ga, oa), fmaxf(gb, ob));
+        ga = fmaxf(ga, oa);
+      }
+      // (clamped, so that differences are no NaN.  Both keys' scores and
+      // magnitudes together are at most |total| + 4 reach: a key below 0 is
+      // one of -reach at least.)
+      float total = p.group_best > 1 && size > 1 ? ga + gb : ga;
+      total = fminf(fmaxf(total, -3e38f), 3e38f);
+      const float margin = 2.f * off * (fabsf(total) + 4.f * reach) + 1e-37f;
+      int higher = 0, near = 0;
+      for (int g = 0; g < p.groups; ++g) {
+        const float o = __shfl(total, lane - at + g * lanes_per_group);
+        higher += g != group && o > total + margin;
+        near += g != group && fabsf(o - total) <= margin;
+      }
+      // surely kept: fewer than top_groups higher ones even if all near ones are
+      // higher; surely dropped: top_groups surely higher ones
+      const bool kept = higher + near < p.top_groups;
+      const bool dropped = higher >= p.top_groups;
+      slow = group < p.groups && ga > -INFINITY && !kept && !dropped;
+      if (!kept) {
+        a = b = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) key[i] = -INFINITY;
+      }
+    }
+    // ---- a lower bound of the K-th highest key
+    float bound = lanes_max<kLanes>(a);
+    for (int k = 1; k < p.K; ++k) {
+      const bool popped = a == bound;
+      a = popped ? b : a;
+      b = popped ? -INFINITY : b;
+      bound = lanes_max<kLanes>(a);
+    }
+    bound -= off * 2.f * (fabsf(bound) + 2.f * reach) + 1e-37f;
+    bound = fmaxf(bound, -3.402823466e38f);     // (never -infinity: masked keys are no candidates)
+    // ---- candidates, in the order of the lanes
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) n += key[i] >= bound;
+    int pos = n;
+    if constexpr (kLanes == 16) {
+      // inclusive sum over rows of 16 lanes
+      pos += __builtin_amdgcn_update_dpp(0, pos, 0x111, 0xf, 0xf, true);
+      pos += __builtin_amdgcn_update_dpp(0, pos, 0x112, 0xf, 0xf, true);
+      pos += __builtin_amdgcn_update_dpp(0, pos, 0x114, 0xf, 0xf, true);
+      pos += __builtin_amdgcn_update_dpp(0, pos, 0x118, 0xf, 0xf, true);
+    } else {
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(pos, d);
+        if (lane >= d) pos += o;
+      }
+    }
+    const int total_n = __shfl(pos, lane - at + kLanes - 1);
+    pos -= n;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (key[i] >= bound) {
+        if (pos < kCap) list[pos].e = first + i;
+        ++pos;
+      }
+    slow |= total_n > kCap;
+    const int cands = min(total_n, kCap);
+    __threadfence_block();
+    // ---- their keys in 64 bits: candidate at (and kLanes further)
+    constexpr int kMine = kCap / kLanes;
+    double ck[kMine], cs[kMine];
+    int ce[kMine];
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      ce[u] = -1;
+      ck[u] = cs[u] = 0.;
+    }
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int c = at + u * kLanes;
+      if (c < cands) {
+        ce[u] = list[c].e;
+        bool ignored = false;
+        const float l = clean(load_one<El>(p.logits, row + ce[u]), ignored);
+        cs[u] = p.softmax ? exp((double)l - (double)top) * (double)inv
+                          : 1. / (1. + exp(-(double)l));
+        ck[u] = cs[u] + (p.bias ? (double)p.bias[ce[u]] : 0.);
+        list[c].key = ck[u];
+      }
+      if (u + 1 < kMine && !__ballot(cands > (u + 1) * kLanes)) break;
+    }
+    __threadfence_block();
+    // ---- ranks
+    int rank[kMine];
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) rank[u] = 0;
+    int most = cands;
+#pragma unroll
+    for (int d = kLanes; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
+    most = __builtin_amdgcn_readfirstlane(most);
+    const bool blurred = p.softmax && p.bias;
+    for (int c = 0; c < most; ++c) {
+      const Candidate o = list[c < cands ? c : 0];
+#pragma unroll
+      for (int u = 0; u < kMine; ++u) {
+        if (c < cands && ce[u] >= 0 && o.e != ce[u]) {
+          rank[u] += o.key > ck[u] || (o.key == ck[u] && o.e < ce[u]);
+          // (the softmax's common factor 1 / sum is off by up to 16 kU)
+          if (blurred && fabs(o.key - ck[u]) <= 0x1p-19 * (fabs(ck[u]) + 2. * (double)reach))
+            slow = true;
+        }
+      }
+    }
+    // ---- weights
+    double sum = 0.;
+#pragma unroll
+    for (int u = 0; u < kMine; ++u)
+      if (ce[u] >= 0 && rank[u] < p.K) sum += cs[u];
+#pragma unroll
+    for (int d = kLanes / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    const unsigned long long slow_bits = __ballot(slow && live);
+    constexpr unsigned long long kSeg = kLanes == 64 ? ~0ull : (1ull << (kLanes & 63)) - 1;
+    const bool seg_slow = (slow_bits >> (lane - at)) & kSeg;
+    if (live && !seg_slow) {
+#pragma unroll
+      for (int u = 0; u < kMine; ++u)
+        if (ce[u] >= 0 && rank[u] < p.K) put_pick(p, t, rank[u], ce[u], cs[u], sum);
+      // (fewer candidates than picks: none)
+      for (int k = cands + at; k < p.K; k += kLanes) put_pick(p, t, k, -1, 0., 1.);
+      if (nan) atomicOr(p.status, MOE_ERR_NAN);
+    }
+    if (slow_bits)
+#pragma unroll 1
+      for (int q = 0; q < kTokens; ++q)
+        if ((slow_bits >> (q * kLanes)) & kSeg)
+          route_exact<El>(p, t0 + q, shared + (size_t)wave * p.E);
+    __threadfence_block();
+  }
+}
 template <typename El, int kPer>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -314,29 +609,85 @@ static moe_status_t route_args(const RouteArgs& p, int dtype, int score) {
   return MOE_OK;
 }
 
+static dim3 route_grid(long long units, long long most) {
+  const long long blocks = (units + kRouteWaves - 1) / kRouteWaves;
+  return dim3((unsigned)(blocks < most ? blocks : most));
+}
+
+template <typename El, int kLanes, int kN>
+static void launch_fast(const RouteArgs& p, int lanes_per_group, int per_lane, hipStream_t st) {
+  constexpr int kTokens = 64 / kLanes;
+  const dim3 grid = route_grid(((long long)p.T + kTokens - 1) / kTokens, 2048);
+  const dim3 block(64 * kRouteWaves);
+  const size_t lds = kRouteWaves * (size_t)p.E * sizeof(double);
+  // every lane's experts are whole 16-byte pieces of a row
+  const bool wide = per_lane == kN && p.E / p.groups % kN == 0 &&
+                    (size_t)p.E * El::kSize % 16 == 0 && ((uintptr_t)p.logits & 15) == 0;
+  if constexpr (kN * El::kSize % 16 == 0) {
+    if (wide) {
+      hipLaunchKernelGGL((route_kernel<El, kLanes, kN, true>), grid, block, lds, st, p,
+                         lanes_per_group, per_lane);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((route_kernel<El, kLanes, kN, false>), grid, block, lds, st, p,
+                     lanes_per_group, per_lane);
+}
+
+template <typename El>
+static void launch_exact(const RouteArgs& p, hipStream_t st) {
+  const size_t lds = kRouteWaves * (size_t)p.E * sizeof(double);
+  hipLaunchKernelGGL((route_exact_kernel<El>), route_grid(p.T, 1 << 22),
+                     dim3(64 * kRouteWaves), lds, st, p);
+}
+
+template <typename El>
+static void launch_route(const RouteArgs& p, hipStream_t st) {
+  const int size = p.E / p.groups;
+  const int g16 = p.groups <= 16 ? 16 / p.groups : 0, g64 = p.groups <= 64 ? 64 / p.groups : 0;
+  const int n16 = g16 ? (size + g16 - 1) / g16 : 1 << 20;
+  const int n64 = g64 ? (size + g64 - 1) / g64 : 1 << 20;
+  if (n16 <= 32 && p.K <= 16) {
+    if (n16 <= 2)
+      launch_fast<El, 16, 2>(p, g16, n16, st);
+    else if (n16 <= 4)
+      launch_fast<El, 16, 4>(p, g16, n16, st);
+    else if (n16 <= 8)
+      launch_fast<El, 16, 8>(p, g16, n16, st);
+    else if (n16 <= 16)
+      launch_fast<El, 16, 16>(p, g16, n16, st);
+    else
+      launch_fast<El, 16, 32>(p, g16, n16, st);
+  } else if (n64 <= 16) {
+    if (n64 <= 4)
+      launch_fast<El, 64, 4>(p, g64, n64, st);
+    else
+      launch_fast<El, 64, 16>(p, g64, n64, st);
+  } else {
+    launch_exact<El>(p, st);
+  }
+}
+
 template <typename El, int kPer>
-static void launch_route(const RouteArgs& p, bool grad, hipStream_t st) {
-  const long long blocks = ((long long)p.T + kRouteWaves - 1) / kRouteWaves;
-  const dim3 grid((unsigned)(blocks < (1 << 22) ? blocks : (1 << 22))), block(64 * kRouteWaves);
-  const size_t lds = p.groups > 1 ? kRouteWaves * (size_t)p.E * sizeof(double) : 0;
-  if (grad)
-    hipLaunchKernelGGL((route_grad_kernel<El, kPer>), grid, block, 0, st, p);
-  else
-    hipLaunchKernelGGL((route_kernel<El, kPer>), grid, block, lds, st, p);
+static void launch_route_grad(const RouteArgs& p, hipStream_t st) {
+  hipLaunchKernelGGL((route_grad_kernel<El, kPer>), route_grid(p.T, 1 << 22),
+                     dim3(64 * kRouteWaves), 0, st, p);
 }
 
 template <typename El>
 static moe_status_t launch_route(const RouteArgs& p, bool grad, hipStream_t st) {
-  if (p.E <= 64)
-    launch_route<El, 1>(p, grad, st);
+  if (!grad)
+    launch_route<El>(p, st);
+  else if (p.E <= 64)
+    launch_route_grad<El, 1>(p, st);
   else if (p.E <= 128)
-    launch_route<El, 2>(p, grad, st);
+    launch_route_grad<El, 2>(p, st);
   else if (p.E <= 256)
-    launch_route<El, 4>(p, grad, st);
+    launch_route_grad<El, 4>(p, st);
   else if (p.E <= 512)
-    launch_route<El, 8>(p, grad, st);
+    launch_route_grad<El, 8>(p, st);
   else
-    launch_route<El, 16>(p, grad, st);
+    launch_route_grad<El, 16>(p, st);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
 }
 

@@ -589,8 +589,9 @@ moe_status_t moe_linear_int8(const void* x, int dtype, const int8_t* w, const fl
  * -infinity (its key is -infinity, in its group's score too); a logit or bias
  * of NaN counts as -infinity and sets MOE_ERR_NAN.  A logit of +infinity
  * counts as the largest fp32 number.  Where fewer than K experts are left the
- * other picks are -1 with the weight 0.  Keys are compared in 64 bits; scores
- * and weights are rounded to fp32 once.
+ * other picks are -1 with the weight 0.  Which expert is picked, and in which
+ * order, is decided as in 64 bits; scores and weights are fp32 (a few
+ * roundings each).
  *
  *   topk_idx  [T, K] int32  picks, as indices of all E experts
  *   local_idx [T, K] int32 or NULL: pick - first_expert for picks in
