@@ -15,6 +15,8 @@
 // Keys are compared as 64-bit numbers: which expert a token goes to does not
 // hang on the last bit of an exponential.  A wave takes a token, lane l holding
 // experts l, l + 64, ...
+#include <type_traits>
+
 #include "row_chunks.hpp"
 
 namespace moe {
@@ -82,17 +84,15 @@ __device__ __forceinline__ float clean(float l, bool& nan) {
   return l == l ? fminf(l, 3.402823466e38f) : -INFINITY;
 }
 
-// Pick k of token t: expert e (-1: none) with score s, of picks that sum to sum.
-__device__ __forceinline__ void put_pick(const RouteArgs& p, long long t, int k, int e, double s,
-                                         double sum) {
+// Pick k of token t: expert e (-1: none) with weight w.
+__device__ __forceinline__ void put_pick(const RouteArgs& p, long long t, int k, int e, float w) {
   const size_t at = (size_t)t * p.K + k;
   p.idx[at] = e;
   if (p.local_idx) {
     const int here = e - p.first;
     p.local_idx[at] = e >= 0 && here >= 0 && here < p.local ? here : -1;
   }
-  if (p.renorm) s /= sum > (double)kLeastSum ? sum : (double)kLeastSum;
-  p.w[at] = e >= 0 ? (float)(s * (double)p.scale) : 0.f;
+  p.w[at] = w;
 }
 
 // ---- the exact form: a token to a wave, lane l on experts l, l + 64, ..., keys
@@ -194,7 +194,8 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, long long t, dou
   bool pick;
   if (mine >= 0) mine_s = score(mine, pick);
   const double sum = wave_add(mine_s);
-  if (lane < p.K) put_pick(p, t, lane, mine, mine_s, sum);
+  if (p.renorm) mine_s /= sum > (double)kLeastSum ? sum : (double)kLeastSum;
+  if (lane < p.K) put_pick(p, t, lane, mine, (float)(mine_s * (double)p.scale));
   __threadfence_block();
 }
 
@@ -210,26 +211,40 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_exact_kernel(RouteArgs
 // ---- the fast form: kLanes lanes to a token, each holding up to kN
 // neighbouring experts of one group.
 //
-// Keys are fp32 here, and only narrow the choice down: the K highest of every
-// lane's two best keys bound the K-th highest key from below, and the experts
-// above that bound (less the keys' error) are candidates, hardly more than K
-// of them.  The candidates' keys are then formed in 64 bits, a candidate to a
-// lane, and ranked by counting the higher ones.  What 32 bits cannot decide goes
-// to route_exact: groups whose scores are closer than their error, more
-// candidates than fit, and, for the softmax with a bias, whose sum is fp32,
-// candidates closer than that sum's error.
+// Keys are fp32 here.  The K highest of every lane's two best keys bound the
+// K-th highest key from below, and the experts above that bound (less the keys'
+// error) are candidates, hardly more than K of them.  A candidate goes to a
+// lane, which ranks it by counting the higher ones.  Where two candidates are
+// closer than their error, or tie, their keys are formed again in 64 bits; what
+// is still open goes to route_exact: groups whose scores are closer than their
+// error, more candidates than fit, and, for a softmax with a bias, whose sum
+// is fp32, candidates that are close.
 constexpr float kU = 0x1p-24f;
 
-// Maximum over the aligned group of kLanes lanes, in all of them.
+// The larger of two numbers that are no NaN, in one instruction (fmaxf first
+// quiets what might be a signalling NaN: one more per operand).
+__device__ __forceinline__ float larger(float a, float b) {
+  return __builtin_amdgcn_fmed3f(a, b, INFINITY);
+}
+
+// Maximum over the aligned group of kLanes lanes, in all of them (no NaN).
+// Rows of 16 lanes exchange as in group16_max, the exchange a part of the
+// instruction that compares; a lane's new value can be exchanged two wait
+// states later.
 template <int kLanes>
 __device__ __forceinline__ float lanes_max(float v) {
-  v = fmaxf(v, dpp_row<0xb1>(v));
-  v = fmaxf(v, dpp_row<0x4e>(v));
-  v = fmaxf(v, dpp_row<0x141>(v));
-  v = fmaxf(v, dpp_row<0x140>(v));
+  asm("s_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 row_mirror row_mask:0xf bank_mask:0xf"
+      : "+v"(v));
   if constexpr (kLanes == 64) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    v = fmaxf(v, __shfl_xor(v, 32));
+    v = larger(v, __shfl_xor(v, 16));
+    v = larger(v, __shfl_xor(v, 32));
   }
   return v;
 }
@@ -247,15 +262,17 @@ __device__ __forceinline__ float lanes_add(float v) {
   return v;
 }
 
-// exp(x) for x <= 0, within 2 ulp down to 2^-126, 0 below: x log2(e) in two
-// parts, since the exponential would scale the rounding of one up by |x|.
-__device__ __forceinline__ float exp_neg(float x) {
-  constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.9259629911266175e-8f;
-  x = fmaxf(x, -1000.f);
+constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.9259629911266175e-8f;
+constexpr float kLn2 = 0.693147182464599609375f;
+
+// exp(x) for x in [-1000, 88], within 3 roundings down to 2^-126, 0 below: x
+// log2(e) in two parts, since the exponential would scale the rounding of one
+// up by |x|.
+__device__ __forceinline__ float exp32(float x) {
   const float t = x * kLog2e;
   const float low = fmaf(x, kLog2e, -t) + x * kLog2eLow;
   const float e = __builtin_amdgcn_exp2f(t);
-  return fmaf(e, low * 0.693147182464599609375f, e);
+  return fmaf(e, low * kLn2, e);
 }
 
 // 1 / x for x in [1, 2^12].
@@ -264,31 +281,44 @@ __device__ __forceinline__ float inverse(float x) {
   return fmaf(fmaf(-x, y, 1.f), y, y);
 }
 
-__device__ __forceinline__ float sigmoid32(float l) {
-  const float e = exp_neg(-fabsf(l));
+// A score within 8 roundings (softmax: of the exponential; l - top adds |l - top|).
+__device__ __forceinline__ float score32(float l, bool softmax, float top, float inv) {
+  if (softmax) return exp32(fmaxf(l - top, -1000.f)) * inv;
+  const float e = exp32(fmaxf(-fabsf(l), -1000.f));
   const float r = inverse(1.f + e);
   return l < 0.f ? e * r : r;
 }
 
-struct Candidate {
-  double key;
+// An fp32 number as an unsigned one of the same order.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+// A candidate: of two, the one of the higher key, or of the same and the lower
+// index, has the higher `order`.  key64 takes its place once it has been formed.
+struct __attribute__((aligned(16))) Candidate {
+  uint64_t order;
+  float key;
   int e;
 };
 
 template <typename El, int kLanes, int kN, bool kWide>
-__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, int lanes_per_group,
+__global__ __launch_bounds__(64 * kRouteWaves, kN <= 16 ? 4 : 2) void route_kernel(RouteArgs p, int lanes_per_group,
                                                                  int per_lane) {
   constexpr int kTokens = 64 / kLanes;          // of a wave
   constexpr int kCap = kLanes == 16 ? 32 : 64;  // candidates of a token
+  constexpr int kMine = kCap / kLanes;          // of them to a lane
   __shared__ Candidate cand[kRouteWaves][kTokens][kCap];
   extern __shared__ double shared[];   // [waves][E], of route_exact
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int at = lane % kLanes, seg = lane / kLanes;
+  const int at = lane % kLanes, seg = lane / kLanes, base = lane - at;
   const int size = p.E / p.groups;
   const int group = at / lanes_per_group, sub = at - group * lanes_per_group;
   const int first = group * size + sub * per_lane;   // the lane's experts
   const int mine = group < p.groups ? max(0, min(per_lane, size - sub * per_lane)) : 0;
   Candidate* list = cand[wave][seg];
+  const bool softmax = p.softmax;
 
   float bias[kN], reach = 0.f;   // reach: the largest finite bias in magnitude
   bool bias_nan = false;
@@ -303,93 +333,125 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, in
     }
   }
   reach = lanes_max<kLanes>(reach);
+  // an fp32 key's error, relative to |key| + 2 reach (which bounds the score
+  // and the key): here the score's 32 roundings, or the softmax's of its
+  // argument (at most 88; scores below e^-88 are 0, within 1e-37) and its sum
+  const float off = softmax ? (112 + kN) * kU : 32.f * kU;
+  uint32_t absent = 0;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) absent |= (i < mine ? 0u : 1u) << i;
 
   for (long long t0 = ((long long)blockIdx.x * kRouteWaves + wave) * kTokens; t0 < p.T;
        t0 += (long long)gridDim.x * kRouteWaves * kTokens) {
     const long long t = t0 + seg;
     const bool live = t < p.T;
     const size_t row = (size_t)(live ? t : t0) * p.E;
-    // ---- logits
+    // ---- logits; `odd`: there are infinities or NaN among them
     float key[kN];
     bool nan = bias_nan;
+    float odd = 0.f;
     if constexpr (kWide) {
-      constexpr int kChunks = kN * El::kSize / 16;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
+      for (int c = 0; c < kN * El::kSize / 16; ++c) {
         float f[El::kN];
         const uint8_t* src = p.logits + (row + first) * El::kSize + 16 * c;
         El::unpack(*reinterpret_cast<const uint4*>(mine > 0 ? src : p.logits), f);
 #pragma unroll
         for (int i = 0; i < El::kN; ++i) key[c * El::kN + i] = f[i];
       }
-#pragma unroll
-      for (int i = 0; i < kN; ++i) key[i] = mine > 0 ? clean(key[i], nan) : -INFINITY;
+      if (mine == 0) key[0] = INFINITY;   // (a lane without experts)
     } else {
 #pragma unroll
       for (int i = 0; i < kN; ++i)
-        key[i] = i < mine ? load_one<El>(p.logits, row + first + i) : -INFINITY;
+        key[i] = i < mine ? load_one<El>(p.logits, row + first + i) : INFINITY;
+    }
 #pragma unroll
-      for (int i = 0; i < kN; ++i) key[i] = clean(key[i], nan);
+    for (int i = 0; i < kN; ++i) odd = fmaf(key[i], key[i], odd);
+    uint32_t masked = absent;   // bit i: expert i is none, or not to be picked
+    const bool special = __ballot(!(odd < INFINITY)) != 0;
+    if (special) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        nan |= key[i] != key[i] && !(absent >> i & 1);
+        masked |= (key[i] > -INFINITY ? 0u : 1u) << i;
+        key[i] = __builtin_amdgcn_fmed3f(key[i], -3.402823466e38f, 3.402823466e38f);
+        if (softmax) key[i] = masked >> i & 1 ? -INFINITY : key[i];
+      }
     }
     // ---- scores and keys
     float top = 0.f, inv = 1.f;
-    if (p.softmax) {
-      top = -INFINITY;
+    if (softmax) {
+      top = -3.402823466e38f;   // (of a row of -infinity)
 #pragma unroll
-      for (int i = 0; i < kN; ++i) top = fmaxf(top, key[i]);
+      for (int i = 0; i < kN; ++i) top = larger(top, key[i]);
       top = lanes_max<kLanes>(top);
-      top = fmaxf(top, -3.402823466e38f);   // (a row of -infinity)
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) sum += exp_neg(key[i] - top);
+      for (int i = 0; i < kN; ++i) {
+        key[i] = exp32(larger(key[i] - top, -1000.f));
+        sum += key[i];
+      }
       sum = lanes_add<kLanes>(sum);
       inv = 1.f / fmaxf(sum, 1.f);
-    }
+      if (p.scores && live)
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const bool pick = key[i] > -INFINITY;
-      const float s = p.softmax ? exp_neg(key[i] - top) * inv : sigmoid32(key[i]);
-      if (p.scores && i < mine && live) p.scores[row + first + i] = pick ? s : 0.f;
-      key[i] = pick ? s + bias[i] : -INFINITY;
+        for (int i = 0; i < kN; ++i)
+          if (i < mine) p.scores[row + first + i] = key[i] * inv;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) key[i] = fmaf(key[i], inv, bias[i]);
+    } else {
+      if (p.scores && live)
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (i < mine)
+            p.scores[row + first + i] = masked >> i & 1 ? 0.f : score32(key[i], false, 0.f, 1.f);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const float x = -__builtin_amdgcn_fmed3f(key[i], -88.f, 88.f);
+        const float u = x * kLog2e;
+        const float e = __builtin_amdgcn_exp2f(u);
+        const float e1 = fmaf(e, fmaf(x, kLog2e, -u) * kLn2, e);
+        key[i] = __builtin_amdgcn_rcpf(1.f + e1) + bias[i];
+      }
     }
-    // a key's error: s within 16 roundings (softmax: the argument's too, which
-    // is the logit's distance from the largest, at most -ln s), the sum one
-    const float off = p.softmax ? (112 + kN) * kU : 16.f * kU;
+    if (special) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) key[i] = masked >> i & 1 ? -INFINITY : key[i];
+    }
 
     // ---- the lane's two best, and its group's
     float a = -INFINITY, b = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       b = __builtin_amdgcn_fmed3f(a, b, key[i]);
-      a = fmaxf(a, key[i]);
+      a = larger(a, key[i]);
     }
     bool slow = false;
     if (p.groups > 1) {
       float ga = a, gb = b;
       for (int d = 1; d < lanes_per_group; ++d) {
         const int s2 = sub + d < lanes_per_group ? sub + d : sub + d - lanes_per_group;
-        const int from = lane - at + group * lanes_per_group + s2;
+        const int from = base + group * lanes_per_group + s2;
         const float oa = __shfl(a, from), ob = __shfl(b, from);
-        gb = fmaxf(fminf(ga, oa), fmaxf(gb, ob));
-        ga = fmaxf(ga, oa);
+        gb = larger(__builtin_amdgcn_fmed3f(ga, oa, gb), ob);
+        ga = larger(ga, oa);
       }
       // (clamped, so that differences are no NaN.  Both keys' scores and
       // magnitudes together are at most |total| + 4 reach: a key below 0 is
       // one of -reach at least.)
       float total = p.group_best > 1 && size > 1 ? ga + gb : ga;
-      total = fminf(fmaxf(total, -3e38f), 3e38f);
+      total = __builtin_amdgcn_fmed3f(total, -3e38f, 3e38f);
       const float margin = 2.f * off * (fabsf(total) + 4.f * reach) + 1e-37f;
-      int higher = 0, near = 0;
+      int higher = 0, near = -1;   // (itself)
       for (int g = 0; g < p.groups; ++g) {
-        const float o = __shfl(total, lane - at + g * lanes_per_group);
-        higher += g != group && o > total + margin;
-        near += g != group && fabsf(o - total) <= margin;
+        const float d = __shfl(total, base + g * lanes_per_group) - total;
+        higher += d > margin;
+        near += fabsf(d) <= margin;
       }
       // surely kept: fewer than top_groups higher ones even if all near ones are
       // higher; surely dropped: top_groups surely higher ones
       const bool kept = higher + near < p.top_groups;
-      const bool dropped = higher >= p.top_groups;
-      slow = group < p.groups && ga > -INFINITY && !kept && !dropped;
+      slow = group < p.groups && ga > -INFINITY && !kept && higher < p.top_groups;
       if (!kept) {
         a = b = -INFINITY;
 #pragma unroll
@@ -398,18 +460,22 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, in
     }
     // ---- a lower bound of the K-th highest key
     float bound = lanes_max<kLanes>(a);
-    for (int k = 1; k < p.K; ++k) {
-      const bool popped = a == bound;
-      a = popped ? b : a;
-      b = popped ? -INFINITY : b;
-      bound = lanes_max<kLanes>(a);
+    {
+      float a1 = a, b1 = b;
+      for (int k = 1; k < p.K; ++k) {
+        const bool popped = a1 == bound;
+        a1 = popped ? b1 : a1;
+        b1 = popped ? -INFINITY : b1;
+        bound = lanes_max<kLanes>(a1);
+      }
     }
-    bound -= off * 2.f * (fabsf(bound) + 2.f * reach) + 1e-37f;
+    bound -= 2.f * off * (fabsf(bound) + 2.f * reach) + 1e-37f;
     bound = fmaxf(bound, -3.402823466e38f);     // (never -infinity: masked keys are no candidates)
     // ---- candidates, in the order of the lanes
-    int n = 0;
+    uint32_t in = 0;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) n += key[i] >= bound;
+    for (int i = kN - 1; i >= 0; --i) in = in + in + (key[i] >= bound ? 1u : 0u);
+    const int n = __builtin_popcount(in);
     int pos = n;
     if constexpr (kLanes == 16) {
       // inclusive sum over rows of 16 lanes
@@ -424,88 +490,127 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, in
         if (lane >= d) pos += o;
       }
     }
-    const int total_n = __shfl(pos, lane - at + kLanes - 1);
+    const int total_n = __shfl(pos, base + kLanes - 1);
     pos -= n;
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (key[i] >= bound) {
-        if (pos < kCap) list[pos].e = first + i;
-        ++pos;
-      }
+    while (in) {
+      if (pos < kCap) list[pos].e = first + __builtin_ctz(in);
+      in &= in - 1;
+      ++pos;
+    }
     slow |= total_n > kCap;
     const int cands = min(total_n, kCap);
-    __threadfence_block();
-    // ---- their keys in 64 bits: candidate at (and kLanes further)
-    constexpr int kMine = kCap / kLanes;
-    double ck[kMine], cs[kMine];
-    int ce[kMine];
-#pragma unroll
-    for (int u = 0; u < kMine; ++u) {
-      ce[u] = -1;
-      ck[u] = cs[u] = 0.;
-    }
-#pragma unroll
-    for (int u = 0; u < kMine; ++u) {
-      const int c = at + u * kLanes;
-      if (c < cands) {
-        ce[u] = list[c].e;
-        bool ignored = false;
-        const float l = clean(load_one<El>(p.logits, row + ce[u]), ignored);
-        cs[u] = p.softmax ? exp((double)l - (double)top) * (double)inv
-                          : 1. / (1. + exp(-(double)l));
-        ck[u] = cs[u] + (p.bias ? (double)p.bias[ce[u]] : 0.);
-        list[c].key = ck[u];
-      }
-      if (u + 1 < kMine && !__ballot(cands > (u + 1) * kLanes)) break;
-    }
-    __threadfence_block();
-    // ---- ranks
-    int rank[kMine];
-#pragma unroll
-    for (int u = 0; u < kMine; ++u) rank[u] = 0;
-    int most = cands;
+    int most = cands;   // of the wave's tokens
 #pragma unroll
     for (int d = kLanes; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
     most = __builtin_amdgcn_readfirstlane(most);
-    const bool blurred = p.softmax && p.bias;
-    for (int c = 0; c < most; ++c) {
-      const Candidate o = list[c < cands ? c : 0];
+    __threadfence_block();
+    // ---- candidate at (and kLanes further): its score again, a few roundings
+    // off, and its rank.  Places behind a token's candidates rank below all.
+    const float off2 = 2.f * (softmax ? off : 16.f * kU);
+    int ce[kMine], rank[kMine];
+    float cl[kMine], cs[kMine], ck[kMine], near2[kMine];
+    uint64_t order[kMine];
+    auto form = [&](auto at_u) __attribute__((always_inline)) {
+      constexpr int u = decltype(at_u)::value;
+      const int c = at + u * kLanes;
+      ce[u] = -1;
+      rank[u] = 0;
+      cl[u] = cs[u] = 0.f;
+      ck[u] = -INFINITY;
+      order[u] = 0;
+      if (c < cands) {
+        ce[u] = list[c].e;
+        bool none = false;
+        cl[u] = clean(load_one<El>(p.logits, row + ce[u]), none);
+        cs[u] = score32(cl[u], softmax, top, inv);
+        ck[u] = cs[u] + (p.bias ? p.bias[ce[u]] : 0.f);
+        order[u] = (uint64_t)ordered(ck[u]) << 32 | (uint32_t)~ce[u];
+      }
+      near2[u] = off2 * (fabsf(ck[u]) + 2.f * reach) + 1e-37f;
+      list[c].order = order[u];
+      list[c].key = ck[u];
+    };
+    // how many of the candidates rank higher, and how many are close (itself
+    // among them)
+    int close = 0;
+    auto count = [&](int upto, auto at_u) __attribute__((always_inline)) {
+      constexpr int u = decltype(at_u)::value;
+      int n_close = 0;
+#pragma unroll 4
+      for (int c = 0; c < upto; ++c) {
+        const uint64_t o = list[c].order;
+        const float ok = list[c].key;
+        rank[u] += o > order[u];
+        n_close += !(fabsf(ok - ck[u]) > near2[u]);
+      }
+      if (ce[u] >= 0) close |= n_close - 1;
+    };
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, kMine - 1>;
+    const bool two = kMine > 1 && most > kLanes;
+    form(First());
+    if (kMine > 1) {
+      ce[kMine - 1] = kMine > 1 ? -1 : ce[0];
+      if (two) form(Second());
+    }
+    __threadfence_block();
+    count(most, First());
+    if (two) count(most, Second());
+    if (__ballot(close != 0 && live)) {
+      // keys in 64 bits.  (A softmax's sum, the same for all, does not change
+      // the order of its scores.)
+      if (softmax && p.bias) slow |= close != 0;
+      double key64[kMine];
 #pragma unroll
       for (int u = 0; u < kMine; ++u) {
-        if (c < cands && ce[u] >= 0 && o.e != ce[u]) {
-          rank[u] += o.key > ck[u] || (o.key == ck[u] && o.e < ce[u]);
-          // (the softmax's common factor 1 / sum is off by up to 16 kU)
-          if (blurred && fabs(o.key - ck[u]) <= 0x1p-19 * (fabs(ck[u]) + 2. * (double)reach))
-            slow = true;
-        }
+        key64[u] = 0.;
+        if (ce[u] < 0) continue;
+        const double l = (double)cl[u];
+        const double x = exp(softmax ? l - (double)top : -l);
+        key64[u] = !softmax ? 1. / (1. + x) : p.bias ? x * (double)inv : x;
+        if (p.bias) key64[u] += (double)p.bias[ce[u]];
+        list[at + u * kLanes].order = __builtin_bit_cast(uint64_t, key64[u]);
+        rank[u] = 0;
+      }
+      __threadfence_block();
+#pragma unroll 1
+      for (int c = 0; c < most; ++c) {
+        const double ok = __builtin_bit_cast(double, list[c].order);
+        const int oe = list[c].e;
+#pragma unroll
+        for (int u = 0; u < kMine; ++u)
+          if (ce[u] >= 0)
+            rank[u] += c < cands && (ok > key64[u] || (ok == key64[u] && oe < ce[u]));
       }
     }
     // ---- weights
-    double sum = 0.;
+    float sum = 0.f;
 #pragma unroll
     for (int u = 0; u < kMine; ++u)
       if (ce[u] >= 0 && rank[u] < p.K) sum += cs[u];
-#pragma unroll
-    for (int d = kLanes / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    sum = lanes_add<kLanes>(sum);
     const unsigned long long slow_bits = __ballot(slow && live);
     constexpr unsigned long long kSeg = kLanes == 64 ? ~0ull : (1ull << (kLanes & 63)) - 1;
-    const bool seg_slow = (slow_bits >> (lane - at)) & kSeg;
+    const bool seg_slow = (slow_bits >> base & kSeg) != 0;
     if (live && !seg_slow) {
+      const float by = p.renorm ? p.scale / fmaxf(sum, kLeastSum) : p.scale;
 #pragma unroll
       for (int u = 0; u < kMine; ++u)
-        if (ce[u] >= 0 && rank[u] < p.K) put_pick(p, t, rank[u], ce[u], cs[u], sum);
+        if (ce[u] >= 0 && rank[u] < p.K) put_pick(p, t, rank[u], ce[u], cs[u] * by);
       // (fewer candidates than picks: none)
-      for (int k = cands + at; k < p.K; k += kLanes) put_pick(p, t, k, -1, 0., 1.);
+      for (int k = cands + at; k < p.K; k += kLanes) put_pick(p, t, k, -1, 0.f);
       if (nan) atomicOr(p.status, MOE_ERR_NAN);
     }
-    if (slow_bits)
+    if (slow_bits) {
 #pragma unroll 1
       for (int q = 0; q < kTokens; ++q)
-        if ((slow_bits >> (q * kLanes)) & kSeg)
+        if (slow_bits >> (q * kLanes) & kSeg)
           route_exact<El>(p, t0 + q, shared + (size_t)wave * p.E);
-    __threadfence_block();
+    }
+    __threadfence_block();   // (the list is written again)
   }
 }
+
 template <typename El, int kPer>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
