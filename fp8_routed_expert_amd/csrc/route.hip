@@ -63,18 +63,39 @@ __device__ __forceinline__ double wave_add(double v) {
   return v;
 }
 
-// The highest (key, lowest index on a tie) of the wave's candidates, in every
-// lane; index -1 where no lane has one.
-__device__ __forceinline__ void wave_best(double& key, int& idx) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const double k = __shfl_xor(key, d);
-    const int i = __shfl_xor(idx, d);
-    if (i >= 0 && (idx < 0 || k > key || (k == key && i < idx))) {
-      key = k;
-      idx = i;
-    }
+// Maximum over the wave, in every lane: rows of 16 lanes as in group16_max, then
+// their results.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, true));
+  const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0);
+  const uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
+  const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32);
+  const uint32_t d = (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
+  return max(max(a, b), max(c, d));
+}
+
+// The index of the highest key (the lowest index on a tie) of the wave's
+// candidates, -1 where no lane has one (idx -1): the keys' upper halves first,
+// the lower ones and the indices among the lanes that are left.
+__device__ __forceinline__ int wave_best(double key, int idx) {
+  uint64_t bits = __builtin_bit_cast(uint64_t, key + 0.0);   // (no -0)
+  bits ^= (uint64_t)((int64_t)bits >> 63) | 0x8000000000000000ull;
+  bool in = idx >= 0;
+  uint64_t left = __ballot(in);
+  if (!left) return -1;
+  uint32_t m = wave_max(in ? (uint32_t)(bits >> 32) : 0u);
+  in = in && (uint32_t)(bits >> 32) == m;
+  left = __ballot(in);
+  if (left & (left - 1)) {
+    m = wave_max(in ? (uint32_t)bits : 0u);
+    in = in && (uint32_t)bits == m;
+    left = __ballot(in);
+    if (left & (left - 1)) return (int)~wave_max(in ? ~(uint32_t)idx : 0u);
   }
+  return __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
 }
 
 // A logit as the router counts it: NaN as -infinity, +infinity as the largest
@@ -140,7 +161,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, long long t, dou
     // lane g has groups g, g + 64, ...; bit j of kept: group lane + 64 j
     auto total = [&](int g) {
       double first = -INFINITY, second = -INFINITY;
-#pragma unroll 1
+#pragma unroll 4
       for (int m = 0; m < size; ++m) {
         const double k = keys[g * size + m];
         second = k > first ? first : k > second ? k : second;
@@ -149,12 +170,13 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, long long t, dou
       return p.group_best > 1 && size > 1 ? first + second : first;
     };
     uint32_t kept = 0;
+    const double own = lane < p.groups ? total(lane) : 0.;
 #pragma unroll 1
     for (int n = 0; n < p.top_groups; ++n) {
-      double k = 0.;
-      int g = -1;
+      double k = own;
+      int g = lane < p.groups && !(kept & 1) ? lane : -1;
 #pragma unroll 1
-      for (int at = lane; at < p.groups; at += 64)
+      for (int at = lane + 64; at < p.groups; at += 64)
         if (!(kept >> (at >> 6) & 1)) {
           const double o = total(at);
           if (g < 0 || o > k) {
@@ -162,7 +184,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, long long t, dou
             g = at;
           }
         }
-      wave_best(k, g);
+      g = wave_best(k, g);
       if (g >= 0 && (g & 63) == lane) kept |= 1u << (g >> 6);
     }
     __threadfence_block();
@@ -179,13 +201,13 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, long long t, dou
   for (int k = 0; k < p.K; ++k) {
     double best = -INFINITY;
     int e = -1;
-#pragma unroll 1
+#pragma unroll 4
     for (int at = lane; at < p.E; at += 64)
       if (keys[at] > best) {
         best = keys[at];
         e = at;
       }
-    wave_best(best, e);
+    e = wave_best(best, e);
     if (e < 0) break;
     if (lane == k) mine = e;
     if (lane == 0) keys[e] = -INFINITY;
@@ -300,16 +322,25 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 struct __attribute__((aligned(16))) Candidate {
   uint64_t order;
   float key;
-  int e;
+  union {
+    float error;
+    int e;
+  };
 };
 
+// Waves of a SIMD that the registers are shared out to.  (16 experts to each of
+// 16 lanes: three 41 us for 65536 tokens of 256 experts in groups, four, with
+// spills, 45; eight experts to each of 64 lanes 89 and 81.)
+constexpr int route_waves(int lanes, int n) { return lanes == 16 && n == 16 ? 3 : 4; }
+
 template <typename El, int kLanes, int kN, bool kWide>
-__global__ __launch_bounds__(64 * kRouteWaves, kN <= 16 ? 4 : 2) void route_kernel(RouteArgs p, int lanes_per_group,
+__global__ __launch_bounds__(64 * kRouteWaves, route_waves(kLanes, kN)) void route_kernel(RouteArgs p, int lanes_per_group,
                                                                  int per_lane) {
   constexpr int kTokens = 64 / kLanes;          // of a wave
   constexpr int kCap = kLanes == 16 ? 32 : 64;  // candidates of a token
   constexpr int kMine = kCap / kLanes;          // of them to a lane
   __shared__ Candidate cand[kRouteWaves][kTokens][kCap];
+  __shared__ __attribute__((aligned(16))) float totals[kRouteWaves][64];
   extern __shared__ double shared[];   // [waves][E], of route_exact
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int at = lane % kLanes, seg = lane / kLanes, base = lane - at;
@@ -323,20 +354,27 @@ __global__ __launch_bounds__(64 * kRouteWaves, kN <= 16 ? 4 : 2) void route_kern
   float bias[kN], reach = 0.f;   // reach: the largest finite bias in magnitude
   bool bias_nan = false;
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    bias[i] = 0.f;
-    if (i < mine && p.bias) {
-      const float b = p.bias[first + i];
-      bias_nan |= b != b;
-      bias[i] = b == b ? b : -INFINITY;
-      if (fabsf(b) < INFINITY) reach = fmaxf(reach, fabsf(b));
+  for (int i = 0; i < kN; ++i) bias[i] = 0.f;
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) bias[i] = p.bias[kWide ? (mine ? first : 0) + i : i < mine ? first + i : 0];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      bias_nan |= i < mine && bias[i] != bias[i];
+      bias[i] = bias[i] == bias[i] ? bias[i] : -INFINITY;
+      if (i < mine && fabsf(bias[i]) < INFINITY) reach = larger(reach, fabsf(bias[i]));
     }
   }
   reach = lanes_max<kLanes>(reach);
-  // an fp32 key's error, relative to |key| + 2 reach (which bounds the score
-  // and the key): here the score's 32 roundings, or the softmax's of its
-  // argument (at most 88; scores below e^-88 are 0, within 1e-37) and its sum
-  const float off = softmax ? (112 + kN) * kU : 32.f * kU;
+  // an fp32 key's error where v = |key| + 2 reach bounds both the key and its
+  // score: 32 roundings of a sigmoid; a softmax's exponential and sum, and its
+  // argument's, which is -ln(score) at most.  Scores below e^-88 are 0, within
+  // 1e-37.  (Two keys with |sum| + 4 reach <= v together: the same.)
+  auto error = [&](float v) {
+    const float roundings =
+        softmax ? 25.f + kN + larger(0.f, -0.7f * __builtin_amdgcn_logf(v)) : 32.f;
+    return fmaf(v, roundings * kU, 1e-37f);
+  };
   uint32_t absent = 0;
 #pragma unroll
   for (int i = 0; i < kN; ++i) absent |= (i < mine ? 0u : 1u) << i;
@@ -441,12 +479,20 @@ __global__ __launch_bounds__(64 * kRouteWaves, kN <= 16 ? 4 : 2) void route_kern
       // one of -reach at least.)
       float total = p.group_best > 1 && size > 1 ? ga + gb : ga;
       total = __builtin_amdgcn_fmed3f(total, -3e38f, 3e38f);
-      const float margin = 2.f * off * (fabsf(total) + 4.f * reach) + 1e-37f;
+      const float margin = 2.f * error(fabsf(total) + 4.f * reach);
+      // (what is no group is lower than all)
+      totals[wave][lane] = -INFINITY;
+      if (sub == 0 && group < p.groups) totals[wave][base + group] = total;
+      __threadfence_block();
       int higher = 0, near = -1;   // (itself)
-      for (int g = 0; g < p.groups; ++g) {
-        const float d = __shfl(total, base + g * lanes_per_group) - total;
-        higher += d > margin;
-        near += fabsf(d) <= margin;
+      for (int g = 0; g < p.groups; g += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(&totals[wave][base + g]);
+        const float d[4] = {o.x - total, o.y - total, o.z - total, o.w - total};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          higher += d[i] > margin;
+          near += fabsf(d[i]) <= margin;
+        }
       }
       // surely kept: fewer than top_groups higher ones even if all near ones are
       // higher; surely dropped: top_groups surely higher ones
@@ -469,8 +515,8 @@ __global__ __launch_bounds__(64 * kRouteWaves, kN <= 16 ? 4 : 2) void route_kern
         bound = lanes_max<kLanes>(a1);
       }
     }
-    bound -= 2.f * off * (fabsf(bound) + 2.f * reach) + 1e-37f;
-    bound = fmaxf(bound, -3.402823466e38f);     // (never -infinity: masked keys are no candidates)
+    bound -= 2.f * error(fabsf(bound) + 2.f * reach);
+    bound = larger(bound == bound ? bound : -INFINITY, -3.402823466e38f);   // (never -infinity: masked keys are no candidates)
     // ---- candidates, in the order of the lanes
     uint32_t in = 0;
 #pragma unroll
@@ -506,9 +552,8 @@ __global__ __launch_bounds__(64 * kRouteWaves, kN <= 16 ? 4 : 2) void route_kern
     __threadfence_block();
     // ---- candidate at (and kLanes further): its score again, a few roundings
     // off, and its rank.  Places behind a token's candidates rank below all.
-    const float off2 = 2.f * (softmax ? off : 16.f * kU);
     int ce[kMine], rank[kMine];
-    float cl[kMine], cs[kMine], ck[kMine], near2[kMine];
+    float cl[kMine], cs[kMine], ck[kMine], err[kMine];
     uint64_t order[kMine];
     auto form = [&](auto at_u) __attribute__((always_inline)) {
       constexpr int u = decltype(at_u)::value;
@@ -526,9 +571,13 @@ __global__ __launch_bounds__(64 * kRouteWaves, kN <= 16 ? 4 : 2) void route_kern
         ck[u] = cs[u] + (p.bias ? p.bias[ce[u]] : 0.f);
         order[u] = (uint64_t)ordered(ck[u]) << 32 | (uint32_t)~ce[u];
       }
-      near2[u] = off2 * (fabsf(ck[u]) + 2.f * reach) + 1e-37f;
+      err[u] = 0.f;
+      if (c < cands)
+        err[u] = fmaf(cs[u], (softmax ? 18.f + kN + (top - cl[u]) : 12.f) * kU,
+                      fmaf(fabsf(ck[u]), kU, 1e-37f));
       list[c].order = order[u];
       list[c].key = ck[u];
+      list[c].error = err[u];
     };
     // how many of the candidates rank higher, and how many are close (itself
     // among them)
@@ -541,7 +590,7 @@ __global__ __launch_bounds__(64 * kRouteWaves, kN <= 16 ? 4 : 2) void route_kern
         const uint64_t o = list[c].order;
         const float ok = list[c].key;
         rank[u] += o > order[u];
-        n_close += !(fabsf(ok - ck[u]) > near2[u]);
+        n_close += !(fabsf(ok - ck[u]) > list[c].error + err[u]);
       }
       if (ce[u] >= 0) close |= n_close - 1;
     };
@@ -570,6 +619,7 @@ __global__ __launch_bounds__(64 * kRouteWaves, kN <= 16 ? 4 : 2) void route_kern
         key64[u] = !softmax ? 1. / (1. + x) : p.bias ? x * (double)inv : x;
         if (p.bias) key64[u] += (double)p.bias[ce[u]];
         list[at + u * kLanes].order = __builtin_bit_cast(uint64_t, key64[u]);
+        list[at + u * kLanes].e = ce[u];
         rank[u] = 0;
       }
       __threadfence_block();
@@ -722,7 +772,10 @@ static dim3 route_grid(long long units, long long most) {
 template <typename El, int kLanes, int kN>
 static void launch_fast(const RouteArgs& p, int lanes_per_group, int per_lane, hipStream_t st) {
   constexpr int kTokens = 64 / kLanes;
-  const dim3 grid = route_grid(((long long)p.T + kTokens - 1) / kTokens, 2048);
+  // as many workgroups as the CUs hold, so that a wave loads its experts'
+  // biases once for several tokens
+  const dim3 grid = route_grid(((long long)p.T + kTokens - 1) / kTokens,
+                               256LL * route_waves(kLanes, kN));
   const dim3 block(64 * kRouteWaves);
   const size_t lds = kRouteWaves * (size_t)p.E * sizeof(double);
   // every lane's experts are whole 16-byte pieces of a row
@@ -752,20 +805,20 @@ static void launch_route(const RouteArgs& p, hipStream_t st) {
   const int g16 = p.groups <= 16 ? 16 / p.groups : 0, g64 = p.groups <= 64 ? 64 / p.groups : 0;
   const int n16 = g16 ? (size + g16 - 1) / g16 : 1 << 20;
   const int n64 = g64 ? (size + g64 - 1) / g64 : 1 << 20;
-  if (n16 <= 32 && p.K <= 16) {
+  if (n16 <= 16 && p.K <= 16) {
     if (n16 <= 2)
       launch_fast<El, 16, 2>(p, g16, n16, st);
     else if (n16 <= 4)
       launch_fast<El, 16, 4>(p, g16, n16, st);
     else if (n16 <= 8)
       launch_fast<El, 16, 8>(p, g16, n16, st);
-    else if (n16 <= 16)
-      launch_fast<El, 16, 16>(p, g16, n16, st);
     else
-      launch_fast<El, 16, 32>(p, g16, n16, st);
+      launch_fast<El, 16, 16>(p, g16, n16, st);
   } else if (n64 <= 16) {
     if (n64 <= 4)
       launch_fast<El, 64, 4>(p, g64, n64, st);
+    else if (n64 <= 8)
+      launch_fast<El, 64, 8>(p, g64, n64, st);
     else
       launch_fast<El, 64, 16>(p, g64, n64, st);
   } else {
