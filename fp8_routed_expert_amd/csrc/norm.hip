@@ -20,6 +20,7 @@
 namespace moe {
 
 constexpr int kNormParts = 512;     // workgroups that keep partial sums, at most
+constexpr int kNormRows = 4;        // rows that make another such workgroup worth its sums
 constexpr int kNormLong = 32768;    // bytes of a row that the registers of a workgroup hold
 
 struct NormArgs {
@@ -37,20 +38,30 @@ struct NormArgs {
   float* stats;      // [T][2], long rows
 };
 
+// The wave's sum, in every lane: rows of 16 lanes by lane permutations, then
+// their four sums.
 __device__ __forceinline__ float wave_add(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  v += dpp_row<0xb1>(v);
+  v += dpp_row<0x4e>(v);
+  v += dpp_row<0x141>(v);
+  v += dpp_row<0x140>(v);
+  const int i = __float_as_int(v);
+  return (__int_as_float(__builtin_amdgcn_readlane(i, 0)) +
+          __int_as_float(__builtin_amdgcn_readlane(i, 16))) +
+         (__int_as_float(__builtin_amdgcn_readlane(i, 32)) +
+          __int_as_float(__builtin_amdgcn_readlane(i, 48)));
 }
 
-// The sums of the kWaves waves that share a row, in every lane of them.
+// The sums of the kWaves waves that share a row, in every lane of them.  Two
+// sums that follow one another take two buffers, so that a sum costs one
+// barrier: whoever writes a buffer again has passed the barrier behind which
+// its last values were read.
 template <int kWaves, int kN>
 __device__ __forceinline__ void row_add(float (&v)[kN], float (*red)[kN]) {
 #pragma unroll
   for (int i = 0; i < kN; ++i) v[i] = wave_add(v[i]);
   if constexpr (kWaves > 1) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    __syncthreads();   // the last sum has been read
+    const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) % kWaves;
     if (lane == 0)
 #pragma unroll
       for (int i = 0; i < kN; ++i) red[wave][i] = v[i];
@@ -100,74 +111,99 @@ __device__ __forceinline__ void chunk_range(const RowShape& row, int c, int& lo,
   hi = row.bytes >= 16 ? El::kN : row.bytes / El::kSize;
 }
 
-// y of a chunk.
+// The weight (or bias, missing: `none`) of a lane's chunk c.
 template <typename El, typename W, bool kWhole>
-__device__ __forceinline__ void norm_store(const NormArgs& p, long long t, int c, float mu, float r,
-                                           float (&v)[El::kN]) {
-  constexpr int N = El::kN;
-  const int at = p.row.start(c) / El::kSize;
-  const int n = kWhole ? N : min(N, p.H - at);
-  float w[N], b[N];
+__device__ __forceinline__ void chunk_param(const uint8_t* p, const NormArgs& a, int c, float none,
+                                            float (&v)[El::kN]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) w[i] = 1.f, b[i] = 0.f;
-  if (p.w) load_param<W, N>(p.w, at, n, w);
-  if (p.b) load_param<W, N>(p.b, at, n, b);
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = fmaf((v[i] - mu) * r, w[i], b[i]);
-  store_chunk<kWhole>(p.y + t * p.row.bytes + p.row.start(c), p.row.bytes, El::pack(v));
+  for (int i = 0; i < El::kN; ++i) v[i] = none;
+  if (!p || c >= a.row.chunks) return;
+  const int at = a.row.start(c) / El::kSize;
+  load_param<W, El::kN>(p, at, kWhole ? El::kN : min(El::kN, a.H - at), v);
 }
 
-// kWaves waves to a row, which its lanes hold in kCh chunks each; kCh 0: a row
-// of any length, read again for each of its sums.
-template <typename El, typename W, int kWaves, int kCh, bool kWhole>
-__global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void norm_kernel(NormArgs p) {
+// kWaves waves to a row, which its lanes hold in kCh chunks each.  A workgroup
+// walks rows, so that a lane keeps the weight and bias of its columns, and the
+// next row is on its way while this one is summed.
+// Waves of a SIMD that the registers are shared out to, and the workgroups that
+// a CU then holds: a launch has no more, since a second round of workgroups
+// that walk would leave most CUs idle.
+constexpr int norm_waves(int waves, int ch) { return ch == 1 ? 8 : waves == 8 ? 6 : 4; }
+constexpr int norm_threads(int waves) { return waves == 1 ? 256 : 64 * waves; }
+constexpr int norm_groups(int waves, int ch) {
+  return 256 * 4 * norm_waves(waves, ch) * 64 / norm_threads(waves);
+}
+
+template <typename El, typename W, int kWaves, int kCh, bool kWhole, bool kStream>
+__global__ __launch_bounds__(norm_threads(kWaves), norm_waves(kWaves, kCh)) void
+norm_kernel(NormArgs p) {
   constexpr int N = El::kN, kStep = 64 * kWaves;
-  constexpr int kPer = kWaves >= 4 ? 1 : 4 / kWaves;   // rows of a workgroup
-  __shared__ float red[kWaves][1];
+  constexpr int kPer = kWaves == 1 ? 4 : 1;   // rows of a workgroup
+  __shared__ float red[2][kWaves][1];
   const int at = threadIdx.x % kStep;
   const float over = 1.f / (float)p.H;
-  for (long long t0 = (long long)blockIdx.x * kPer; t0 < p.T; t0 += (long long)gridDim.x * kPer) {
-    const long long t = t0 + (kPer > 1 ? threadIdx.x / kStep : 0);
-    if (kPer > 1 && t >= p.T) continue;   // (a wave of its own)
-    const uint8_t* src = p.x + t * p.row.bytes;
-    float v[kCh ? kCh : 1][N];
-    auto load = [&](int c, float (&f)[N]) {
-      El::unpack(load_chunk<kWhole>(src + p.row.start(c < p.row.chunks ? c : 0), p.row.bytes), f);
-    };
-    auto each = [&](auto f) __attribute__((always_inline)) {
-      if constexpr (kCh != 0) {
+  const long long step = (long long)gridDim.x * kPer;
+  long long t = (long long)blockIdx.x * kPer + (kPer > 1 ? threadIdx.x / kStep : 0);
+  if (t >= p.T) return;   // (all waves of a row)
+  uint4 raw[kCh];
+  auto load = [&](long long row) __attribute__((always_inline)) {
+    const uint8_t* src = p.x + row * p.row.bytes;
 #pragma unroll
-        for (int u = 0; u < kCh; ++u) f(at + u * kStep, v[u]);
-      } else {
-        for (int c = at; c < p.row.chunks; c += kStep) {
-          load(c, v[0]);
-          f(c, v[0]);
-        }
-      }
-    };
-    // the sum of f over the row's elements, each once
-    auto sum = [&](auto f) __attribute__((always_inline)) {
-      float s[1] = {0.f};
-      each([&](int c, float (&e)[N]) {
-        int lo = 0, hi = N;
-        if (!kWhole) chunk_range<El>(p.row, c, lo, hi);
-        if (c < p.row.chunks)
+    for (int u = 0; u < kCh; ++u) {
+      const int c = at + u * kStep;
+      raw[u] = load_chunk<kWhole, kStream>(src + p.row.start(c < p.row.chunks ? c : 0), p.row.bytes);
+    }
+  };
+  load(t);
+  float w[kCh][N], b[kCh][N];
+  int lo[kCh], hi[kCh];   // the elements of a chunk that count
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (kWhole || (i >= lo && i < hi)) s[0] += f(e[i]);
-      });
-      row_add<kWaves>(s, red);
-      return s[0];
-    };
-    if constexpr (kCh != 0)
+  for (int u = 0; u < kCh; ++u) {
+    const int c = at + u * kStep;
+    chunk_param<El, W, kWhole>(p.w, p, c, 1.f, w[u]);
+    chunk_param<El, W, kWhole>(p.b, p, c, 0.f, b[u]);
+    lo[u] = 0;
+    hi[u] = N;
+    if (!kWhole) chunk_range<El>(p.row, c, lo[u], hi[u]);
+    if (c >= p.row.chunks) hi[u] = 0;
+  }
+  for (; t < p.T; t += step) {
+    float v[kCh][N];
 #pragma unroll
-      for (int u = 0; u < kCh; ++u) load(at + u * kStep, v[u]);
-    const float mu = sum([](float e) { return e; }) * over;
-    const float var = sum([&](float e) { return (e - mu) * (e - mu); }) * over;
-    const float r = 1.f / sqrtf(var + p.eps);
-    each([&](int c, float (&e)[N]) {
-      if (c < p.row.chunks) norm_store<El, W, kWhole>(p, t, c, mu, r, e);
-    });
+    for (int u = 0; u < kCh; ++u) El::unpack(raw[u], v[u]);
+    load(t + step < p.T ? t + step : t);
+    float s[1] = {0.f};
+#pragma unroll
+    for (int u = 0; u < kCh; ++u)
+      if (!kWhole || hi[u])
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (kWhole || (i >= lo[u] && i < hi[u])) s[0] += v[u][i];
+    row_add<kWaves>(s, red[0]);
+    // (divided: the mean of equal values is that value, and no product with a
+    // rounded 1 / H that the subtraction below could be contracted with)
+    const float mu = s[0] / (float)p.H;
+    s[0] = 0.f;
+#pragma unroll
+    for (int u = 0; u < kCh; ++u) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[u][i] -= mu;
+      if (!kWhole || hi[u])
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (kWhole || (i >= lo[u] && i < hi[u])) s[0] = fmaf(v[u][i], v[u][i], s[0]);
+    }
+    row_add<kWaves>(s, red[1]);
+    const float r = 1.f / sqrtf(fmaf(s[0], over, p.eps));
+#pragma unroll
+    for (int u = 0; u < kCh; ++u) {
+      const int c = at + u * kStep;
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[u][i] = fmaf(v[u][i] * r, w[u][i], b[u][i]);
+      if (c < p.row.chunks)
+        store_chunk<kWhole>(p.y + t * p.row.bytes + p.row.start(c), p.row.bytes,
+                            pack_row<El>(v[u]));
+    }
     if (at == 0) {
       if (p.mean) p.mean[t] = mu;
       if (p.rstd) p.rstd[t] = r;
@@ -175,86 +211,183 @@ __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void norm_kernel(No
   }
 }
 
-// The gradient: a workgroup of kWaves waves walks rows, its lanes holding the
-// same kCh chunks of every row, and so the sums over the rows of their
-// columns.
-template <typename El, typename W, int kWaves, int kCh, bool kWhole>
-__global__ __launch_bounds__(64 * kWaves) void norm_grad_kernel(NormArgs p) {
-  constexpr int N = El::kN, kStep = 64 * kWaves;
-  __shared__ float red[kWaves][2];
-  const int at = threadIdx.x;
+// Rows of any length, read again for each of their sums.
+template <typename El, typename W>
+__global__ __launch_bounds__(256) void norm_long_kernel(NormArgs p) {
+  constexpr int N = El::kN;
+  __shared__ float red[2][4][1];
   const float over = 1.f / (float)p.H;
-  float dw[kCh][N], db[kCh][N];
-#pragma unroll
-  for (int u = 0; u < kCh; ++u)
-#pragma unroll
-    for (int i = 0; i < N; ++i) dw[u][i] = db[u][i] = 0.f;
   for (long long t = blockIdx.x; t < p.T; t += gridDim.x) {
-    const float mu = p.mean[t], r = p.rstd[t];
-    float z[kCh][N], g[kCh][N];
+    const uint8_t* src = p.x + t * p.row.bytes;
+    auto sum = [&](float (*buffer)[1], auto f) __attribute__((always_inline)) {
+      float s[1] = {0.f};
+      for (int c = threadIdx.x; c < p.row.chunks; c += 256) {
+        float e[N];
+        El::unpack(load_chunk<false>(src + p.row.start(c), p.row.bytes), e);
+        int lo, hi;
+        chunk_range<El>(p.row, c, lo, hi);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (i >= lo && i < hi) s[0] += f(e[i]);
+      }
+      row_add<4>(s, buffer);
+      return s[0];
+    };
+    const float mu = sum(red[0], [](float e) { return e; }) / (float)p.H;
+    const float var = sum(red[1], [&](float e) { return (e - mu) * (e - mu); }) * over;
+    const float r = 1.f / sqrtf(var + p.eps);
+    for (int c = threadIdx.x; c < p.row.chunks; c += 256) {
+      float e[N], w[N], b[N];
+      El::unpack(load_chunk<false>(src + p.row.start(c), p.row.bytes), e);
+      chunk_param<El, W, false>(p.w, p, c, 1.f, w);
+      chunk_param<El, W, false>(p.b, p, c, 0.f, b);
+#pragma unroll
+      for (int i = 0; i < N; ++i) e[i] = fmaf((e[i] - mu) * r, w[i], b[i]);
+      store_chunk<false>(p.y + t * p.row.bytes + p.row.start(c), p.row.bytes, pack_row<El>(e));
+    }
+    if (threadIdx.x == 0) {
+      if (p.mean) p.mean[t] = mu;
+      if (p.rstd) p.rstd[t] = r;
+    }
+  }
+}
+
+// The gradient: a workgroup walks rows, kRows at a time, kWaves waves to a row,
+// their lanes holding the same kCh chunks of every row, and so the sums over the
+// rows of their columns.  The next row is on its way while this one is summed.
+// (Rows of 64 chunks: 512 workgroups of one wave, one row at a time, left most
+// of the memory idle: 65536 rows of 512 bf16 66 us.)
+template <typename El, typename W, int kRows, int kWaves, int kCh, bool kWhole, bool kStream>
+__global__ __launch_bounds__(64 * kWaves * kRows) void norm_grad_kernel(NormArgs p) {
+  constexpr int N = El::kN, kStep = 64 * kWaves;
+  __shared__ float red[2][kRows * kWaves][2];
+  __shared__ float joined[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? 2 * kCh * N : 1]
+                         [kRows > 1 ? kStep : 1];
+  const int at = threadIdx.x % kStep, part = threadIdx.x / kStep;
+  const float over = 1.f / (float)p.H;
+  uint4 raw_x[kCh], raw_g[kCh];
+  float mu, r;
+  auto load = [&](long long t) __attribute__((always_inline)) {
+    if (t >= p.T) t = p.T - 1;
 #pragma unroll
     for (int u = 0; u < kCh; ++u) {
       const int c = at + u * kStep;
       const long long off = t * p.row.bytes + p.row.start(c < p.row.chunks ? c : 0);
-      El::unpack(load_chunk<kWhole>(p.x + off, p.row.bytes), z[u]);
-      El::unpack(load_chunk<kWhole>(p.dy + off, p.row.bytes), g[u]);
+      raw_x[u] = load_chunk<kWhole, kStream>(p.x + off, p.row.bytes);
+      raw_g[u] = load_chunk<kWhole, kStream>(p.dy + off, p.row.bytes);
     }
+    mu = p.mean[t];
+    r = p.rstd[t];
+  };
+  const long long step = (long long)gridDim.x * kRows;
+  long long t = (long long)blockIdx.x * kRows + part;
+  load(t);
+  float w[kCh][N], dw[kCh][N], db[kCh][N];
+  int lo[kCh], hi[kCh];   // the elements of a chunk that count
+#pragma unroll
+  for (int u = 0; u < kCh; ++u) {
+    const int c = at + u * kStep;
+    chunk_param<El, W, kWhole>(p.w, p, c, 1.f, w[u]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[u][i] = db[u][i] = 0.f;
+    lo[u] = 0;
+    hi[u] = N;
+    if (!kWhole) chunk_range<El>(p.row, c, lo[u], hi[u]);
+    if (c >= p.row.chunks) hi[u] = 0;
+  }
+  int parity = 0;
+  for (; t - part < p.T; t += step) {   // (the same for all of a workgroup's rows)
+    const bool live = t < p.T;
+    float z[kCh][N], g[kCh][N];
+    const float rt = r, mut = mu;
+#pragma unroll
+    for (int u = 0; u < kCh; ++u) {
+      El::unpack(raw_x[u], z[u]);
+      El::unpack(raw_g[u], g[u]);
+    }
+    load(t + step);
     float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < kCh; ++u)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const bool in = live && (kWhole ? hi[u] != 0 : i >= lo[u] && i < hi[u]);
+        z[u][i] = (z[u][i] - mut) * rt;
+        if (!in) g[u][i] = z[u][i] = 0.f;
+        dw[u][i] = fmaf(g[u][i], z[u][i], dw[u][i]);
+        db[u][i] += g[u][i];
+        g[u][i] *= w[u][i];
+        s[0] += g[u][i];
+        s[1] = fmaf(g[u][i], z[u][i], s[1]);
+      }
+    if (!p.y) continue;
+    row_add<kWaves>(s, red[parity] + part * kWaves);
+    parity ^= 1;
+    const float c1 = s[0] * over, c2 = s[1] * over;
 #pragma unroll
     for (int u = 0; u < kCh; ++u) {
       const int c = at + u * kStep;
-      int lo = 0, hi = N;
-      if (!kWhole) chunk_range<El>(p.row, c, lo, hi);
-      if (c >= p.row.chunks) hi = 0;
-      const int first = p.row.start(c < p.row.chunks ? c : 0) / El::kSize;
-      float w[N];
+      float d[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = 1.f;
-      if (p.w) load_param<W, N>(p.w, first, kWhole ? N : min(N, p.H - first), w);
+      for (int i = 0; i < N; ++i) d[i] = rt * (g[u][i] - c1 - z[u][i] * c2);
+      if (c >= p.row.chunks || !live) continue;
+      uint8_t* out = p.y + t * p.row.bytes + p.row.start(c);
+      if (kWhole || lo[u] == 0) {
+        store_chunk<kWhole>(out, p.row.bytes, pack_row<El>(d));
+      } else {
+        // (the elements that the chunk before holds too were left out here)
+        const uint4 v = pack_row<El>(d);
+        alignas(16) uint8_t byte[16];
+        __builtin_memcpy(byte, &v, 16);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const bool in = kWhole ? hi != 0 : i >= lo && i < hi;
-        z[u][i] = (z[u][i] - mu) * r;
-        if (in) {
-          dw[u][i] = fmaf(g[u][i], z[u][i], dw[u][i]);
-          db[u][i] += g[u][i];
-        }
-        g[u][i] *= w[i];
-        if (in) {
-          s[0] += g[u][i];
-          s[1] = fmaf(g[u][i], z[u][i], s[1]);
-        }
-      }
-    }
-    if (p.y) {
-      row_add<kWaves>(s, red);
-      const float c1 = s[0] * over, c2 = s[1] * over;
-#pragma unroll
-      for (int u = 0; u < kCh; ++u) {
-        const int c = at + u * kStep;
-        float d[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) d[i] = r * (g[u][i] - c1 - z[u][i] * c2);
-        if (c < p.row.chunks)
-          store_chunk<kWhole>(p.y + t * p.row.bytes + p.row.start(c), p.row.bytes, El::pack(d));
+        for (int i = 0; i < 16; ++i)
+          if (i >= lo[u] * El::kSize) out[i] = byte[i];
       }
     }
   }
   if (!p.parts) return;
+  if constexpr (kRows > 1) {
+    if (part > 0)
+#pragma unroll
+      for (int u = 0; u < kCh; ++u)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          joined[part - 1][2 * (u * N + i)][at] = dw[u][i];
+          joined[part - 1][2 * (u * N + i) + 1][at] = db[u][i];
+        }
+    __syncthreads();
+    if (part > 0) return;
+    for (int q = 0; q < kRows - 1; ++q)
+#pragma unroll
+      for (int u = 0; u < kCh; ++u)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          dw[u][i] += joined[q][2 * (u * N + i)][at];
+          db[u][i] += joined[q][2 * (u * N + i) + 1][at];
+        }
+  }
   float* out = p.parts + (size_t)blockIdx.x * 2 * p.H;
 #pragma unroll
   for (int u = 0; u < kCh; ++u) {
     const int c = at + u * kStep;
     if (c >= p.row.chunks) continue;
-    int lo = 0, hi = N;
-    if (!kWhole) chunk_range<El>(p.row, c, lo, hi);
     const int first = p.row.start(c) / El::kSize;
+    if (kWhole) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (kWhole || (i >= lo && i < hi)) {
-        out[first + i] = dw[u][i];
-        out[p.H + first + i] = db[u][i];
+      for (int i = 0; i < N; i += 4) {
+        *reinterpret_cast<float4*>(out + first + i) =
+            make_float4(dw[u][i], dw[u][i + 1], dw[u][i + 2], dw[u][i + 3]);
+        *reinterpret_cast<float4*>(out + p.H + first + i) =
+            make_float4(db[u][i], db[u][i + 1], db[u][i + 2], db[u][i + 3]);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i >= lo[u] && i < hi[u]) {
+          out[first + i] = dw[u][i];
+          out[p.H + first + i] = db[u][i];
+        }
+    }
   }
 }
 
@@ -262,7 +395,8 @@ __global__ __launch_bounds__(64 * kWaves) void norm_grad_kernel(NormArgs p) {
 template <typename El, typename W>
 __global__ __launch_bounds__(256) void norm_grad_sums_kernel(NormArgs p) {
   constexpr int N = El::kN;
-  __shared__ float red[4][2];
+  __shared__ float red[2][4][2];
+  int parity = 0;
   for (long long t = blockIdx.x; t < p.T; t += gridDim.x) {
     const float mu = p.mean[t], r = p.rstd[t];
     float s[2] = {0.f, 0.f};
@@ -283,7 +417,8 @@ __global__ __launch_bounds__(256) void norm_grad_sums_kernel(NormArgs p) {
           s[1] = fmaf(g[i] * w[i], (x[i] - mu) * r, s[1]);
         }
     }
-    row_add<4>(s, red);
+    row_add<4>(s, red[parity]);
+    parity ^= 1;
     if (threadIdx.x == 0) {
       p.stats[2 * t] = s[0];
       p.stats[2 * t + 1] = s[1];
@@ -320,7 +455,7 @@ __global__ __launch_bounds__(256) void norm_grad_strip_kernel(NormArgs p) {
       db[i] += g[i];
       g[i] = r * (g[i] * w[i] - c1 - z * c2);
     }
-    if (p.y) store_chunk<false>(p.y + off, p.row.bytes, El::pack(g));
+    if (p.y) store_chunk<false>(p.y + off, p.row.bytes, pack_row<El>(g));
   }
   if (!p.parts) return;
   float* out = p.parts + (size_t)blockIdx.y * 2 * p.H;
@@ -332,29 +467,45 @@ __global__ __launch_bounds__(256) void norm_grad_strip_kernel(NormArgs p) {
     }
 }
 
-// dw and db from the partial sums: 32 columns to a workgroup, whose eight
-// groups of 32 lanes each add every eighth part, in order.
-template <typename W>
+// dw and db from the partial sums: 32 columns to a workgroup, four to a lane;
+// its 32 groups of eight lanes each add every 32nd part, in order, and their
+// sums are added in order too.
+template <typename W, bool kWide>
 __global__ __launch_bounds__(256) void norm_join_kernel(const float* __restrict__ parts, int n,
                                                         int H, uint8_t* __restrict__ dw,
                                                         uint8_t* __restrict__ db) {
-  __shared__ float red[8][32];
-  const int col = threadIdx.x & 31, group = threadIdx.x >> 5;
+  __shared__ float red[32][33];
+  const int col = (threadIdx.x & 7) * 4, group = threadIdx.x >> 3;
   const long long all = 2LL * H;
   const long long j = (long long)blockIdx.x * 32 + col;   // dw's columns, then db's
-  float s = 0.f;
-  if (j < all)
-    for (int i = group; i < n; i += 8) s += parts[i * all + j];
-  red[group][col] = s;
-  __syncthreads();
-  if (group != 0 || j >= all) return;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (j < all) {
+#pragma unroll 8
+    for (int i = group; i < n; i += 32) {
+      const float* p = parts + i * all + j;
+      if (kWide) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+      } else {
 #pragma unroll
-  for (int i = 1; i < 8; ++i) s += red[i][col];
-  uint8_t* out = j < H ? dw : db;
+        for (int u = 0; u < 4; ++u) s[u] += j + u < all ? p[u] : 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) red[group][col + u] = s[u];
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  float sum = red[0][threadIdx.x];
+#pragma unroll
+  for (int i = 1; i < 32; ++i) sum += red[i][threadIdx.x];
+  const long long at = (long long)blockIdx.x * 32 + threadIdx.x;
+  if (at >= all) return;
+  uint8_t* out = at < H ? dw : db;
   if (!out) return;
-  float v[W::kN] = {s};
+  float v[W::kN] = {sum};
   const uint4 c = W::pack(v);
-  __builtin_memcpy(out + (j < H ? j : j - H) * W::kSize, &c, W::kSize);
+  __builtin_memcpy(out + (at < H ? at : at - H) * W::kSize, &c, W::kSize);
 }
 
 static int norm_type_size(int dtype) {
@@ -396,36 +547,80 @@ static unsigned walk(long long n) {
   return (unsigned)(n < 1 ? 1 : n > (1 << 22) ? (1 << 22) : n);
 }
 
+// Reads past the caches where they are more than the memory-side cache (256
+// MB) keeps: 65536 rows of 7168 bf16 343 us against 352, the gradient of 32768
+// 270 against 279; but 65536 rows of 2048 96 against 88.
+static bool norm_streams(const NormArgs& p) {
+  return (long long)p.T * p.row.bytes * (p.dy ? 2 : 1) > (400LL << 20);
+}
+
+template <typename El, typename W, int kWaves, int kCh, bool kWhole>
+static void launch_norm_as(const NormArgs& p, hipStream_t st) {
+  constexpr long long most = norm_groups(kWaves, kCh);
+  constexpr int kPer = kWaves == 1 ? 4 : 1;
+  const long long blocks = ((long long)p.T + kPer - 1) / kPer;
+  const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(norm_threads(kWaves));
+  if (norm_streams(p))
+    hipLaunchKernelGGL((norm_kernel<El, W, kWaves, kCh, kWhole, true>), grid, block, 0, st, p);
+  else
+    hipLaunchKernelGGL((norm_kernel<El, W, kWaves, kCh, kWhole, false>), grid, block, 0, st, p);
+}
+
 template <typename El, typename W, bool kWhole>
 static void launch_norm(const NormArgs& p, hipStream_t st) {
   const int c = p.row.chunks;
-  if (c <= 64)
-    hipLaunchKernelGGL((norm_kernel<El, W, 1, 1, kWhole>), dim3(walk((p.T + 3LL) / 4)), dim3(256),
-                       0, st, p);
+  if (p.row.bytes > kNormLong)
+    hipLaunchKernelGGL((norm_long_kernel<El, W>), dim3(walk(p.T)), dim3(256), 0, st, p);
+  else if (c <= 64)
+    launch_norm_as<El, W, 1, 1, kWhole>(p, st);
+  else if (c <= 128)
+    launch_norm_as<El, W, 2, 1, kWhole>(p, st);
   else if (c <= 256)
-    hipLaunchKernelGGL((norm_kernel<El, W, 4, 1, kWhole>), dim3(walk(p.T)), dim3(256), 0, st, p);
+    launch_norm_as<El, W, 4, 1, kWhole>(p, st);
+  else if (c <= 512)
+    launch_norm_as<El, W, 8, 1, kWhole>(p, st);
+  else if (c <= 1024 && p.T <= 512)   // (a row as fast as it goes: 16 waves to it)
+    launch_norm_as<El, W, 16, 1, kWhole>(p, st);
   else if (c <= 1024)
-    hipLaunchKernelGGL((norm_kernel<El, W, 4, 4, kWhole>), dim3(walk(p.T)), dim3(256), 0, st, p);
-  else if (p.row.bytes <= kNormLong)
-    hipLaunchKernelGGL((norm_kernel<El, W, 16, 2, kWhole>), dim3(walk(p.T)), dim3(1024), 0, st, p);
+    launch_norm_as<El, W, 8, 2, kWhole>(p, st);
   else
-    hipLaunchKernelGGL((norm_kernel<El, W, 4, 0, kWhole>), dim3(walk(p.T)), dim3(256), 0, st, p);
+    launch_norm_as<El, W, 16, 2, kWhole>(p, st);
+}
+
+template <typename El, typename W, int kRows, int kWaves, int kCh, bool kWhole>
+static void launch_norm_grad_as(const NormArgs& p, int parts, hipStream_t st) {
+  const dim3 grid((unsigned)parts), block(64 * kWaves * kRows);
+  if (norm_streams(p))
+    hipLaunchKernelGGL((norm_grad_kernel<El, W, kRows, kWaves, kCh, kWhole, true>), grid, block, 0,
+                       st, p);
+  else
+    hipLaunchKernelGGL((norm_grad_kernel<El, W, kRows, kWaves, kCh, kWhole, false>), grid, block,
+                       0, st, p);
+}
+
+// Workgroups with partial sums: as many as the CUs hold at once, each with
+// enough rows to be worth its sums.
+static int norm_parts(const NormArgs& p) {
+  const long long least = (long long)p.T / kNormRows + (p.T % kNormRows != 0);
+  const int most = p.row.chunks > 512 ? kNormParts / 2 : kNormParts;
+  return (int)(least < most ? least : most);
 }
 
 template <typename El, typename W, bool kWhole>
 static void launch_norm_grad(const NormArgs& p, int parts, hipStream_t st) {
   const int c = p.row.chunks;
-  const dim3 grid((unsigned)parts);
   if (c <= 64)
-    hipLaunchKernelGGL((norm_grad_kernel<El, W, 1, 1, kWhole>), grid, dim3(64), 0, st, p);
+    launch_norm_grad_as<El, W, 8, 1, 1, kWhole>(p, parts, st);
+  else if (c <= 128)
+    launch_norm_grad_as<El, W, 4, 2, 1, kWhole>(p, parts, st);
   else if (c <= 256)
-    hipLaunchKernelGGL((norm_grad_kernel<El, W, 4, 1, kWhole>), grid, dim3(256), 0, st, p);
+    launch_norm_grad_as<El, W, 2, 4, 1, kWhole>(p, parts, st);
   else if (c <= 512)
-    hipLaunchKernelGGL((norm_grad_kernel<El, W, 8, 1, kWhole>), grid, dim3(512), 0, st, p);
+    launch_norm_grad_as<El, W, 1, 8, 1, kWhole>(p, parts, st);
   else if (c <= 1024)
-    hipLaunchKernelGGL((norm_grad_kernel<El, W, 8, 2, kWhole>), grid, dim3(512), 0, st, p);
+    launch_norm_grad_as<El, W, 1, 16, 1, kWhole>(p, parts, st);
   else
-    hipLaunchKernelGGL((norm_grad_kernel<El, W, 16, 2, kWhole>), grid, dim3(1024), 0, st, p);
+    launch_norm_grad_as<El, W, 1, 16, 2, kWhole>(p, parts, st);
 }
 
 }  // namespace moe
@@ -494,12 +689,12 @@ extern "C" moe_status_t moe_layer_norm_grad(const void* dy, const void* x, int d
       (((uintptr_t)mean | (uintptr_t)rstd) & 3) || ((uintptr_t)workspace & 15))
     return MOE_UNSUPPORTED_SHAPE;
   if (T == 0 && !params) return MOE_OK;
-  const int parts = T < kNormParts ? T : kNormParts;
   p.x = static_cast<const uint8_t*>(x);
   p.dy = static_cast<const uint8_t*>(dy);
   p.w = static_cast<const uint8_t*>(weight);
   p.T = T;
   p.H = H;
+  const int parts = norm_parts(p);
   p.y = static_cast<uint8_t*>(dx);
   p.mean = const_cast<float*>(mean);
   p.rstd = const_cast<float*>(rstd);
@@ -530,8 +725,12 @@ extern "C" moe_status_t moe_layer_norm_grad(const void* dy, const void* x, int d
     uint8_t* dw = static_cast<uint8_t*>(dweight);
     uint8_t* db = static_cast<uint8_t*>(dbias);
     by_type(w_dtype, w_dtype, [&](auto el, auto) {
-      hipLaunchKernelGGL((norm_join_kernel<decltype(el)>), grid, dim3(256), 0, st, ws, parts, H,
-                         dw, db);
+      if (H % 2 == 0)
+        hipLaunchKernelGGL((norm_join_kernel<decltype(el), true>), grid, dim3(256), 0, st, ws,
+                           parts, H, dw, db);
+      else
+        hipLaunchKernelGGL((norm_join_kernel<decltype(el), false>), grid, dim3(256), 0, st, ws,
+                           parts, H, dw, db);
     });
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;

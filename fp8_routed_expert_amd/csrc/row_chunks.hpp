@@ -10,6 +10,8 @@
 // single bytes.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.hpp"
 
 namespace moe {
@@ -63,6 +65,24 @@ struct F16 {
     return __builtin_bit_cast(uint4, h);
   }
 };
+
+// A chunk of rounded values; bf16 in the hardware's conversion (to nearest
+// even, as BF16::pack, a NaN stays one).
+template <typename El>
+__device__ __forceinline__ uint4 pack_row(const float (&f)[El::kN]) {
+  if constexpr (std::is_same<El, BF16>::value) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = __builtin_bit_cast(
+          uint32_t, __builtin_convertvector((f32x2){f[2 * i], f[2 * i + 1]}, bf16x2));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    return El::pack(f);
+  }
+}
 
 // A row's chunks: chunk c starts at byte start(c).
 struct RowShape {
