@@ -660,11 +660,16 @@ def moe_route_tokens(logits, topk_idx, topk_w, status, bias=None, score=SCORE_SO
     others -1 (local_experts None: up to the last expert)."""
     T, E = _matrix(logits, "logits")
     K = _matrix(topk_idx, "topk_idx")[1]
+    if local_experts is None:
+        local_experts = E - first_expert
+    numbers = groups, top_groups, first_expert, local_experts
+    if max(numbers) > _INT_MAX or min(numbers) < 0:
+        raise ValueError(f"moe_route_tokens: numbers {numbers} outside [0, {_INT_MAX}]")
     dev = logits.get_device()
     _call("moe_route_tokens", stream, dev, _arg(logits, _FLOATS, "logits", dev),
           _type(logits, "logits"), T, E, _opt(bias, _F32, "bias", dev, (E,)), score, groups,
           top_groups, group_best, K, bool(renorm), scale, first_expert,
-          E - first_expert if local_experts is None else local_experts,
+          local_experts,
           _arg(topk_idx, _I32, "topk_idx", dev, (T, K)),
           _opt(local_idx, _I32, "local_idx", dev, (T, K)),
           _arg(topk_w, _F32, "topk_w", dev, (T, K)), _opt(scores, _F32, "scores", dev, (T, E)),
@@ -689,11 +694,15 @@ def moe_route_tokens_grad(logits, topk_idx, dtopk_w, dlogits, status, score=SCOR
 def _param_type(x, *params):
     """The one type of the weights, biases and their gradients that are given
     (x's, or float32)."""
-    types = {t.dtype for t in params if t is not None}
-    if len(types) > 1:
-        raise TypeError(f"weight and bias of different types: {types}")
-    dt = types.pop() if types else x.dtype
-    if dt not in (x.dtype, torch.float32):
+    dt = None
+    for t in params:
+        if t is not None and t.dtype != dt:
+            if dt is not None:
+                raise TypeError(f"weight and bias of different types: {dt}, {t.dtype}")
+            dt = t.dtype
+    if dt is None:
+        return x.dtype
+    if dt != x.dtype and dt != torch.float32:
         raise TypeError(f"weight: dtype {dt}, must be x's or float32")
     return dt
 
