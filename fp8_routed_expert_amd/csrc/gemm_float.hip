@@ -26,107 +26,11 @@ struct FloatArgs {
   uint8_t* out;
   int out_type;
   int32_t* status;
+  int splits;   // of a segment, for the weights' gradient: 1, or as many fp32 outputs
 };
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-// fp32: a 64 x 64 tile by four waves of 32 x 32, l advancing 32 a step through
-// LDS.  A lane's fragment is eight values of l of one row; an instruction takes
-// one of them from every lane, the same one of both operands.
-template <int kMode>
-__global__ __launch_bounds__(256) void float_tile_kernel(FloatArgs p) {
-  typedef float El;
-  typedef float Frag __attribute__((ext_vector_type(8)));
-  constexpr int BM = 64, BN = 64, BL = 32, kPitch = BL + 8;
-  __shared__ __attribute__((aligned(16))) El sp[BM][kPitch], sq[BN][kPitch];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (blockIdx.x == 0 && threadIdx.x < 64 && p.status &&
-      segments_bad(p.offsets, p.counts, p.E, lane) && lane == 0)
-    atomicOr(p.status, MOE_ERR_BAD_INDEX);
-  // operands of the tile: rows [i0, i_end) of P, [j0, j_end) of Q, L products
-  const int width = kMode == kProduct ? p.N : p.K;
-  const int n_tiles = (width + BN - 1) / BN;
-  const int tile_i = blockIdx.x / n_tiles;
-  const int j0 = (blockIdx.x - tile_i * n_tiles) * BN, j_end = width;
-  int e = 0, i0 = 0, i_end = 0, L;
-  const El* P = reinterpret_cast<const El*>(p.p);
-  const El* Q = reinterpret_cast<const El*>(p.q);
-  size_t pp, qp;   // elements from one row of memory to the next
-  if (kMode == kWeightsGrad) {
-    int s, en;
-    const int i_tiles = (p.N + BM - 1) / BM;
-    e = tile_i / i_tiles;
-    expert_rows(p.offsets, p.counts, e, p.rows, s, en);
-    i0 = (tile_i - e * i_tiles) * BM;
-    i_end = p.N;
-    L = en - s;
-    pp = p.N;
-    qp = p.K;
-    P += (size_t)s * pp;
-    Q += (size_t)s * qp;
-  } else {
-    find_mtile<BM>(p.offsets, p.counts, p.E, p.rows, tile_i, lane, e, i0, i_end);
-    if (e < 0) return;
-    L = kMode == kProduct ? p.K : p.N;
-    pp = L;
-    qp = p.K;
-    Q += (size_t)e * p.N * p.K;
-  }
-  const El zero = (El)0;
-  // eight elements of memory a thread and step: along l, or along the row
-  auto stage = [&](El (*tile)[kPitch], const El* base, size_t pitch, bool along_l, int r0,
-                   int r_end, int l0) {
-    const int fast = along_l ? (threadIdx.x & 3) * 8 : (threadIdx.x & 7) * 8;
-    const int slow = along_l ? threadIdx.x >> 2 : threadIdx.x >> 3;
-    const int r = r0 + (along_l ? slow : fast), l = l0 + (along_l ? fast : slow);
-    El v[8];
-    const bool in = r < r_end && l < L;   // (both are in steps of eight along memory)
-    const El* src = base + (along_l ? (size_t)r * pitch + l : (size_t)l * pitch + r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = in ? src[i] : zero;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (along_l)
-        tile[slow][fast + i] = v[i];
-      else
-        tile[fast + i][slow] = v[i];
-  };
-  v4f acc[2][2] = {};
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  const int g = lane >> 4, r16 = lane & 15;
-  for (int l0 = 0; l0 < L; l0 += BL) {
-    __syncthreads();
-    stage(sp, P, pp, kMode != kWeightsGrad, i0, i_end, l0);
-    stage(sq, Q, qp, kMode == kProduct, j0, j_end, l0);
-    __syncthreads();
-    Frag fp[2], fq[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      __builtin_memcpy(&fp[u], &sp[wm + 16 * u + r16][8 * g], sizeof(Frag));
-      __builtin_memcpy(&fq[u], &sq[wn + 16 * u + r16][8 * g], sizeof(Frag));
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          acc[u][v] = __builtin_amdgcn_mfma_f32_16x16x4f32(fq[v][i], fp[u][i], acc[u][v], 0, 0, 0);
-  }
-  // sums (u, v) of a lane: row r16 of P, four neighbours 4 g .. 4 g + 3 of Q
-#pragma unroll
-  for (int u = 0; u < 2; ++u)
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int i = i0 + wm + 16 * u + r16, j = j0 + wn + 16 * v + 4 * g;
-      if (i >= i_end || j >= j_end) continue;
-      const size_t at = ((kMode == kWeightsGrad ? (size_t)e * p.N : 0) + i) * width + j;
-      const v4f s = acc[u][v];
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) =
-          make_float4(s[0], s[1], s[2], s[3]);
-    }
-}
 
 template <int i>
 using Int = std::integral_constant<int, i>;
@@ -152,25 +56,30 @@ struct Stage {
 
 constexpr uint32_t kOutOfRange = 0x80000000u;
 
-// An operand of a 16-bit tile, B rows of 64 l (a step) in 128 B bytes of LDS.
+// An operand of a tile: B rows of a step's l's (64, in fp32 32) in 128 B bytes of
+// LDS.
 //
 // Contiguous along l (kSlow false): as the 8-bit products have it, a row of
 // the tile is 128 bytes of LDS, its 16-byte pieces permuted (swz), and a lane's
-// fragment is pieces 2 g and 2 g + 1: l = 16 g .. 16 g + 15.
+// fragment is pieces 2 g and 2 g + 1: l = 16 g .. 16 g + 15 (fp32: 8 g .. 8 g + 7).
 //
-// Contiguous along the rows (kSlow true): the step's 64 values of l are lines
-// of 2 B bytes.  Line 16 u + 4 t + g of the stage holds l = 16 g + 4 u + t, so
+// Contiguous along the rows (kSlow true), fp32: the step's l's are lines of
+// 4 B bytes, of which a lane reads its row's element of eight.  (The four g's
+// meet in a bank; the matrix cores take eight times as long in fp32 and hide it.)
+//
+// The same in 16 bits: the step's 64 values of l are lines of 2 B bytes.  Line 16 u + 4 t + g of the stage holds l = 16 g + 4 u + t, so
 // that the four lines t of a group of 16 lanes, which ds_read_b64_tr_b16 turns
 // into four l of 16 rows, belong to the same g as the other operand's fragment.
 // Those 16 lanes read 32 bytes of each of the lines t = 0 .. 3, and the group
 // next to them (g + 1) of four others: the 32-byte columns of a line are
 // permuted by 2 t + g % 2 (64-byte-row lines: by t; neighbours then lie in
 // other banks by themselves), so the eight lines lie in different banks.
-template <int B, bool kSlow>
+template <int B, bool kSlow, int kSize>
 struct Operand {
-  static constexpr int kLine = 2 * B;             // bytes of a line (slow)
+  static constexpr int kStepL = kBK / kSize;      // l's of a step
+  static constexpr int kLine = kSize * B;         // bytes of a line (slow)
   static constexpr int kPieces = kLine / 16;      // of a line
-  static constexpr int kReads = kSlow ? 4 : 2;    // LDS reads of a fragment
+  static constexpr int kReads = !kSlow ? 2 : kSize == 2 ? 4 : 8;   // LDS reads of a fragment
   uint32_t vl[2];     // a lane's offset in a chunk's memory, by the chunk's parity
   int lim[2];         // (along l) l's left behind the lane's piece, in bytes
   FragLane frag;      // (slow: lo only)
@@ -188,9 +97,13 @@ struct Operand {
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
         vl[o] = (uint32_t)(lane >> 3) * pitch + (uint32_t)((piece ^ o) << 4);
-        lim[o] = 2 * L - ((piece ^ o) << 4);
+        lim[o] = kSize * L - ((piece ^ o) << 4);
       }
       frag = frag_lane(w0, r16, g);
+    } else if constexpr (kSize == 4) {
+      vl[0] = vl[1] = (uint32_t)(lane / kPieces) * pitch + (uint32_t)((lane % kPieces) << 4);
+      frag.lo = (uint32_t)(8 * g * kLine + (w0 + r16) * 4);
+      frag.hi = 0;
     } else {
       const int at = lane % kPieces, line = lane / kPieces;
       if constexpr (B == 256) {        // lines g % 2
@@ -220,7 +133,7 @@ struct Operand {
     } else {
       base = (uint64_t)(uintptr_t)p;
       bytes = n;
-      step = 64LL * pitch;
+      step = (long long)kStepL * pitch;
     }
   }
   // chunks [wave * kC, wave * kC + kC) of step kb into its stage; steps are
@@ -249,7 +162,10 @@ struct Operand {
 #pragma unroll
       for (int u = 0; u < kC; ++u) {
         const int c = wave * kC + u;
-        if constexpr (B == 256) {
+        if constexpr (kSize == 4) {
+          dma16_add(r, stage + c * 1024, vl[0],
+                    __builtin_amdgcn_readfirstlane((uint32_t)(c * (64 / kPieces)) * pitch));
+        } else if constexpr (B == 256) {
           const uint32_t t = (uint32_t)((c >> 1) & 3);
           dma16_split(r, stage + c * 1024, vl[0], __builtin_amdgcn_readfirstlane(t * 64u),
                       __builtin_amdgcn_readfirstlane(
@@ -271,6 +187,12 @@ struct Operand {
   __device__ __forceinline__ v8i load(const uint8_t* stage, int i) const {
     if constexpr (!kSlow) {
       return load_frag_at(stage, i * 16 * kBK, frag);
+    } else if constexpr (kSize == 4) {
+      v8i r;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        r[u] = *reinterpret_cast<const int*>(stage + frag.lo + u * kLine + i * 64);
+      return r;
     } else {
       typedef short s4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s4 lds_s4;
@@ -293,14 +215,26 @@ struct Operand {
   }
 };
 
-template <int kType>
-__device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
-  if constexpr (kType == MOE_TYPE_BF16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+// c += the products of half h of two fragments (16 bits: eight l's of a lane in
+// one instruction; fp32: four, one of every lane to an instruction).
+template <int kType, int h>
+__device__ __forceinline__ v4f multiply_half(const v8i& a, const v8i& b, v4f c) {
+  if constexpr (kType == MOE_TYPE_F32) {
+#pragma unroll
+    for (int i = 4 * h; i < 4 * h + 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__int_as_float(a[i]), __int_as_float(b[i]), c, 0, 0,
+                                               0);
+    return c;
+  } else {
+    const v4i x = {a[4 * h], a[4 * h + 1], a[4 * h + 2], a[4 * h + 3]};
+    const v4i y = {b[4 * h], b[4 * h + 1], b[4 * h + 2], b[4 * h + 3]};
+    if constexpr (kType == MOE_TYPE_BF16)
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x),
+                                                     __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x),
+                                                    __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+  }
 }
 
 __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
@@ -308,15 +242,16 @@ __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, (h2){(_Float16)lo, (_Float16)hi});
 }
 
-// The 16-bit products: a BM x BN tile by waves of WM x WN, l advancing 64 a
-// step.  The operands go from global memory straight into LDS, P's a step
+// A BM x BN tile by waves of WM x WN, l advancing 128 bytes a step.  The operands go from global memory straight into LDS, P's a step
 // further ahead than Q's; the pipeline is that of the 8-bit products (waits and
 // barriers are explained there): the next step's loads go out first, the step's
 // barrier comes once a wave's last LDS read of it has landed, and the next
 // step's fragments are read under the last subtile row's multiplications.
 // kDeep: 0, or the stages of both operands for launches of few tiles.
 template <int kType, int kMode, int BM, int BN, int WM, int WN, int GM, int kDeep, bool kRagged>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void half_tile_kernel(FloatArgs p) {
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void float_tile_kernel(FloatArgs p) {
+  constexpr int kSize = kType == MOE_TYPE_F32 ? 4 : 2;
+  constexpr int kStepL = kBK / kSize;
   constexpr int NWN = BN / WN;
   constexpr int NW = BM / WM * NWN;
   constexpr int MI = WM / 16, NJ = WN / 16;
@@ -335,7 +270,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void half_tile_kernel(F
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int width = kMode == kProduct ? p.N : p.K;
-  if (blockIdx.x == 0 && threadIdx.x < 64 && p.status &&
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 64 && p.status &&
       segments_bad(p.offsets, p.counts, p.E, lane) && lane == 0)
     atomicOr(p.status, MOE_ERR_BAD_INDEX);
   const int n_tiles = (width + BN - 1) / BN;
@@ -357,6 +292,14 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void half_tile_kernel(F
     expert_rows(p.offsets, p.counts, e, p.rows, s0, en);
     s0 = __builtin_amdgcn_readfirstlane(s0);
     L = __builtin_amdgcn_readfirstlane(en) - s0;
+    if (p.splits > 1) {
+      // this workgroup's steps of the segment
+      const int steps = (L + kStepL - 1) / kStepL;
+      const int per = (steps + p.splits - 1) / p.splits * kStepL;
+      const int skip = min(L, per * (int)blockIdx.y);
+      s0 += skip;
+      L = min(L - skip, per);
+    }
     row0 = (tile_m - e * i_tiles) * BM;
     row_end = p.N;
   } else {
@@ -367,25 +310,26 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void half_tile_kernel(F
 
   // ---- operands
   constexpr bool kSlowA = kMode == kWeightsGrad, kSlowB = kMode != kProduct;
-  Operand<BM, kSlowA> A;
-  Operand<BN, kSlowB> B;
-  const uint32_t pitch_a = 2u * (uint32_t)(kMode == kProduct ? p.K : p.N);
-  const uint32_t pitch_b = 2u * (uint32_t)p.K;
+  Operand<BM, kSlowA, kSize> A;
+  Operand<BN, kSlowB, kSize> B;
+  const uint32_t pitch_a = (uint32_t)kSize * (uint32_t)(kMode == kProduct ? p.K : p.N);
+  const uint32_t pitch_b = (uint32_t)kSize * (uint32_t)p.K;
   const int wm = wave / NWN, wn = wave - wm * NWN;
   A.lanes(lane, pitch_a, L, wm * WM);
   B.lanes(lane, pitch_b, L, wn * WN);
   if constexpr (kMode == kWeightsGrad)
-    A.tile(p.p + (size_t)s0 * pitch_a + 2 * row0, (long long)L * pitch_a - 2 * row0, pitch_a);
+    A.tile(p.p + (size_t)s0 * pitch_a + kSize * row0, (long long)L * pitch_a - kSize * row0,
+           pitch_a);
   else
     A.tile(p.p + (size_t)row0 * pitch_a, (long long)(p.rows - row0) * pitch_a, pitch_a);
   const uint8_t* we = p.q + (size_t)e * p.N * pitch_b;
   if constexpr (kMode == kProduct)
     B.tile(we + (size_t)n0 * pitch_b, (long long)min(BN, p.N - n0) * pitch_b, pitch_b);
   else if constexpr (kMode == kRowsGrad)
-    B.tile(we + 2 * n0, (long long)L * pitch_b - 2 * n0, pitch_b);
+    B.tile(we + kSize * n0, (long long)L * pitch_b - kSize * n0, pitch_b);
   else
-    B.tile(p.q + (size_t)s0 * pitch_b + 2 * n0, (long long)L * pitch_b - 2 * n0, pitch_b);
-  const int Lb = (L + 63) / 64;
+    B.tile(p.q + (size_t)s0 * pitch_b + kSize * n0, (long long)L * pitch_b - kSize * n0, pitch_b);
+  const int Lb = (L + kStepL - 1) / kStepL;
   auto issue_a = [&](int kb, uint8_t* st) {
     A.template issue<CA, kRagged>(kb, st, wave, pitch_a, kb < Lb);
   };
@@ -396,15 +340,13 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void half_tile_kernel(F
   v4f acc[MI][NJ] = {};
   v8i bf[NJ];
   v8i af_next;
-  auto lo = [](const v8i& v) { return (v4i){v[0], v[1], v[2], v[3]}; };
-  auto hi = [](const v8i& v) { return (v4i){v[4], v[5], v[6], v[7]}; };
   auto subtile = [&](int i, int j, bool hi_first, const v8i& af) __attribute__((always_inline)) {
     if (hi_first) {
-      acc[i][j] = mfma16<kType>(hi(bf[j]), hi(af), acc[i][j]);
-      acc[i][j] = mfma16<kType>(lo(bf[j]), lo(af), acc[i][j]);
+      acc[i][j] = multiply_half<kType, 1>(bf[j], af, acc[i][j]);
+      acc[i][j] = multiply_half<kType, 0>(bf[j], af, acc[i][j]);
     } else {
-      acc[i][j] = mfma16<kType>(lo(bf[j]), lo(af), acc[i][j]);
-      acc[i][j] = mfma16<kType>(hi(bf[j]), hi(af), acc[i][j]);
+      acc[i][j] = multiply_half<kType, 0>(bf[j], af, acc[i][j]);
+      acc[i][j] = multiply_half<kType, 1>(bf[j], af, acc[i][j]);
     }
   };
   constexpr int kLateRow = MI >= 3 ? 1 : 0;
@@ -444,10 +386,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void half_tile_kernel(F
     af_next = A.load(tAn, 0);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, Operand<BN, kSlowB>::kReads, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kSize == 2 ? 2 : 8, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, decltype(B)::kReads, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x100, Operand<BM, kSlowA>::kReads, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, decltype(A)::kReads, 0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(acc[MI - 1][j]));
@@ -468,22 +410,43 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void half_tile_kernel(F
 #pragma unroll
   for (int j = 0; j < NJ; ++j) bf[j] = B.load(stB(Int<0>()), j);
   af_next = A.load(stA(Int<0>()), 0);
-  for (int kb = 0; kb < Lb; kb += 6)
+  // fp32: an instruction adds four products to a sum, so a long sum is a chain of
+  // l / 4 roundings; one of 48 is added to a total every six steps instead (over
+  // 7168 l's the error falls from 1.3e-6 to 3e-7 of the result).
+  v4f total[kSize == 4 ? MI : 1][kSize == 4 ? NJ : 1] = {};
+  for (int kb = 0; kb < Lb; kb += 6) {
     each<0, 6>([&](auto u) __attribute__((always_inline)) {
       constexpr int U = decltype(u)::value;
       if (U == 0 || kb + U < Lb) step(kb + U, u);
     });
+    if constexpr (kSize == 4)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          total[i][j] += acc[i][j];
+          acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+        }
+  }
   wait_vm<0>();   // (the loads past the last step)
+  if constexpr (kSize == 4)
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = total[i][j];
 
   // ---- epilogue: sums (i, j) of a lane are four columns 4 g .. 4 g + 3 of row
   // r16.  In 16 bits two subtiles' halves are exchanged between neighbouring
   // rows of 16 lanes, so that a lane holds eight columns, then lanes of rows
   // 0..7 exchange their second piece for the first piece of the row 8 further:
-  // a store writes eight rows' whole 128 bytes.
+  // a store writes eight rows' whole 128 bytes, past the caches.  In fp32 a row's
+  // 128 bytes take two stores, which the cache has to put together (past it, 32
+  // x 4096 x 7168 of few rows 1063 us against 719).
   const int g = lane >> 4, r16 = lane & 15;
-  const size_t out0 = kMode == kWeightsGrad ? (size_t)e * p.N : 0;
+  const size_t out0 =
+      kMode == kWeightsGrad ? ((size_t)blockIdx.y * p.E + (size_t)e) * (size_t)p.N : 0;
   const int top = row0 + wm * WM, left = n0 + wn * WN;
-  if (p.out_type == MOE_TYPE_F32) {
+  if (kType == MOE_TYPE_F32 || p.out_type == MOE_TYPE_F32) {
     float* out = reinterpret_cast<float*>(p.out);
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -491,8 +454,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void half_tile_kernel(F
       for (int j = 0; j < NJ; ++j) {
         const int row = top + 16 * i + r16, col = left + 16 * j + 4 * g;
         if (row < row_end && col < width)
-          __builtin_nontemporal_store(acc[i][j],
-                                      reinterpret_cast<v4f*>(out + (out0 + row) * width + col));
+          *reinterpret_cast<v4f*>(out + (out0 + row) * width + col) = acc[i][j];
       }
     return;
   }
@@ -539,6 +501,115 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void half_tile_kernel(F
   }
 }
 
+// Products of at most 16 rows of an expert in 16 bits, where tiles would be too
+// few to keep the memory busy: bound by the weights' one pass through HBM.  A
+// workgroup computes 16 NT channels; its eight waves share out K, so that
+// every CU has many waves' weight loads in flight (a wave's fragments go from
+// global memory straight to its registers: each weight is used by one wave),
+// and their sums are added in LDS in the order of the waves.
+constexpr int kSkinnyWaves = 8;
+constexpr int kSlab = 64;   // bytes of a row that one multiplication takes: 16 of four lanes
+
+template <int kType, int NT>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_float_kernel(FloatArgs p) {
+  constexpr int kAhead = 8;   // slabs loaded at once
+  __shared__ float sums[kSkinnyWaves][NT * 4][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int N = p.N, bytes = 2 * p.K;   // of a row
+  const int n_tiles = (N + 16 * NT - 1) / (16 * NT);
+  const int tile_m = blockIdx.x / n_tiles, n0 = (blockIdx.x - tile_m * n_tiles) * 16 * NT;
+  if (blockIdx.x == 0 && threadIdx.x < 64 && p.status &&
+      segments_bad(p.offsets, p.counts, p.E, lane) && lane == 0)
+    atomicOr(p.status, MOE_ERR_BAD_INDEX);
+  int e, row0, row_end;
+  find_mtile<16>(p.offsets, p.counts, p.E, p.rows, tile_m, lane, e, row0, row_end);
+  if (e < 0) return;
+  const int g = lane >> 4, r16 = lane & 15;
+  const uint8_t* wp[NT];
+  bool w_in[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int n = n0 + j * 16 + r16;
+    w_in[j] = n < N;
+    wp[j] = p.q + ((size_t)e * N + (w_in[j] ? n : 0)) * bytes + 16 * g;
+  }
+  const bool a_in = row0 + r16 < row_end;
+  const uint8_t* ap = p.p + (size_t)(a_in ? row0 + r16 : row0) * bytes + 16 * g;
+  auto load = [](const uint8_t* at, bool in) {
+    const v4i z = {0, 0, 0, 0};
+    return in ? *reinterpret_cast<const v4i*>(at) : z;
+  };
+  v4f acc[NT] = {};
+  // wave w takes slabs [first, last), pairs of them (one 128-byte line) together
+  const int lines = (bytes + 2 * kSlab - 1) / (2 * kSlab);
+  const int first = 2 * (int)((long long)lines * wave / kSkinnyWaves);
+  const int last = min(2 * (int)((long long)lines * (wave + 1) / kSkinnyWaves),
+                       (bytes + kSlab - 1) / kSlab);
+  for (int s0 = first; s0 < last; s0 += kAhead) {
+    v4i wf[kAhead][NT], af[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const bool in = s0 + u < last && (s0 + u) * kSlab + 16 * g < bytes;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) wf[u][j] = load(wp[j] + (s0 + u) * kSlab, in && w_in[j]);
+      af[u] = load(ap + (s0 + u) * kSlab, in && a_in);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if constexpr (kType == MOE_TYPE_BF16)
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wf[u][j]),
+                                                           __builtin_bit_cast(bf16x8, af[u]),
+                                                           acc[j], 0, 0, 0);
+        else
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, wf[u][j]),
+                                                          __builtin_bit_cast(f16x8, af[u]),
+                                                          acc[j], 0, 0, 0);
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sums[wave][4 * j + q][lane] = acc[j][q];
+  __syncthreads();
+  // channels 16 j + 4 (l / 16) + 0 .. 3 of row l % 16
+  for (int u = threadIdx.x; u < NT * 64; u += 64 * kSkinnyWaves) {
+    const int j = u >> 6, l = u & 63;
+    const int row = row0 + (l & 15), n = n0 + 16 * j + 4 * (l >> 4);
+    if (row >= row_end || n >= N) continue;
+    float v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = sums[0][4 * j + q][l];
+#pragma unroll
+      for (int w = 1; w < kSkinnyWaves; ++w) v[q] += sums[w][4 * j + q][l];
+    }
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)row * N + n) =
+        kType == MOE_TYPE_F16 ? make_uint2(pack2_f16(v[0], v[1]), pack2_f16(v[2], v[3]))
+                              : make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
+  }
+}
+
+// The weights' gradient from `n` fp32 parts of it, added in order.
+__global__ __launch_bounds__(256) void join_parts_kernel(const float* __restrict__ parts, int n,
+                                                         long long values, uint8_t* out,
+                                                         int out_type) {
+  for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4; i < values;
+       i += (long long)gridDim.x * 1024) {
+    v4f s = *reinterpret_cast<const v4f*>(parts + i);
+#pragma unroll 4
+    for (int k = 1; k < n; ++k) s += *reinterpret_cast<const v4f*>(parts + k * values + i);
+    if (out_type == MOE_TYPE_F32)
+      *reinterpret_cast<v4f*>(reinterpret_cast<float*>(out) + i) = s;
+    else
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + i) =
+          out_type == MOE_TYPE_F16 ? make_uint2(pack2_f16(s[0], s[1]), pack2_f16(s[2], s[3]))
+                                   : make_uint2(pack2_bf16(s[0], s[1]), pack2_bf16(s[2], s[3]));
+  }
+}
+
 // Rows that no expert has, set to zero: a wave to a row.
 __global__ __launch_bounds__(256) void zero_rest_kernel(const int32_t* offsets,
                                                         const int32_t* counts, int E, int rows,
@@ -566,43 +637,113 @@ static long long tiles_of(const FloatArgs& p, int bm, int bn) {
 }
 
 template <int kType, int kMode, int BM, int BN, int WM, int WN, int GM, int kDeep>
-static moe_status_t launch_half(const FloatArgs& p, hipStream_t st) {
+static moe_status_t launch_tiles(const FloatArgs& p, hipStream_t st) {
   constexpr int threads = 64 * (BM / WM) * (BN / WN);
   const long long blocks = tiles_of<kMode>(p, BM, BN);
   if (blocks * threads > 0xffffffffLL || blocks > 0x7fffffffLL) return MOE_UNSUPPORTED_SHAPE;
-  const dim3 grid((unsigned)blocks), block(threads);
+  const dim3 grid((unsigned)blocks, (unsigned)p.splits), block(threads);
   // (a weights' gradient ends where its operands' descriptors end)
-  const bool ragged = kMode != kWeightsGrad && (kMode == kProduct ? p.K : p.N) % 64 != 0;
+  const bool ragged = kMode != kWeightsGrad && (kMode == kProduct ? p.K : p.N) % (kType == MOE_TYPE_F32 ? 32 : 64) != 0;
   if constexpr (kMode != kWeightsGrad) {
     if (ragged) {
-      hipLaunchKernelGGL((half_tile_kernel<kType, kMode, BM, BN, WM, WN, GM, kDeep, true>), grid,
+      hipLaunchKernelGGL((float_tile_kernel<kType, kMode, BM, BN, WM, WN, GM, kDeep, true>), grid,
                          block, 0, st, p);
       return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
     }
   }
-  hipLaunchKernelGGL((half_tile_kernel<kType, kMode, BM, BN, WM, WN, GM, kDeep, false>), grid,
+  hipLaunchKernelGGL((float_tile_kernel<kType, kMode, BM, BN, WM, WN, GM, kDeep, false>), grid,
                      block, 0, st, p);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
 }
 
+template <int kType, int NT>
+static moe_status_t launch_skinny(const FloatArgs& p, hipStream_t st) {
+  const long long blocks =
+      ((long long)p.rows / 16 + p.E) * ((p.N + 16 * NT - 1) / (16 * NT));
+  if (blocks * 64 * kSkinnyWaves > 0xffffffffLL) return MOE_UNSUPPORTED_SHAPE;
+  hipLaunchKernelGGL((skinny_float_kernel<kType, NT>), dim3((unsigned)blocks),
+                     dim3(64 * kSkinnyWaves), 0, st, p);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
+}
+
+// Parts that the weights' gradient splits its segments into: where the experts'
+// 128 x 128 tiles are fewer than a round of the CUs (two workgroups to each),
+// and segments (of the buffer, on average) long enough for at least 512 rows
+// in a part.
+static int weight_splits(int E, int rows, int N, int K) {
+  const long long tiles = (long long)E * ((N + 127) / 128) * ((K + 127) / 128);
+  long long n = tiles < 256 ? 512 / tiles : 1;
+  const long long parts = rows / E / 512;
+  if (n > parts) n = parts;
+  return n < 1 ? 1 : n > 32 ? 32 : (int)n;
+}
+
+// Tiles are chosen from the sizes alone (the same inside graph capture).  `rows`
+// is a segment's on average: the buffer's, less the 127 that a contiguous one
+// has for the padding between segments (a capacity of 128 rows or more counts
+// as less than it may hold).  Times in us, weights from HBM, rows x experts x N
+// x K, bf16; p: product, r: rows' gradient, w: weights' gradient.
+//
+//   * Few rows: 64 x 128 tiles, several workgroups to a CU, once there are more
+//     of them than CUs (p 256 x 32 x 4096 x 7168 318, 64 x 64 tiles loaded five
+//     steps ahead 366, 128 x 128 354; r 357, 450, 375) or l is short; else 64 x
+//     64 (r 8 x 8 x 7168 x 2048 36, 64 x 128 68, 128 x 128 55); and where
+//     there are so few channels that those leave CUs idle, the product
+//     without tiles (p 1 x 1 x 4096 x 7168 14, 64 x 64 31; 1 x 1 x 7168 x 2048
+//     9.6 and 12; 8 x 8 x 4096 x 7168 66 and 80; but 4 x 4 36 and 32).
+//   * else 256 x 256 or 128 x 128, whichever takes less time by their rounds of
+//     the CUs: a step of 256 tiles of 256 x 256 takes 1.59 us at the rate of
+//     large products, one of 256 tiles of 128 x 128 0.605 (p 1024 x 8 x 4096 x
+//     7168 185 and 152, r 117 and 140; p 4096 x 32 571 and 483; 6144 x 6 x
+//     7168 x 2048 p 163 and 210, r 185 and 229; prefill shares 131040 x 9 x 4096
+//     x 7168 p 5700 and 9090).  128 x 128 with two workgroups to a CU, or, for
+//     the rows' gradient and where there are no two, loaded two steps ahead
+//     (r 4096 x 32 x 7168 x 2048 243 and 301; p 8192 x 32 402 and 372).
+//   * fp32: 64 x 128, or 64 x 64 where those are few (16384 x 8 x 1024 x 1024 p
+//     294, 64 x 64 591, 128 x 128 329, 256 x 256 485: its steps have half the
+//     l's and eight times the multiplications, so the loads hide in any tile and
+//     what counts is that the last round is full).
 template <int kType, int kMode>
-static moe_status_t launch_half(const FloatArgs& p, hipStream_t st) {
-  const long long rows = kMode == kWeightsGrad ? p.N : ((long long)p.rows + p.E - 1) / p.E;
-  if (tiles_of<kMode>(p, 64, 64) <= 512 || rows <= 64)
-    return launch_half<kType, kMode, 64, 64, 32, 64, 4, 6>(p, st);
-  if (tiles_of<kMode>(p, 256, 256) <= 128 || rows < 256)
-    return launch_half<kType, kMode, 128, 128, 64, 64, 4, 0>(p, st);
-  return launch_half<kType, kMode, 256, 256, 128, 64, 2, 0>(p, st);
+static moe_status_t launch_tiles(const FloatArgs& p, hipStream_t st) {
+  const int width = kMode == kProduct ? p.N : p.K;
+  if (kType == MOE_TYPE_F32) {
+    if (tiles_of<kMode>(p, 64, 64) <= 512 && p.splits == 1)
+      return launch_tiles<kType, kMode, 64, 64, 32, 64, 4, 6>(p, st);
+    return launch_tiles<kType, kMode, 64, 128, 32, 64, 4, 0>(p, st);
+  } else {
+    long long rows = ((long long)p.rows + p.E - 1) / p.E;
+    if (rows >= 128) rows -= 127;
+    if (kMode != kWeightsGrad && rows <= 48) {
+      const long long wide = (long long)p.E * ((width + 127) / 128);
+      const int L = kMode == kProduct ? p.K : p.N;
+      if (wide > 256 || (wide > 128 && L <= 1024))
+        return launch_tiles<kType, kMode, 64, 128, 32, 64, 4, 0>(p, st);
+      if constexpr (kMode == kProduct)
+        if (rows <= 16)
+          return (long long)p.E * p.N >= 448 * 16 ? launch_skinny<kType, 2>(p, st)
+                                                  : launch_skinny<kType, 1>(p, st);
+      return launch_tiles<kType, kMode, 64, 64, 32, 64, 4, 6>(p, st);
+    }
+    // (segments differ, and end anywhere in a tile: six tenths of one more each)
+    auto tiles = [&](int b) {
+      const long long m = kMode == kWeightsGrad ? (long long)p.E * ((p.N + b - 1) / b)
+                                                : p.E * (10 * rows + 6 * b) / (10 * b);
+      return m * ((width + b - 1) / b);
+    };
+    auto rounds = [](long long n) { return (n + 255) / 256; };
+    if (p.splits == 1 && rounds(tiles(256)) * 159 <= rounds(tiles(128)) * 60)
+      return launch_tiles<kType, kMode, 256, 256, 128, 64, 2, 0>(p, st);
+    if (kMode != kRowsGrad && tiles(128) > 256)
+      return launch_tiles<kType, kMode, 128, 128, 64, 64, 4, 0>(p, st);
+    return launch_tiles<kType, kMode, 128, 128, 64, 64, 4, 3>(p, st);
+  }
 }
 
 template <int kMode>
 static moe_status_t launch_float(const FloatArgs& p, int dtype, hipStream_t st) {
-  if (dtype == MOE_TYPE_BF16) return launch_half<MOE_TYPE_BF16, kMode>(p, st);
-  if (dtype == MOE_TYPE_F16) return launch_half<MOE_TYPE_F16, kMode>(p, st);
-  const long long tiles = tiles_of<kMode>(p, 64, 64);
-  if (tiles * 256 > 0xffffffffLL) return MOE_UNSUPPORTED_SHAPE;   // threads of a launch
-  hipLaunchKernelGGL((float_tile_kernel<kMode>), dim3((unsigned)tiles), dim3(256), 0, st, p);
-  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
+  if (dtype == MOE_TYPE_BF16) return launch_tiles<MOE_TYPE_BF16, kMode>(p, st);
+  if (dtype == MOE_TYPE_F16) return launch_tiles<MOE_TYPE_F16, kMode>(p, st);
+  return launch_tiles<MOE_TYPE_F32, kMode>(p, st);
 }
 
 constexpr int kMaxFloatDim = 1 << 20;     // N and K
@@ -645,7 +786,7 @@ extern "C" moe_status_t moe_grouped_gemm_float(const void* a, const void* w, int
                                                int E, int rows_total, int N, int K, void* c,
                                                int zero_rest, int32_t* status_dev, void* stream) {
   const FloatArgs p{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(w), offsets,
-                    counts, E, rows_total, N, K, static_cast<uint8_t*>(c), dtype, status_dev};
+                    counts, E, rows_total, N, K, static_cast<uint8_t*>(c), dtype, status_dev, 1};
   return float_rows<kProduct>(p, dtype, zero_rest, stream);
 }
 
@@ -656,27 +797,40 @@ extern "C" moe_status_t moe_grouped_gemm_float_grad_rows(const void* dc, const v
                                                          int zero_rest, int32_t* status_dev,
                                                          void* stream) {
   const FloatArgs p{static_cast<const uint8_t*>(dc), static_cast<const uint8_t*>(w), offsets,
-                    counts, E, rows_total, N, K, static_cast<uint8_t*>(da), dtype, status_dev};
+                    counts, E, rows_total, N, K, static_cast<uint8_t*>(da), dtype, status_dev, 1};
   return float_rows<kRowsGrad>(p, dtype, zero_rest, stream);
 }
 
 extern "C" size_t moe_grouped_gemm_float_workspace_bytes(int E, int rows_total, int N, int K) {
-  (void)E; (void)rows_total; (void)N; (void)K;
-  return 0;
+  if (E <= 0 || rows_total < 0 || N <= 0 || K <= 0) return 0;
+  const int n = weight_splits(E, rows_total, N, K);
+  return n > 1 ? (size_t)n * E * N * K * sizeof(float) : 0;
 }
 
 extern "C" moe_status_t moe_grouped_gemm_float_grad_weights(
     const void* dc, const void* a, int dtype, const int32_t* offsets, const int32_t* counts, int E,
     int rows_total, int N, int K, void* dw, int dw_type, void* workspace, size_t workspace_bytes,
     int32_t* status_dev, void* stream) {
-  const FloatArgs p{static_cast<const uint8_t*>(dc), static_cast<const uint8_t*>(a), offsets,
-                    counts, E, rows_total, N, K, static_cast<uint8_t*>(dw), dw_type, status_dev};
-  const moe_status_t ok = float_args(p, dtype);
+  FloatArgs p{static_cast<const uint8_t*>(dc), static_cast<const uint8_t*>(a), offsets, counts, E,
+              rows_total, N, K, static_cast<uint8_t*>(dw), dw_type, status_dev, 1};
+  moe_status_t ok = float_args(p, dtype);
   if (ok != MOE_OK) return ok;
   if (dw_type != dtype && dw_type != MOE_TYPE_F32) return MOE_INVALID_ARG;
   if (!dw || (rows_total > 0 && (!dc || !a))) return MOE_INVALID_ARG;
   const size_t need = moe_grouped_gemm_float_workspace_bytes(E, rows_total, N, K);
   if (need && (!workspace || workspace_bytes < need)) return MOE_INVALID_ARG;
   if ((uintptr_t)workspace & 15) return MOE_UNSUPPORTED_SHAPE;
-  return launch_float<kWeightsGrad>(p, dtype, reinterpret_cast<hipStream_t>(stream));
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  p.splits = weight_splits(E, rows_total, N, K);
+  if (p.splits == 1) return launch_float<kWeightsGrad>(p, dtype, st);
+  p.out = static_cast<uint8_t*>(workspace);
+  p.out_type = MOE_TYPE_F32;
+  ok = launch_float<kWeightsGrad>(p, dtype, st);
+  if (ok != MOE_OK) return ok;
+  const long long values = (long long)E * N * K;
+  const long long blocks = (values + 1023) / 1024;
+  hipLaunchKernelGGL(join_parts_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256),
+                     0, st, static_cast<const float*>(workspace), p.splits, values,
+                     static_cast<uint8_t*>(dw), dw_type);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
 }
