@@ -367,12 +367,14 @@ __global__ __launch_bounds__(64 * kRouteWaves, route_waves(kLanes, kN)) void rou
   }
   reach = lanes_max<kLanes>(reach);
   // an fp32 key's error where v = |key| + 2 reach bounds both the key and its
-  // score: 32 roundings of a sigmoid; a softmax's exponential and sum, and its
-  // argument's, which is -ln(score) at most.  Scores below e^-88 are 0, within
-  // 1e-37.  (Two keys with |sum| + 4 reach <= v together: the same.)
+  // score.  Sigmoid: 9 roundings (exponential 3, sum, reciprocal 2, bias), and
+  // of the exponent's low part, left out here, 0.22 per unit of the argument,
+  // which is -ln(score) at most where it counts.  Softmax: the exponential's and
+  // the sum's, and one per unit of the argument.  Scores below e^-88 are 0,
+  // within 1e-37.  (Two keys with |sum| + 4 reach <= v together: the same.)
   auto error = [&](float v) {
-    const float roundings =
-        softmax ? 25.f + kN + larger(0.f, -0.7f * __builtin_amdgcn_logf(v)) : 32.f;
+    const float units = larger(0.f, -0.7f * __builtin_amdgcn_logf(v));
+    const float roundings = softmax ? 25.f + kN + units : fmaf(0.22f, units, 9.f);
     return fmaf(v, roundings * kU, 1e-37f);
   };
   uint32_t absent = 0;
