@@ -103,6 +103,29 @@ __device__ __forceinline__ void load_param(const uint8_t* p, int at, int n, floa
   }
 }
 
+// Rows: shorter than a chunk; of any longer length, read and written through
+// unaligned 16-byte accesses; of whole aligned chunks.
+enum { kShortRows = 0, kLooseRows = 1, kWholeRows = 2 };
+
+template <int kKind, bool kStream = false>
+__device__ __forceinline__ uint4 load_row(const uint8_t* p, int row_bytes) {
+  if constexpr (kKind == kLooseRows) {
+    uint4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+  } else {
+    return load_chunk<kKind == kWholeRows, kStream>(p, row_bytes);
+  }
+}
+
+template <int kKind>
+__device__ __forceinline__ void store_row(uint8_t* p, int row_bytes, const uint4& v) {
+  if constexpr (kKind == kLooseRows)
+    __builtin_memcpy(p, &v, 16);
+  else
+    store_chunk<kKind == kWholeRows>(p, row_bytes, v);
+}
+
 // The elements of chunk c that count: [lo, hi) of its El::kN (a last chunk
 // overlaps the one before it, a row shorter than a chunk ends inside it).
 template <typename El>
@@ -112,14 +135,14 @@ __device__ __forceinline__ void chunk_range(const RowShape& row, int c, int& lo,
 }
 
 // The weight (or bias, missing: `none`) of a lane's chunk c.
-template <typename El, typename W, bool kWhole>
+template <typename El, typename W, int kKind>
 __device__ __forceinline__ void chunk_param(const uint8_t* p, const NormArgs& a, int c, float none,
                                             float (&v)[El::kN]) {
 #pragma unroll
   for (int i = 0; i < El::kN; ++i) v[i] = none;
   if (!p || c >= a.row.chunks) return;
   const int at = a.row.start(c) / El::kSize;
-  load_param<W, El::kN>(p, at, kWhole ? El::kN : min(El::kN, a.H - at), v);
+  load_param<W, El::kN>(p, at, kKind != kShortRows ? El::kN : min(El::kN, a.H - at), v);
 }
 
 // kWaves waves to a row, which its lanes hold in kCh chunks each.  A workgroup
@@ -134,7 +157,7 @@ constexpr int norm_groups(int waves, int ch) {
   return 256 * 4 * norm_waves(waves, ch) * 64 / norm_threads(waves);
 }
 
-template <typename El, typename W, int kWaves, int kCh, bool kWhole, bool kStream>
+template <typename El, typename W, int kWaves, int kCh, int kKind, bool kStream>
 __global__ __launch_bounds__(norm_threads(kWaves), norm_waves(kWaves, kCh)) void
 norm_kernel(NormArgs p) {
   constexpr int N = El::kN, kStep = 64 * kWaves;
@@ -151,7 +174,7 @@ norm_kernel(NormArgs p) {
 #pragma unroll
     for (int u = 0; u < kCh; ++u) {
       const int c = at + u * kStep;
-      raw[u] = load_chunk<kWhole, kStream>(src + p.row.start(c < p.row.chunks ? c : 0), p.row.bytes);
+      raw[u] = load_row<kKind, kStream>(src + p.row.start(c < p.row.chunks ? c : 0), p.row.bytes);
     }
   };
   load(t);
@@ -160,11 +183,11 @@ norm_kernel(NormArgs p) {
 #pragma unroll
   for (int u = 0; u < kCh; ++u) {
     const int c = at + u * kStep;
-    chunk_param<El, W, kWhole>(p.w, p, c, 1.f, w[u]);
-    chunk_param<El, W, kWhole>(p.b, p, c, 0.f, b[u]);
+    chunk_param<El, W, kKind>(p.w, p, c, 1.f, w[u]);
+    chunk_param<El, W, kKind>(p.b, p, c, 0.f, b[u]);
     lo[u] = 0;
     hi[u] = N;
-    if (!kWhole) chunk_range<El>(p.row, c, lo[u], hi[u]);
+    if (kKind != kWholeRows) chunk_range<El>(p.row, c, lo[u], hi[u]);
     if (c >= p.row.chunks) hi[u] = 0;
   }
   for (; t < p.T; t += step) {
@@ -172,13 +195,18 @@ norm_kernel(NormArgs p) {
 #pragma unroll
     for (int u = 0; u < kCh; ++u) El::unpack(raw[u], v[u]);
     load(t + step < p.T ? t + step : t);
+    // (all of a chunk, but for the lane with the row's end)
     float s[1] = {0.f};
 #pragma unroll
     for (int u = 0; u < kCh; ++u)
-      if (!kWhole || hi[u])
+      if (hi[u] - lo[u] == N) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[0] += v[u][i];
+      } else if (kKind != kWholeRows && hi[u]) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (kWhole || (i >= lo[u] && i < hi[u])) s[0] += v[u][i];
+          if (i >= lo[u] && i < hi[u]) s[0] += v[u][i];
+      }
     row_add<kWaves>(s, red[0]);
     // (divided: the mean of equal values is that value, and no product with a
     // rounded 1 / H that the subtraction below could be contracted with)
@@ -188,10 +216,14 @@ norm_kernel(NormArgs p) {
     for (int u = 0; u < kCh; ++u) {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[u][i] -= mu;
-      if (!kWhole || hi[u])
+      if (hi[u] - lo[u] == N) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[0] = fmaf(v[u][i], v[u][i], s[0]);
+      } else if (kKind != kWholeRows && hi[u]) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (kWhole || (i >= lo[u] && i < hi[u])) s[0] = fmaf(v[u][i], v[u][i], s[0]);
+          if (i >= lo[u] && i < hi[u]) s[0] = fmaf(v[u][i], v[u][i], s[0]);
+      }
     }
     row_add<kWaves>(s, red[1]);
     const float r = 1.f / sqrtf(fmaf(s[0], over, p.eps));
@@ -201,8 +233,8 @@ norm_kernel(NormArgs p) {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[u][i] = fmaf(v[u][i] * r, w[u][i], b[u][i]);
       if (c < p.row.chunks)
-        store_chunk<kWhole>(p.y + t * p.row.bytes + p.row.start(c), p.row.bytes,
-                            pack_row<El>(v[u]));
+        store_row<kKind>(p.y + t * p.row.bytes + p.row.start(c), p.row.bytes,
+                         pack_row<El>(v[u]));
     }
     if (at == 0) {
       if (p.mean) p.mean[t] = mu;
@@ -239,8 +271,8 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs p) {
     for (int c = threadIdx.x; c < p.row.chunks; c += 256) {
       float e[N], w[N], b[N];
       El::unpack(load_chunk<false>(src + p.row.start(c), p.row.bytes), e);
-      chunk_param<El, W, false>(p.w, p, c, 1.f, w);
-      chunk_param<El, W, false>(p.b, p, c, 0.f, b);
+      chunk_param<El, W, kShortRows>(p.w, p, c, 1.f, w);
+      chunk_param<El, W, kShortRows>(p.b, p, c, 0.f, b);
 #pragma unroll
       for (int i = 0; i < N; ++i) e[i] = fmaf((e[i] - mu) * r, w[i], b[i]);
       store_chunk<false>(p.y + t * p.row.bytes + p.row.start(c), p.row.bytes, pack_row<El>(e));
@@ -257,7 +289,7 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs p) {
 // rows of their columns.  The next row is on its way while this one is summed.
 // (Rows of 64 chunks: 512 workgroups of one wave, one row at a time, left most
 // of the memory idle: 65536 rows of 512 bf16 66 us.)
-template <typename El, typename W, int kRows, int kWaves, int kCh, bool kWhole, bool kStream>
+template <typename El, typename W, int kRows, int kWaves, int kCh, int kKind, bool kStream>
 __global__ __launch_bounds__(64 * kWaves * kRows) void norm_grad_kernel(NormArgs p) {
   constexpr int N = El::kN, kStep = 64 * kWaves;
   __shared__ float red[2][kRows * kWaves][2];
@@ -273,8 +305,8 @@ __global__ __launch_bounds__(64 * kWaves * kRows) void norm_grad_kernel(NormArgs
     for (int u = 0; u < kCh; ++u) {
       const int c = at + u * kStep;
       const long long off = t * p.row.bytes + p.row.start(c < p.row.chunks ? c : 0);
-      raw_x[u] = load_chunk<kWhole, kStream>(p.x + off, p.row.bytes);
-      raw_g[u] = load_chunk<kWhole, kStream>(p.dy + off, p.row.bytes);
+      raw_x[u] = load_row<kKind, kStream>(p.x + off, p.row.bytes);
+      raw_g[u] = load_row<kKind, kStream>(p.dy + off, p.row.bytes);
     }
     mu = p.mean[t];
     r = p.rstd[t];
@@ -287,12 +319,12 @@ __global__ __launch_bounds__(64 * kWaves * kRows) void norm_grad_kernel(NormArgs
 #pragma unroll
   for (int u = 0; u < kCh; ++u) {
     const int c = at + u * kStep;
-    chunk_param<El, W, kWhole>(p.w, p, c, 1.f, w[u]);
+    chunk_param<El, W, kKind>(p.w, p, c, 1.f, w[u]);
 #pragma unroll
     for (int i = 0; i < N; ++i) dw[u][i] = db[u][i] = 0.f;
     lo[u] = 0;
     hi[u] = N;
-    if (!kWhole) chunk_range<El>(p.row, c, lo[u], hi[u]);
+    if (kKind != kWholeRows) chunk_range<El>(p.row, c, lo[u], hi[u]);
     if (c >= p.row.chunks) hi[u] = 0;
   }
   int parity = 0;
@@ -308,18 +340,23 @@ __global__ __launch_bounds__(64 * kWaves * kRows) void norm_grad_kernel(NormArgs
     load(t + step);
     float s[2] = {0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < kCh; ++u)
+    for (int u = 0; u < kCh; ++u) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[u][i] = (z[u][i] - mut) * rt;
+      // (what does not count, in few waves: zeros)
+      if (!live || hi[u] - lo[u] != N)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (!live || i < lo[u] || i >= hi[u]) g[u][i] = z[u][i] = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const bool in = live && (kWhole ? hi[u] != 0 : i >= lo[u] && i < hi[u]);
-        z[u][i] = (z[u][i] - mut) * rt;
-        if (!in) g[u][i] = z[u][i] = 0.f;
         dw[u][i] = fmaf(g[u][i], z[u][i], dw[u][i]);
         db[u][i] += g[u][i];
         g[u][i] *= w[u][i];
         s[0] += g[u][i];
         s[1] = fmaf(g[u][i], z[u][i], s[1]);
       }
+    }
     if (!p.y) continue;
     row_add<kWaves>(s, red[parity] + part * kWaves);
     parity ^= 1;
@@ -332,8 +369,8 @@ __global__ __launch_bounds__(64 * kWaves * kRows) void norm_grad_kernel(NormArgs
       for (int i = 0; i < N; ++i) d[i] = rt * (g[u][i] - c1 - z[u][i] * c2);
       if (c >= p.row.chunks || !live) continue;
       uint8_t* out = p.y + t * p.row.bytes + p.row.start(c);
-      if (kWhole || lo[u] == 0) {
-        store_chunk<kWhole>(out, p.row.bytes, pack_row<El>(d));
+      if (kKind == kWholeRows || lo[u] == 0) {
+        store_row<kKind>(out, p.row.bytes, pack_row<El>(d));
       } else {
         // (the elements that the chunk before holds too were left out here)
         const uint4 v = pack_row<El>(d);
@@ -372,7 +409,7 @@ __global__ __launch_bounds__(64 * kWaves * kRows) void norm_grad_kernel(NormArgs
     const int c = at + u * kStep;
     if (c >= p.row.chunks) continue;
     const int first = p.row.start(c) / El::kSize;
-    if (kWhole) {
+    if (kKind == kWholeRows) {
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
         *reinterpret_cast<float4*>(out + first + i) =
@@ -554,47 +591,49 @@ static bool norm_streams(const NormArgs& p) {
   return (long long)p.T * p.row.bytes * (p.dy ? 2 : 1) > (400LL << 20);
 }
 
-template <typename El, typename W, int kWaves, int kCh, bool kWhole>
+template <typename El, typename W, int kWaves, int kCh, int kKind>
 static void launch_norm_as(const NormArgs& p, hipStream_t st) {
   constexpr long long most = norm_groups(kWaves, kCh);
   constexpr int kPer = kWaves == 1 ? 4 : 1;
   const long long blocks = ((long long)p.T + kPer - 1) / kPer;
   const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(norm_threads(kWaves));
   if (norm_streams(p))
-    hipLaunchKernelGGL((norm_kernel<El, W, kWaves, kCh, kWhole, true>), grid, block, 0, st, p);
+    hipLaunchKernelGGL((norm_kernel<El, W, kWaves, kCh, kKind, true>), grid, block, 0, st, p);
   else
-    hipLaunchKernelGGL((norm_kernel<El, W, kWaves, kCh, kWhole, false>), grid, block, 0, st, p);
+    hipLaunchKernelGGL((norm_kernel<El, W, kWaves, kCh, kKind, false>), grid, block, 0, st, p);
 }
 
-template <typename El, typename W, bool kWhole>
+template <typename El, typename W, int kKind>
 static void launch_norm(const NormArgs& p, hipStream_t st) {
   const int c = p.row.chunks;
   if (p.row.bytes > kNormLong)
     hipLaunchKernelGGL((norm_long_kernel<El, W>), dim3(walk(p.T)), dim3(256), 0, st, p);
-  else if (c <= 64)
-    launch_norm_as<El, W, 1, 1, kWhole>(p, st);
+  else if (kKind == kShortRows || c <= 64)   // (a short row is one chunk)
+    launch_norm_as<El, W, 1, 1, kKind>(p, st);
+  else if constexpr (kKind == kShortRows)
+    return;
   else if (c <= 128)
-    launch_norm_as<El, W, 2, 1, kWhole>(p, st);
+    launch_norm_as<El, W, 2, 1, kKind>(p, st);
   else if (c <= 256)
-    launch_norm_as<El, W, 4, 1, kWhole>(p, st);
+    launch_norm_as<El, W, 4, 1, kKind>(p, st);
   else if (c <= 512)
-    launch_norm_as<El, W, 8, 1, kWhole>(p, st);
+    launch_norm_as<El, W, 8, 1, kKind>(p, st);
   else if (c <= 1024 && p.T <= 512)   // (a row as fast as it goes: 16 waves to it)
-    launch_norm_as<El, W, 16, 1, kWhole>(p, st);
+    launch_norm_as<El, W, 16, 1, kKind>(p, st);
   else if (c <= 1024)
-    launch_norm_as<El, W, 8, 2, kWhole>(p, st);
+    launch_norm_as<El, W, 8, 2, kKind>(p, st);
   else
-    launch_norm_as<El, W, 16, 2, kWhole>(p, st);
+    launch_norm_as<El, W, 16, 2, kKind>(p, st);
 }
 
-template <typename El, typename W, int kRows, int kWaves, int kCh, bool kWhole>
+template <typename El, typename W, int kRows, int kWaves, int kCh, int kKind>
 static void launch_norm_grad_as(const NormArgs& p, int parts, hipStream_t st) {
   const dim3 grid((unsigned)parts), block(64 * kWaves * kRows);
   if (norm_streams(p))
-    hipLaunchKernelGGL((norm_grad_kernel<El, W, kRows, kWaves, kCh, kWhole, true>), grid, block, 0,
+    hipLaunchKernelGGL((norm_grad_kernel<El, W, kRows, kWaves, kCh, kKind, true>), grid, block, 0,
                        st, p);
   else
-    hipLaunchKernelGGL((norm_grad_kernel<El, W, kRows, kWaves, kCh, kWhole, false>), grid, block,
+    hipLaunchKernelGGL((norm_grad_kernel<El, W, kRows, kWaves, kCh, kKind, false>), grid, block,
                        0, st, p);
 }
 
@@ -606,21 +645,23 @@ static int norm_parts(const NormArgs& p) {
   return (int)(least < most ? least : most);
 }
 
-template <typename El, typename W, bool kWhole>
+template <typename El, typename W, int kKind>
 static void launch_norm_grad(const NormArgs& p, int parts, hipStream_t st) {
   const int c = p.row.chunks;
-  if (c <= 64)
-    launch_norm_grad_as<El, W, 8, 1, 1, kWhole>(p, parts, st);
+  if (kKind == kShortRows || c <= 64)
+    launch_norm_grad_as<El, W, 8, 1, 1, kKind>(p, parts, st);
+  else if constexpr (kKind == kShortRows)
+    return;
   else if (c <= 128)
-    launch_norm_grad_as<El, W, 4, 2, 1, kWhole>(p, parts, st);
+    launch_norm_grad_as<El, W, 4, 2, 1, kKind>(p, parts, st);
   else if (c <= 256)
-    launch_norm_grad_as<El, W, 2, 4, 1, kWhole>(p, parts, st);
+    launch_norm_grad_as<El, W, 2, 4, 1, kKind>(p, parts, st);
   else if (c <= 512)
-    launch_norm_grad_as<El, W, 1, 8, 1, kWhole>(p, parts, st);
+    launch_norm_grad_as<El, W, 1, 8, 1, kKind>(p, parts, st);
   else if (c <= 1024)
-    launch_norm_grad_as<El, W, 1, 16, 1, kWhole>(p, parts, st);
+    launch_norm_grad_as<El, W, 1, 16, 1, kKind>(p, parts, st);
   else
-    launch_norm_grad_as<El, W, 1, 16, 2, kWhole>(p, parts, st);
+    launch_norm_grad_as<El, W, 1, 16, 2, kKind>(p, parts, st);
 }
 
 }  // namespace moe
@@ -651,10 +692,12 @@ extern "C" moe_status_t moe_layer_norm(const void* x, int dtype, int T, int H, c
   p.rstd = rstd;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   by_type(dtype, w_dtype, [&](auto el, auto w) {
-    if (whole_rows(p))
-      launch_norm<decltype(el), decltype(w), true>(p, st);
+    if (p.row.bytes < 16)
+      launch_norm<decltype(el), decltype(w), kShortRows>(p, st);
+    else if (whole_rows(p))
+      launch_norm<decltype(el), decltype(w), kWholeRows>(p, st);
     else
-      launch_norm<decltype(el), decltype(w), false>(p, st);
+      launch_norm<decltype(el), decltype(w), kLooseRows>(p, st);
   });
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
 }
@@ -714,10 +757,12 @@ extern "C" moe_status_t moe_layer_norm_grad(const void* dy, const void* x, int d
     });
   } else if (T > 0) {
     by_type(dtype, w_dtype, [&](auto el, auto w) {
-      if (whole_rows(p))
-        launch_norm_grad<decltype(el), decltype(w), true>(p, parts, st);
+      if (p.row.bytes < 16)
+        launch_norm_grad<decltype(el), decltype(w), kShortRows>(p, parts, st);
+      else if (whole_rows(p))
+        launch_norm_grad<decltype(el), decltype(w), kWholeRows>(p, parts, st);
       else
-        launch_norm_grad<decltype(el), decltype(w), false>(p, parts, st);
+        launch_norm_grad<decltype(el), decltype(w), kLooseRows>(p, parts, st);
     });
   }
   if (params) {
