@@ -14,7 +14,8 @@
 // waves) the waves in order.  Nothing is added with atomics: the gradients of
 // w and b are kept by column in each workgroup's registers over all the rows
 // that it walks, written once as partial sums, and joined by a second kernel
-// in the order of the workgroups.  Bound by HBM bandwidth.
+// in the order of the workgroups.  Bound by HBM bandwidth: 65536 rows of 7168
+// bf16 338 us (5.6 TB/s), the gradient of 32768 242 (5.8 TB/s).
 #include "row_chunks.hpp"
 
 namespace moe {
@@ -104,7 +105,9 @@ __device__ __forceinline__ void load_param(const uint8_t* p, int at, int n, floa
 }
 
 // Rows: shorter than a chunk; of any longer length, read and written through
-// unaligned 16-byte accesses; of whole aligned chunks.
+// unaligned 16-byte accesses; of whole aligned chunks.  (65536 rows of 2050 bf16
+// 124 us, the gradient 194; with a mask for every element and narrow accesses
+// 149 and 256; rows of 2048 88 and 139.)
 enum { kShortRows = 0, kLooseRows = 1, kWholeRows = 2 };
 
 template <int kKind, bool kStream = false>
@@ -618,7 +621,10 @@ static void launch_norm(const NormArgs& p, hipStream_t st) {
     launch_norm_as<El, W, 4, 1, kKind>(p, st);
   else if (c <= 512)
     launch_norm_as<El, W, 8, 1, kKind>(p, st);
-  else if (c <= 1024 && p.T <= 512)   // (a row as fast as it goes: 16 waves to it)
+  // (few rows: one as fast as it goes; us for rows of 7168 bf16, 16 waves to a
+  // row and 8: 1 row 3.0 and 3.6, 512 5.1 and 5.5, 2048 11.1 and 10.6, 8192 40.6
+  // and 38.2)
+  else if (c <= 1024 && p.T <= 512)
     launch_norm_as<El, W, 16, 1, kKind>(p, st);
   else if (c <= 1024)
     launch_norm_as<El, W, 8, 2, kKind>(p, st);

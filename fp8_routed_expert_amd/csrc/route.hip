@@ -128,7 +128,8 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, long long t, dou
   double all = 0.;
   if (p.softmax) {
 #pragma unroll 1
-    for (int e = lane; e < p.E; e += 64) top = fmaxf(top, clean(load_one<El>(p.logits, row + e), nan));
+    for (int e = lane; e < p.E; e += 64)
+      top = fmaxf(top, clean(load_one<El>(p.logits, row + e), nan));
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
     top = fmaxf(top, -3.402823466e38f);   // (a row of -infinity)
@@ -330,12 +331,12 @@ struct __attribute__((aligned(16))) Candidate {
 
 // Waves of a SIMD that the registers are shared out to.  (16 experts to each of
 // 16 lanes: three 41 us for 65536 tokens of 256 experts in groups, four, with
-// spills, 45; eight experts to each of 64 lanes 89 and 81.)
+// spills, 45.  Later steps brought the first to 33.)
 constexpr int route_waves(int lanes, int n) { return lanes == 16 && n == 16 ? 3 : 4; }
 
 template <typename El, int kLanes, int kN, bool kWide>
-__global__ __launch_bounds__(64 * kRouteWaves, route_waves(kLanes, kN)) void route_kernel(RouteArgs p, int lanes_per_group,
-                                                                 int per_lane) {
+__global__ __launch_bounds__(64 * kRouteWaves, route_waves(kLanes, kN)) void
+route_kernel(RouteArgs p, int lanes_per_group, int per_lane) {
   constexpr int kTokens = 64 / kLanes;          // of a wave
   constexpr int kCap = kLanes == 16 ? 32 : 64;  // candidates of a token
   constexpr int kMine = kCap / kLanes;          // of them to a lane
@@ -357,7 +358,8 @@ __global__ __launch_bounds__(64 * kRouteWaves, route_waves(kLanes, kN)) void rou
   for (int i = 0; i < kN; ++i) bias[i] = 0.f;
   if (p.bias) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) bias[i] = p.bias[kWide ? (mine ? first : 0) + i : i < mine ? first + i : 0];
+    for (int i = 0; i < kN; ++i)
+      bias[i] = p.bias[kWide ? (mine ? first : 0) + i : i < mine ? first + i : 0];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       bias_nan |= i < mine && bias[i] != bias[i];
@@ -518,7 +520,8 @@ __global__ __launch_bounds__(64 * kRouteWaves, route_waves(kLanes, kN)) void rou
       }
     }
     bound -= 2.f * error(fabsf(bound) + 2.f * reach);
-    bound = larger(bound == bound ? bound : -INFINITY, -3.402823466e38f);   // (never -infinity: masked keys are no candidates)
+    // (never -infinity: masked keys are no candidates)
+    bound = larger(bound == bound ? bound : -INFINITY, -3.402823466e38f);
     // ---- candidates, in the order of the lanes
     uint32_t in = 0;
 #pragma unroll
@@ -834,6 +837,13 @@ static void launch_exact(const RouteArgs& p, hipStream_t st) {
                      dim3(64 * kRouteWaves), lds, st, p);
 }
 
+// 16 lanes to a token where they hold its experts, 16 at most each, else 64,
+// else the exact form.  Four tokens to a wave share its instructions, which
+// bound many tokens (us, 16 and 64 lanes: 65536 x 256 in 8 groups 33 and 86,
+// without groups 26 and 60, 65536 x 64 16 and 57; 4096 x 256 in groups 15 and
+// 16).  For few tokens a lane's longer list shows (1 x 256 in groups 5.8 and
+// 5.4, 1024 x 256 6.6 and 5.7; 1 x 64 4.0 and 4.6); the rule leaves T out, so
+// that a token's scores and weights have the same bits in every batch.
 template <typename El>
 static void launch_route(const RouteArgs& p, hipStream_t st) {
   const int size = p.E / p.groups;
@@ -866,7 +876,8 @@ static void launch_route_grad(const RouteArgs& p, hipStream_t st) {
   constexpr int kTokens = 64 / kLanes;
   const dim3 grid = route_grid(((long long)p.T + kTokens - 1) / kTokens, 1 << 22);
   const dim3 block(64 * kRouteWaves);
-  const bool wide = (p.E + kLanes - 1) / kLanes == kN && p.E % kN == 0 && (size_t)p.E * El::kSize % 16 == 0 &&
+  const bool wide = (p.E + kLanes - 1) / kLanes == kN && p.E % kN == 0 &&
+                    (size_t)p.E * El::kSize % 16 == 0 &&
                     (((uintptr_t)p.logits | (uintptr_t)p.dlogits) & 15) == 0;
   if constexpr (kN * El::kSize % 16 == 0) {
     if (wide) {
