@@ -115,7 +115,8 @@ static moe_status_t gated_act(const ActArgs& p, int dtype, hipStream_t st) {
   if ((dtype != MOE_TYPE_F32 && dtype != MOE_TYPE_BF16 && dtype != MOE_TYPE_F16) || p.E <= 0 ||
       p.E > MOE_MAX_EXPERTS || p.rows < 0 || p.I <= 0)
     return MOE_INVALID_ARG;
-  if (p.I % 8 != 0 || p.I > (1 << 28)) return MOE_UNSUPPORTED_SHAPE;
+  // (a wave's last row may lie 64 behind the last one)
+  if (p.I % 8 != 0 || p.I > (1 << 28) || p.rows > 0x7fff0000) return MOE_UNSUPPORTED_SHAPE;
   if (!p.offsets || !p.counts) return MOE_INVALID_ARG;
   if (p.rows == 0) return MOE_OK;
   if (!p.h || !p.out || (kGrad && !p.dq)) return MOE_INVALID_ARG;

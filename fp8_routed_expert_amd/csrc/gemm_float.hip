@@ -753,12 +753,14 @@ static moe_status_t launch_float(const FloatArgs& p, int dtype, hipStream_t st) 
 }
 
 constexpr int kMaxFloatDim = 1 << 20;     // N and K
+constexpr int kMaxFloatRows = 0x7fff0000; // rounded up to tiles, 32 bits still hold them
 
 static moe_status_t float_args(const FloatArgs& p, int dtype) {
   if (!float_type(dtype) || p.E <= 0 || p.E > MOE_MAX_EXPERTS || p.rows < 0 || p.N <= 0 ||
       p.K <= 0)
     return MOE_INVALID_ARG;
-  if (p.N % 8 != 0 || p.K % 8 != 0 || p.N > kMaxFloatDim || p.K > kMaxFloatDim)
+  if (p.N % 8 != 0 || p.K % 8 != 0 || p.N > kMaxFloatDim || p.K > kMaxFloatDim ||
+      p.rows > kMaxFloatRows)
     return MOE_UNSUPPORTED_SHAPE;
   if (!p.offsets || !p.counts) return MOE_INVALID_ARG;
   if (((uintptr_t)p.p | (uintptr_t)p.q | (uintptr_t)p.out) & 15) return MOE_UNSUPPORTED_SHAPE;

@@ -684,8 +684,8 @@ moe_status_t moe_layer_norm_grad(const void* dy, const void* x, int dtype, int T
  *            (may be 0), 16-byte aligned; what the call leaves there is
  *            unspecified.  Calls (or captured graphs) that may run at the same
  *            time need one each.
- * N, K and I must be multiples of 8, N and K at most 2^20, I at most 2^28;
- * matrices 16-byte aligned; a launch holds 2^32 threads: MOE_UNSUPPORTED_SHAPE
+ * N, K and I must be multiples of 8, N and K at most 2^20, I at most 2^28,
+ * rows_total at most 0x7fff0000; matrices 16-byte aligned; a launch holds 2^32 threads: MOE_UNSUPPORTED_SHAPE
  * otherwise.  offsets / counts / status_dev as for moe_grouped_gemm_fp8.
  * Outputs may not overlap inputs.
  */

@@ -129,3 +129,14 @@ def test_binding_refusals():
         fre.gated_act(l, t)
     with pytest.raises(ValueError, match="the table has 2"):
         fre.grouped_linear(torch.zeros(8, 16), torch.zeros(3, 16, 16), t)
+
+
+def test_rows_past_31_bits():
+    """A buffer whose rows, rounded up to a tile, leave 31 bits is refused."""
+    rows = 0x7fff0001
+    for name in ("moe_grouped_gemm_float", "moe_grouped_gemm_float_grad_rows"):
+        assert caller(name, dict(a=P, w=P, dtype=1, off=P, cnt=P, E=4, rows=rows, N=8, K=8, c=P, zero=0, status=P))() == 2
+    assert caller("moe_grouped_gemm_float_grad_weights", dict(
+        dc=P, a=P, dtype=1, off=P, cnt=P, E=4, rows=rows, N=8, K=8, dw=P, wt=0, ws=P, wsb=1 << 40, status=P))() == 2
+    for name, ok in (("moe_gated_act", dict(h=P)), ("moe_gated_act_grad", dict(dq=P, h=P))):
+        assert caller(name, dict(**ok, dtype=1, off=P, cnt=P, E=4, rows=rows, I=8, out=P, zero=0, status=P))() == 2
