@@ -202,6 +202,9 @@ class RoutedExperts(torch.nn.Module):
         self.scores = self.table = self.route_status = None
 
     def forward(self, x):
+        # what the last call left holds its graph, whose accumulations belong
+        # to that call's stream and would end a capture of this one
+        self.scores = self.table = self.route_status = None
         xn = layer_norm(x, self.norm_weight, self.norm_bias, self.eps)
         logits = torch.nn.functional.linear(xn.float(), self.router)
         self.route_status = torch.zeros(1, dtype=torch.int32, device=x.device)

@@ -685,9 +685,9 @@ moe_status_t moe_layer_norm_grad(const void* dy, const void* x, int dtype, int T
  *            unspecified.  Calls (or captured graphs) that may run at the same
  *            time need one each.
  * N, K and I must be multiples of 8, N and K at most 2^20, I at most 2^28,
- * rows_total at most 0x7fff0000; matrices 16-byte aligned; a launch holds 2^32 threads: MOE_UNSUPPORTED_SHAPE
- * otherwise.  offsets / counts / status_dev as for moe_grouped_gemm_fp8.
- * Outputs may not overlap inputs.
+ * rows_total at most 0x7fff0000; matrices 16-byte aligned; a launch holds
+ * 2^32 threads: MOE_UNSUPPORTED_SHAPE otherwise.  offsets / counts /
+ * status_dev as for moe_grouped_gemm_fp8.  Outputs may not overlap inputs.
  */
 moe_status_t moe_grouped_gemm_float(const void* a, const void* w, int dtype,
                                     const int32_t* offsets, const int32_t* counts, int E,

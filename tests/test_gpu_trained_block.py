@@ -187,3 +187,32 @@ def test_two_streams(gpu):
         torch.cuda.synchronize()
         for a, b in zip(alone, got):
             assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_captured_module(gpu):
+    """A module's training step captured after an eager one of the same
+    parameters, replayed with eager passes of a copy between the replays."""
+    torch.manual_seed(4)
+    kw = dict(E=6, H=128, I=64, K=2)
+    m, other = fre.RoutedExperts(**kw), fre.RoutedExperts(**kw)
+    other.load_state_dict(m.state_dict())
+    x = torch.randn(70, 128, device="cuda", dtype=torch.bfloat16)
+
+    def step(m):
+        out = m(x)
+        (out.float().square().mean() + m.scores.square().mean()).backward()
+        return out.detach()
+    step(m)
+    m.zero_grad(set_to_none=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(m)
+    for i in range(3):
+        with torch.no_grad():
+            x.copy_(torch.randn(70, 128, device="cuda") * (i + 1))
+        for v in m.parameters():
+            v.grad.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        other.zero_grad(set_to_none=True)
+        assert torch.equal(got, step(other)), i

@@ -3,12 +3,13 @@ bits and the gated activation: their refusals, in the library (no launch: the
 pointers are never followed) and in the binding."""
 
 import ctypes
+import weakref
 
 import pytest
 import torch
 
 import fp8_routed_expert_amd as fre
-from fp8_routed_expert_amd import _lib
+from fp8_routed_expert_amd import _lib, experts
 
 P = ctypes.c_void_p(4096)
 ODD = ctypes.c_void_p(4097)
@@ -140,3 +141,22 @@ def test_rows_past_31_bits():
         dc=P, a=P, dtype=1, off=P, cnt=P, E=4, rows=rows, N=8, K=8, dw=P, wt=0, ws=P, wsb=1 << 40, status=P))() == 2
     for name, ok in (("moe_gated_act", dict(h=P)), ("moe_gated_act_grad", dict(dq=P, h=P))):
         assert caller(name, dict(**ok, dtype=1, off=P, cnt=P, E=4, rows=rows, I=8, out=P, zero=0, status=P))() == 2
+
+
+def test_module_frees_its_last_pass_first(monkeypatch):
+    """The scores that a module holds carry the last pass's graph: it is gone
+    before the next one is built."""
+    m = fre.RoutedExperts(E=2, H=8, I=8, K=1, device="cpu")
+    m.scores = m.router.exp()
+    last = weakref.ref(m.scores)
+
+    class Stop(Exception):
+        pass
+
+    def layer_norm(*_):
+        assert last() is None
+        raise Stop
+
+    monkeypatch.setattr(experts, "layer_norm", layer_norm)
+    with pytest.raises(Stop):
+        m(torch.zeros(1, 8))
