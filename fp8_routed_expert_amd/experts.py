@@ -206,7 +206,8 @@ class RoutedExperts(torch.nn.Module):
         # to that call's stream and would end a capture of this one
         self.scores = self.table = self.route_status = None
         xn = layer_norm(x, self.norm_weight, self.norm_bias, self.eps)
-        logits = torch.nn.functional.linear(xn.float(), self.router)
+        with torch.autocast(x.device.type, enabled=False):
+            logits = torch.nn.functional.linear(xn.float(), self.router)
         self.route_status = torch.zeros(1, dtype=torch.int32, device=x.device)
         idx, w, self.scores = route_tokens(logits, self.K, self.bias, status=self.route_status,
                                            **self.route)

@@ -216,3 +216,14 @@ def test_captured_module(gpu):
         torch.cuda.synchronize()
         other.zero_grad(set_to_none=True)
         assert torch.equal(got, step(other)), i
+
+
+def test_router_in_float32_under_autocast(gpu):
+    torch.manual_seed(5)
+    m = fre.RoutedExperts(E=16, H=128, I=64, K=4)
+    x = torch.randn(40, 128, device="cuda", dtype=torch.bfloat16)
+    with torch.no_grad():
+        want = m(x), m.scores
+        with torch.autocast("cuda", dtype=torch.bfloat16):
+            got = m(x), m.scores
+    assert got[0].dtype == want[0].dtype and all(torch.equal(a, b) for a, b in zip(got, want))
