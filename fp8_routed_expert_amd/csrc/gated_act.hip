@@ -75,19 +75,19 @@ __global__ __launch_bounds__(256) void gated_act_kernel(ActArgs p) {
       valid = row_valid(p.offsets, p.counts, p.E, p.rows, m);
     }
     if (m >= p.rows || (!valid && !p.zero_rest)) continue;
-    const size_t at = (size_t)c * 16;
-    uint8_t* out = p.out + m * (kGrad ? 2 * row : row) + at;
+    uint8_t* out = p.out + chunk_at(m, kGrad ? 2 * row : row, c);
     if (!valid) {
       store_chunk<true>(out, 16, make_uint4(0, 0, 0, 0));
       if (kGrad) store_chunk<true>(out + row, 16, make_uint4(0, 0, 0, 0));
       continue;
     }
-    const uint8_t* h = p.h + m * 2 * row + at;
+    const uint8_t* h = p.h + chunk_at(m, 2 * row, c);
     float g[N], v[N], d[N];
     El::unpack(load_chunk<true, kStream>(h, 16), g);
     El::unpack(load_chunk<true, kStream>(h + row, 16), v);
     if (kGrad) {
-      El::unpack(load_chunk<true, kStream>(p.dq + m * row + at, 16), d);
+      const uint8_t* dq = p.dq + chunk_at(m, row, c);
+      El::unpack(load_chunk<true, kStream>(dq, 16), d);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         float s, rest;

@@ -93,6 +93,12 @@ struct RowShape {
   }
 };
 
+// The byte at which chunk c of row m starts in a matrix of whole chunks, in 64
+// bits: rows times bytes leave 31, and so does twice a row number.
+__host__ __device__ __forceinline__ size_t chunk_at(int m, size_t row_bytes, unsigned c) {
+  return (size_t)m * row_bytes + (size_t)c * 16;
+}
+
 // Sixteen bytes at p (all of the row where it is shorter).  kAligned: p is
 // 16-byte aligned and the row a multiple of 16 bytes.  kStream: past the
 // caches (see streamed()).
