@@ -373,9 +373,11 @@ route_kernel(RouteArgs p, int lanes_per_group, int per_lane) {
   // of the exponent's low part, left out here, 0.22 per unit of the argument,
   // which is -ln(score) at most where it counts.  Softmax: the exponential's and
   // the sum's, and one per unit of the argument.  Scores below e^-88 are 0,
-  // within 1e-37.  (Two keys with |sum| + 4 reach <= v together: the same.)
+  // within 1e-37.  (Two keys with |sum| + 4 reach <= v together: the same.)  v is
+  // 0 where all scores that it bounds are and there is no bias: its logarithm
+  // is taken of the least normal number then, since 0 times -log 0 is NaN.
   auto error = [&](float v) {
-    const float units = larger(0.f, -0.7f * __builtin_amdgcn_logf(v));
+    const float units = larger(0.f, -0.7f * __builtin_amdgcn_logf(larger(v, 0x1p-126f)));
     const float roundings = softmax ? 25.f + kN + units : fmaf(0.22f, units, 9.f);
     return fmaf(v, roundings * kU, 1e-37f);
   };
