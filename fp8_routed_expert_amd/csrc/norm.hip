@@ -77,6 +77,30 @@ __device__ __forceinline__ void row_add(float (&v)[kN], float (*red)[kN]) {
   }
 }
 
+// The row's sum, in every lane of its waves.  Rows of 513 to 1024 chunks are
+// taken by 16 waves of one chunk to a lane or, where there are many, by eight of
+// two (launch_norm): wave w of the sixteen and wave w + 8 hold what wave w of the
+// eight has in its first and second chunks.  Both add these two waves' sums
+// first (kSums: the eight have a sum for each chunk; kPairs: the sixteen), so
+// that a row's bits do not depend on its batch.  (second: the wave has second
+// chunks; the sum of none is 0.)
+template <int kWaves, int kSums, bool kPairs>
+__device__ __forceinline__ float row_total(const float (&v)[kSums], bool second, float* red) {
+  float s = wave_add(v[0]);
+  if constexpr (kSums == 2)
+    if (second) s += wave_add(v[1]);
+  if constexpr (kWaves > 1) {
+    const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) % kWaves;
+    if (lane == 0) red[wave] = s;
+    __syncthreads();
+    constexpr int kHalf = kPairs ? kWaves / 2 : kWaves;
+    s = kPairs ? red[0] + red[kHalf] : red[0];
+#pragma unroll
+    for (int w = 1; w < kHalf; ++w) s += kPairs ? red[w] + red[w + kHalf] : red[w];
+  }
+  return s;
+}
+
 // Values [at, at + n) of a weight or bias, n <= kN of them.
 template <typename W, int kN>
 __device__ __forceinline__ void load_param(const uint8_t* p, int at, int n, float (&v)[kN]) {
@@ -165,8 +189,11 @@ __global__ __launch_bounds__(norm_threads(kWaves), norm_waves(kWaves, kCh)) void
 norm_kernel(NormArgs p) {
   constexpr int N = El::kN, kStep = 64 * kWaves;
   constexpr int kPer = kWaves == 1 ? 4 : 1;   // rows of a workgroup
-  __shared__ float red[2][kWaves][1];
+  constexpr int kSums = kWaves == 8 && kCh == 2 ? 2 : 1;   // (see row_total)
+  constexpr bool kPairs = kWaves == 16 && kCh == 1;
+  __shared__ float red[2][kWaves];
   const int at = threadIdx.x % kStep;
+  const bool second = __builtin_amdgcn_readfirstlane(threadIdx.x & -64) + kStep < p.row.chunks;
   const float over = 1.f / (float)p.H;
   const long long step = (long long)gridDim.x * kPer;
   long long t = (long long)blockIdx.x * kPer + (kPer > 1 ? threadIdx.x / kStep : 0);
@@ -193,43 +220,50 @@ norm_kernel(NormArgs p) {
     if (kKind != kWholeRows) chunk_range<El>(p.row, c, lo[u], hi[u]);
     if (c >= p.row.chunks) hi[u] = 0;
   }
+  // The row's end is among the lanes' last chunks, so that the others need no
+  // mask: loose rows go without (8192 x 4099 bf16 29 us, with it 33, of spills).
+  // Whole rows keep it: at the memory's rate they are slower without (65536 x
+  // 7168 bf16 347 us, with it 333).
+  auto whole = [&](int u) __attribute__((always_inline)) {
+    return (kKind == kLooseRows && u < kCh - 1) || hi[u] - lo[u] == N;
+  };
   for (; t < p.T; t += step) {
     float v[kCh][N];
 #pragma unroll
     for (int u = 0; u < kCh; ++u) El::unpack(raw[u], v[u]);
     load(t + step < p.T ? t + step : t);
     // (all of a chunk, but for the lane with the row's end)
-    float s[1] = {0.f};
+    float s[kSums] = {};
 #pragma unroll
     for (int u = 0; u < kCh; ++u)
-      if (hi[u] - lo[u] == N) {
+      if (whole(u)) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[0] += v[u][i];
+        for (int i = 0; i < N; ++i) s[u % kSums] += v[u][i];
       } else if (kKind != kWholeRows && hi[u]) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (i >= lo[u] && i < hi[u]) s[0] += v[u][i];
+          if (i >= lo[u] && i < hi[u]) s[u % kSums] += v[u][i];
       }
-    row_add<kWaves>(s, red[0]);
     // (divided: the mean of equal values is that value, and no product with a
     // rounded 1 / H that the subtraction below could be contracted with)
-    const float mu = s[0] / (float)p.H;
-    s[0] = 0.f;
+    const float mu = row_total<kWaves, kSums, kPairs>(s, second, red[0]) / (float)p.H;
+#pragma unroll
+    for (int u = 0; u < kSums; ++u) s[u] = 0.f;
 #pragma unroll
     for (int u = 0; u < kCh; ++u) {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[u][i] -= mu;
-      if (hi[u] - lo[u] == N) {
+      if (whole(u)) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[0] = fmaf(v[u][i], v[u][i], s[0]);
+        for (int i = 0; i < N; ++i) s[u % kSums] = fmaf(v[u][i], v[u][i], s[u % kSums]);
       } else if (kKind != kWholeRows && hi[u]) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (i >= lo[u] && i < hi[u]) s[0] = fmaf(v[u][i], v[u][i], s[0]);
+          if (i >= lo[u] && i < hi[u]) s[u % kSums] = fmaf(v[u][i], v[u][i], s[u % kSums]);
       }
     }
-    row_add<kWaves>(s, red[1]);
-    const float r = 1.f / sqrtf(fmaf(s[0], over, p.eps));
+    const float r =
+        1.f / sqrtf(fmaf(row_total<kWaves, kSums, kPairs>(s, second, red[1]), over, p.eps));
 #pragma unroll
     for (int u = 0; u < kCh; ++u) {
       const int c = at + u * kStep;

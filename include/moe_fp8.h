@@ -631,8 +631,9 @@ moe_status_t moe_route_tokens_grad(const void* logits, int dtype, int T, int E,
  *   dweight_h = round(sum_t dy_th z_th),  dbias_h = round(sum_t dy_th)
  *
  * Everything is held in fp32 and rounded once, to nearest even; sums have a
- * fixed order (no atomics: the same call gives the same bits).  T = 0 gives
- * zero gradients.  A row with an infinity or a NaN gives NaN.
+ * fixed order (no atomics: the same call gives the same bits), a row's mean,
+ * rstd and y the same one in every batch.  T = 0 gives zero gradients.  A row
+ * with an infinity or a NaN gives NaN.
  *
  *   x, y, dy, dx [T, H]  of dtype (MOE_TYPE_F32, _BF16 or _F16)
  *   weight, bias, dweight, dbias [H]  of w_dtype: dtype or MOE_TYPE_F32;
