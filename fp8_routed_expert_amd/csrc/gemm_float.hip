@@ -13,11 +13,10 @@
 // weights' one pass through HBM (256 x 32 x 4096 x 7168 bf16 6.0 TB/s).
 #include <type_traits>
 
+#include "float_tile.hpp"
 #include "gemm_tiles.hpp"
 
 namespace moe {
-
-enum { kProduct = 0, kRowsGrad = 1, kWeightsGrad = 2 };
 
 struct FloatArgs {
   const uint8_t* p;   // a; dc in both gradients
@@ -631,19 +630,10 @@ static bool float_type(int dtype) {
   return dtype == MOE_TYPE_F32 || dtype == MOE_TYPE_BF16 || dtype == MOE_TYPE_F16;
 }
 
-// Tiles of a launch: those of every expert's rows, rounded up.
-template <int kMode>
-static long long tiles_of(const FloatArgs& p, int bm, int bn) {
-  const int width = kMode == kProduct ? p.N : p.K;
-  const long long m = kMode == kWeightsGrad ? (long long)p.E * ((p.N + bm - 1) / bm)
-                                            : (long long)p.rows / bm + p.E;
-  return m * ((width + bn - 1) / bn);
-}
-
 template <int kType, int kMode, int BM, int BN, int WM, int WN, int GM, int kDeep>
 static moe_status_t launch_tiles(const FloatArgs& p, hipStream_t st) {
   constexpr int threads = 64 * (BM / WM) * (BN / WN);
-  const long long blocks = tiles_of<kMode>(p, BM, BN);
+  const long long blocks = tiles_of(kMode, p.E, p.rows, p.N, p.K, BM, BN);
   if (blocks * threads > 0xffffffffLL || blocks > 0x7fffffffLL) return MOE_UNSUPPORTED_SHAPE;
   const dim3 grid((unsigned)blocks, (unsigned)p.splits), block(threads);
   // (a weights' gradient ends where its operands' descriptors end)
@@ -671,85 +661,32 @@ static moe_status_t launch_skinny(const FloatArgs& p, hipStream_t st) {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_HIP_ERROR;
 }
 
-// Parts that the weights' gradient splits its segments into: where the experts'
-// 128 x 128 tiles are fewer than a round of the CUs (two workgroups to each),
-// and segments (of the buffer, on average) long enough for at least 512 rows
-// in a part.  (65536 rows of one expert, 512 x 512 bf16: 306 us whole, 73 in 32
-// parts, their join included.)
-static int weight_splits(int E, int rows, int N, int K) {
-  const long long tiles = (long long)E * ((N + 127) / 128) * ((K + 127) / 128);
-  long long n = tiles < 256 ? 512 / tiles : 1;
-  const long long parts = rows / E / 512;
-  if (n > parts) n = parts;
-  return n < 1 ? 1 : n > 32 ? 32 : (int)n;
-}
-
-// Tiles are chosen from the sizes alone (the same inside graph capture).  `rows`
-// is a segment's on average: the buffer's, less the 127 that a contiguous one
-// has for the padding between segments (a capacity of 128 rows or more counts
-// as less than it may hold).  Times in us, weights from HBM, rows x experts x N
-// x K, bf16; p: product, r: rows' gradient, w: weights' gradient.
-//
-//   * Few rows: 64 x 128 tiles, several workgroups to a CU, once there are more
-//     of them than CUs (p 256 x 32 x 4096 x 7168 318, 64 x 64 tiles loaded five
-//     steps ahead 366, 128 x 128 354; r 357, 450, 375) or l is short; else 64 x
-//     64 (r 8 x 8 x 7168 x 2048 36, 64 x 128 68, 128 x 128 55); and where
-//     there are so few channels that those leave CUs idle, the product
-//     without tiles (p 1 x 1 x 4096 x 7168 14, 64 x 64 31; 1 x 1 x 7168 x 2048
-//     9.6 and 12; 8 x 8 x 4096 x 7168 66 and 80; but 4 x 4 36 and 32).
-//   * else 256 x 256 or 128 x 128, whichever takes less time by their rounds of
-//     the CUs: a step of 256 tiles of 256 x 256 takes 1.59 us at the rate of
-//     large products, one of 256 tiles of 128 x 128 0.605 (p 1024 x 8 x 4096 x
-//     7168 185 and 152, r 117 and 140; p 4096 x 32 571 and 483; 6144 x 6 x
-//     7168 x 2048 p 163 and 210, r 185 and 229; prefill shares 131040 x 9 x 4096
-//     x 7168 p 5700 and 9090).  128 x 128 with two workgroups to a CU, or, for
-//     the rows' gradient and where there are no two, loaded two steps ahead
-//     (r 4096 x 32 x 7168 x 2048 243 and 301; p 8192 x 32 402 and 372).
-//   * fp32: 64 x 128, or 64 x 64 where those are few (16384 x 8 x 1024 x 1024 p
-//     294, 64 x 64 591, 128 x 128 329, 256 x 256 485: its steps have half the
-//     l's and eight times the multiplications, so the loads hide in any tile and
-//     what counts is that the last round is full).
 template <int kType, int kMode>
-static moe_status_t launch_tiles(const FloatArgs& p, hipStream_t st) {
-  const int width = kMode == kProduct ? p.N : p.K;
-  if (kType == MOE_TYPE_F32) {
-    if (tiles_of<kMode>(p, 64, 64) <= 512 && p.splits == 1)
-      return launch_tiles<kType, kMode, 64, 64, 32, 64, 4, 6>(p, st);
+static moe_status_t launch_float(const FloatArgs& p, hipStream_t st) {
+  const FloatTile t = float_tile(kMode, kType == MOE_TYPE_F32, p.E, p.rows, p.N, p.K, p.splits);
+  if constexpr (kType == MOE_TYPE_F32) {
+    if (t.cols == 64) return launch_tiles<kType, kMode, 64, 64, 32, 64, 4, 6>(p, st);
     return launch_tiles<kType, kMode, 64, 128, 32, 64, 4, 0>(p, st);
   } else {
-    long long rows = ((long long)p.rows + p.E - 1) / p.E;
-    if (rows >= 128) rows -= 127;
-    if (kMode != kWeightsGrad && rows <= 48) {
-      const long long wide = (long long)p.E * ((width + 127) / 128);
-      const int L = kMode == kProduct ? p.K : p.N;
-      if (wide > 256 || (wide > 128 && L <= 1024))
-        return launch_tiles<kType, kMode, 64, 128, 32, 64, 4, 0>(p, st);
-      if constexpr (kMode == kProduct)
-        if (rows <= 16)
-          return (long long)p.E * p.N >= 448 * 16 ? launch_skinny<kType, 2>(p, st)
-                                                  : launch_skinny<kType, 1>(p, st);
-      return launch_tiles<kType, kMode, 64, 64, 32, 64, 4, 6>(p, st);
-    }
-    // (segments differ, and end anywhere in a tile: six tenths of one more each)
-    auto tiles = [&](int b) {
-      const long long m = kMode == kWeightsGrad ? (long long)p.E * ((p.N + b - 1) / b)
-                                                : p.E * (10 * rows + 6 * b) / (10 * b);
-      return m * ((width + b - 1) / b);
-    };
-    auto rounds = [](long long n) { return (n + 255) / 256; };
-    if (p.splits == 1 && rounds(tiles(256)) * 159 <= rounds(tiles(128)) * 60)
-      return launch_tiles<kType, kMode, 256, 256, 128, 64, 2, 0>(p, st);
-    if (kMode != kRowsGrad && tiles(128) > 256)
-      return launch_tiles<kType, kMode, 128, 128, 64, 64, 4, 0>(p, st);
+    if constexpr (kMode == kProduct)
+      if (t.rows == 16)
+        return t.cols == 32 ? launch_skinny<kType, 2>(p, st) : launch_skinny<kType, 1>(p, st);
+    if constexpr (kMode != kWeightsGrad)
+      if (t.rows == 64)
+        return t.cols == 64 ? launch_tiles<kType, kMode, 64, 64, 32, 64, 4, 6>(p, st)
+                            : launch_tiles<kType, kMode, 64, 128, 32, 64, 4, 0>(p, st);
+    if (t.rows == 256) return launch_tiles<kType, kMode, 256, 256, 128, 64, 2, 0>(p, st);
+    if constexpr (kMode != kRowsGrad)
+      if (t.ahead == 0) return launch_tiles<kType, kMode, 128, 128, 64, 64, 4, 0>(p, st);
     return launch_tiles<kType, kMode, 128, 128, 64, 64, 4, 3>(p, st);
   }
 }
 
 template <int kMode>
 static moe_status_t launch_float(const FloatArgs& p, int dtype, hipStream_t st) {
-  if (dtype == MOE_TYPE_BF16) return launch_tiles<MOE_TYPE_BF16, kMode>(p, st);
-  if (dtype == MOE_TYPE_F16) return launch_tiles<MOE_TYPE_F16, kMode>(p, st);
-  return launch_tiles<MOE_TYPE_F32, kMode>(p, st);
+  if (dtype == MOE_TYPE_BF16) return launch_float<MOE_TYPE_BF16, kMode>(p, st);
+  if (dtype == MOE_TYPE_F16) return launch_float<MOE_TYPE_F16, kMode>(p, st);
+  return launch_float<MOE_TYPE_F32, kMode>(p, st);
 }
 
 constexpr int kMaxFloatDim = 1 << 20;     // N and K
