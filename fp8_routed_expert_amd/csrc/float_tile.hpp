@@ -72,10 +72,12 @@ inline FloatTile float_tile(int mode, bool f32, int E, int rows_total, int N, in
     if (mode == kProduct && rows <= 16) return {16, (long long)E * N >= 448 * 16 ? 32 : 16, 0};
     return {64, 64, 6};
   }
-  // (segments differ, and end anywhere in a tile: six tenths of one more each)
+  // (segments differ, and end anywhere in a tile: six tenths of one more each,
+  // but a tile at least.  One expert's 100 rows x 4096 x 7168 counted as none
+  // took 256 x 256 tiles, p 152 us, and take 62.)
   auto tiles = [&](int b) {
-    const long long m = mode == kWeightsGrad ? (long long)E * ((N + b - 1) / b)
-                                             : E * (10 * rows + 6 * b) / (10 * b);
+    const long long few = E * (10 * rows + 6 * b) / (10 * b);
+    const long long m = mode == kWeightsGrad ? (long long)E * ((N + b - 1) / b) : few ? few : 1;
     return m * ((width + b - 1) / b);
   };
   auto rounds = [](long long n) { return (n + 255) / 256; };

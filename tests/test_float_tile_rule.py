@@ -74,3 +74,12 @@ def test_every_kernel_is_chosen_and_run(rule, tmp_path):
     assert built - run == set(), "built, and reached by no case"
     assert run - built == set() and len(built) == 56
     assert any(t[3] > 1 for t in tiles) and any(t[3] == 1 for t in tiles)
+
+
+def test_few_rows_of_one_expert(rule):
+    """Rows that fill less than half of a tile count as a tile, not as none: 256
+    x 256 tiles of 4096 channels would leave 240 CUs idle."""
+    rows = [49, 60, 100, 101, 176, 200, 228]
+    for mode, N, K in ((PRODUCT, 4096, 7168), (PRODUCT, 7168, 2048), (ROWS, 7168, 2048), (ROWS, 4096, 7168)):
+        tiles = rule([(mode, 0, 1, R, N, K) for R in rows])
+        assert all(t[:2] == (128, 128) for t in tiles), (mode, N, K, tiles)
