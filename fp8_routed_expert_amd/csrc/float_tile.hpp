@@ -39,7 +39,14 @@ inline int weight_splits(int E, int rows, int N, int K) {
 //     64 (r 8 x 8 x 7168 x 2048 36, 64 x 128 68, 128 x 128 55); and where
 //     there are so few channels that those leave CUs idle, the product
 //     without tiles (p 1 x 1 x 4096 x 7168 14, 64 x 64 31; 1 x 1 x 7168 x 2048
-//     9.6 and 12; 8 x 8 x 4096 x 7168 66 and 80; but 4 x 4 36 and 32).
+//     9.6 and 12; 8 x 8 x 4096 x 7168 66 and 80; but 4 x 4 36 and 32).  That
+//     one reads the weights once for every 16 rows.  A buffer of 128 to 143
+//     rows to an expert may be a contiguous one of few rows or hold full
+//     segments (x 4096 x 7168, experts x rows of each, without tiles and 64 x
+//     64: 4 x 1 50 and 47, 4 x 128 316 and 80; 8 x 1 95 and 94, 8 x 128 629 and
+//     162; but 1 x 1 14 and 36, 1 x 128 104 and 36; 2 x 1 26 and 39, 2 x 128 161
+//     and 41): it takes 64 x 64 tiles where these are as many as the CUs, and
+//     with fewer channels stays without, for the few rows.
 //   * else 256 x 256 or 128 x 128, whichever takes less time by their rounds of
 //     the CUs: a step of 256 tiles of 256 x 256 takes 1.59 us at the rate of
 //     large products, one of 256 tiles of 128 x 128 0.605 (p 1024 x 8 x 4096 x
@@ -63,13 +70,14 @@ inline FloatTile float_tile(int mode, bool f32, int E, int rows_total, int N, in
     if (tiles_of(mode, E, rows_total, N, K, 64, 64) <= 512 && splits == 1) return {64, 64, 6};
     return {64, 128, 0};
   }
-  long long rows = ((long long)rows_total + E - 1) / E;
-  if (rows >= 128) rows -= 127;
+  const long long most = ((long long)rows_total + E - 1) / E;
+  const long long rows = most >= 128 ? most - 127 : most;
   if (mode != kWeightsGrad && rows <= 48) {
     const long long wide = (long long)E * ((width + 127) / 128);
     const int L = mode == kProduct ? K : N;
     if (wide > 256 || (wide > 128 && L <= 1024)) return {64, 128, 0};
-    if (mode == kProduct && rows <= 16) return {16, (long long)E * N >= 448 * 16 ? 32 : 16, 0};
+    if (mode == kProduct && rows <= 16 && (most <= 16 || (long long)E * N < 256 * 64))
+      return {16, (long long)E * N >= 448 * 16 ? 32 : 16, 0};
     return {64, 64, 6};
   }
   // (segments differ, and end anywhere in a tile: six tenths of one more each,

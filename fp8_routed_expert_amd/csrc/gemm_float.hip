@@ -504,12 +504,13 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void float_tile_kernel(
   }
 }
 
-// Products of at most 16 rows of an expert in 16 bits, where tiles would be too
-// few to keep the memory busy: bound by the weights' one pass through HBM.  A
-// workgroup computes 16 NT channels; its eight waves share out K, so that
-// every CU has many waves' weight loads in flight (a wave's fragments go from
-// global memory straight to its registers: each weight is used by one wave),
-// and their sums are added in LDS in the order of the waves.
+// Products of a few rows of every expert in 16 bits, 16 of them to a workgroup,
+// where tiles would be too few to keep the memory busy: bound by the weights'
+// way from HBM, once for 16 rows.  A workgroup computes 16 NT channels; its
+// eight waves share out K, so that every CU has many waves' weight loads in
+// flight (a wave's fragments go from global memory straight to its registers:
+// each weight is used by one wave), and their sums are added in LDS in the
+// order of the waves.
 constexpr int kSkinnyWaves = 8;
 constexpr int kSlab = 64;   // bytes of a row that one multiplication takes: 16 of four lanes
 

@@ -83,3 +83,13 @@ def test_few_rows_of_one_expert(rule):
     for mode, N, K in ((PRODUCT, 4096, 7168), (PRODUCT, 7168, 2048), (ROWS, 7168, 2048), (ROWS, 4096, 7168)):
         tiles = rule([(mode, 0, 1, R, N, K) for R in rows])
         assert all(t[:2] == (128, 128) for t in tiles), (mode, N, K, tiles)
+
+
+@pytest.mark.parametrize("E,N,K", [(4, 4096, 7168), (8, 2048, 7168), (8, 4096, 7168), (2, 8192, 2048)])
+def test_buffers_of_128_rows_to_an_expert(rule, E, N, K):
+    """They may be contiguous ones of few rows, or full segments: the product
+    without tiles, which reads the weights once for every 16 rows, is for buffers
+    that hold no more, or for too few channels for 64 x 64 tiles."""
+    tiles = rule([(PRODUCT, 0, E, E * rows, N, K) for rows in (16, 128, 143)])
+    assert all(t[:2] == (64, 64) for t in tiles[1:]) and tiles[0][0] == 16, tiles
+    assert all(t[0] == 16 for t in rule([(PRODUCT, 0, 1, 128, 7168, 2048), (PRODUCT, 0, 1, 143, 4096, 7168)]))

@@ -75,3 +75,11 @@ def test_weights_gradient_past_4_gb(gpu, dt):
             s = slice(i, min(n, i + 20000))
             ref += dc[s].double().t().contiguous() @ a[s].double()
         assert torch.equal(dw[e].double(), ref), e
+
+
+@pytest.mark.parametrize("rows", [127, 128, 143, 160])
+def test_full_segments(gpu, rows):
+    """Fixed-capacity segments that are all full, on both sides of the buffers
+    that a contiguous layout of few rows has too."""
+    for E, N, K in ((8, 2048, 520), (1, 4096, 264)):
+        run_case([rows] * E, rows, 1, 1, N, K, torch.bfloat16, False, torch.float32)
