@@ -201,6 +201,11 @@ class RoutedExperts(torch.nn.Module):
             torch.nn.init.normal_(w, std=0.02)
         self.scores = self.table = self.route_status = None
 
+    def __getstate__(self):
+        # (a copy starts without what the last call left: a graph's tensors
+        # cannot be copied)
+        return {**self.__dict__, "scores": None, "table": None, "route_status": None}
+
     def forward(self, x):
         # what the last call left holds its graph, whose accumulations belong
         # to that call's stream and would end a capture of this one
