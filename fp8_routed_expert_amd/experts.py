@@ -181,7 +181,9 @@ class RoutedExperts(torch.nn.Module):
     bias [E] float32 (a buffer, not a parameter) moves the choice of experts; a
     balancing scheme writes it.  After a call, `scores` holds the router's
     scores [T, E] and `table` the sorted tokens (its status tells of dropped
-    rows, `route_status` of NaN logits)."""
+    rows, `route_status` of NaN logits).  with_scores=True returns (output,
+    scores): what a balancing loss takes where the call is checkpointed, since a
+    re-entrant checkpoint's first pass leaves `scores` without a graph."""
 
     def __init__(self, E, H, I, K, score=ops.SCORE_SOFTMAX, groups=1, top_groups=1, group_best=1,
                  renorm=True, scale=1.0, eps=1e-5, dtype=torch.bfloat16, device="cuda"):
@@ -206,7 +208,7 @@ class RoutedExperts(torch.nn.Module):
         # cannot be copied)
         return {**self.__dict__, "scores": None, "table": None, "route_status": None}
 
-    def forward(self, x):
+    def forward(self, x, with_scores=False):
         # what the last call left holds its graph, whose accumulations belong
         # to that call's stream and would end a capture of this one
         self.scores = self.table = self.route_status = None
@@ -219,4 +221,5 @@ class RoutedExperts(torch.nn.Module):
         t = self.table = sort_tokens(idx, self.E, contiguous_rows(idx.numel(), self.E))
         a = permute_tokens(xn, t)
         q = gated_act(grouped_linear(a, self.w13, t), t)
-        return combine_tokens(grouped_linear(q, self.w2, t), w, t)
+        out = combine_tokens(grouped_linear(q, self.w2, t), w, t)
+        return (out, self.scores) if with_scores else out
