@@ -213,11 +213,12 @@ class RoutedExperts(torch.nn.Module):
         # to that call's stream and would end a capture of this one
         self.scores = self.table = self.route_status = None
         xn = layer_norm(x, self.norm_weight, self.norm_bias, self.eps)
+        # (router and bias are float32, unless the module was converted)
         with torch.autocast(x.device.type, enabled=False):
-            logits = torch.nn.functional.linear(xn.float(), self.router)
+            logits = torch.nn.functional.linear(xn.float(), self.router.float())
         self.route_status = torch.zeros(1, dtype=torch.int32, device=x.device)
-        idx, w, self.scores = route_tokens(logits, self.K, self.bias, status=self.route_status,
-                                           **self.route)
+        idx, w, self.scores = route_tokens(logits, self.K, self.bias.float(),
+                                           status=self.route_status, **self.route)
         t = self.table = sort_tokens(idx, self.E, contiguous_rows(idx.numel(), self.E))
         a = permute_tokens(xn, t)
         q = gated_act(grouped_linear(a, self.w13, t), t)

@@ -47,3 +47,22 @@ def test_returned_scores_are_the_kept_ones(gpu):
     x = torch.randn(9, 64, device="cuda", dtype=torch.bfloat16)
     out, scores = m(x, with_scores=True)
     assert scores is m.scores and scores.shape == (9, 4) and torch.equal(out, m(x))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16, torch.float32])
+def test_converted_module(gpu, dt):
+    """A module that its program converted as a whole: the router's product and
+    the bias are still float32, from the converted values."""
+    m = fre.RoutedExperts(E=6, H=64, I=32, K=2, score=fre.SCORE_SIGMOID)
+    m.bias[2] = 0.25
+    m.to(dt)
+    x = torch.randn(40, 64, device="cuda", dtype=dt, requires_grad=True)
+    out, scores = m(x, with_scores=True)
+    assert out.dtype == dt and scores.dtype == torch.float32
+    xn = fre.layer_norm(x, m.norm_weight, m.norm_bias)
+    idx, _, want = fre.route_tokens(torch.nn.functional.linear(xn.float(), m.router.float()), 2,
+                                    m.bias.float(), score=fre.SCORE_SIGMOID)
+    assert torch.equal(scores, want) and int(m.route_status) == 0
+    (out.float().square().sum() + scores.square().sum()).backward()
+    for k, v in m.named_parameters():
+        assert v.grad.dtype == dt and v.grad.isfinite().all() and v.grad.abs().sum() > 0, k
