@@ -665,6 +665,8 @@ def moe_route_tokens(logits, topk_idx, topk_w, status, bias=None, score=SCORE_SO
     numbers = groups, top_groups, first_expert, local_experts
     if max(numbers) > _INT_MAX or min(numbers) < 0:
         raise ValueError(f"moe_route_tokens: numbers {numbers} outside [0, {_INT_MAX}]")
+    if abs(score) > _INT_MAX or abs(group_best) > _INT_MAX:
+        raise ValueError(f"moe_route_tokens: score {score}, group_best {group_best}, at most {_INT_MAX}")
     dev = logits.get_device()
     _call("moe_route_tokens", stream, dev, _arg(logits, _FLOATS, "logits", dev),
           _type(logits, "logits"), T, E, _opt(bias, _F32, "bias", dev, (E,)), score, groups,
@@ -682,6 +684,8 @@ def moe_route_tokens_grad(logits, topk_idx, dtopk_w, dlogits, status, score=SCOR
     weights (float32 [T, K]) and, where given, scores (float32 [T, E])."""
     T, E = _matrix(logits, "logits")
     K = _matrix(topk_idx, "topk_idx")[1]
+    if abs(score) > _INT_MAX:
+        raise ValueError(f"moe_route_tokens_grad: score {score}, at most {_INT_MAX}")
     dev = logits.get_device()
     _call("moe_route_tokens_grad", stream, dev, _arg(logits, _FLOATS, "logits", dev),
           _type(logits, "logits"), T, E, _arg(topk_idx, _I32, "topk_idx", dev, (T, K)), K, score,
