@@ -44,7 +44,10 @@ __device__ __forceinline__ void sigmoid(float g, float& s, float& rest) {
 // of a row and the next.  Up to 64 experts (kFew), the wave's lanes hold their
 // segments, so that the rows are looked up without a search through memory:
 // a search for every row took 9.3 us at a decode share of 1193 rows on 32
-// experts.
+// experts, and takes 6.8 (floor 2.4: the vector units are active in 77% of the
+// cycles, mostly for waves that find their rows not valid).  More experts are
+// searched for: 131040 rows of 2048 bf16 on 65 351 us, the gradient
+// 452, on 256 386 and 474; on 9 260 and 446.
 template <typename El, bool kGrad, bool kStream, bool kFew>
 __global__ __launch_bounds__(256) void gated_act_kernel(ActArgs p) {
   constexpr int N = El::kN;

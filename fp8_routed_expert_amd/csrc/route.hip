@@ -118,7 +118,9 @@ __device__ __forceinline__ void put_pick(const RouteArgs& p, long long t, int k,
 
 // ---- the exact form: a token to a wave, lane l on experts l, l + 64, ..., keys
 // in 64 bits throughout, in E doubles of LDS.  It takes the tokens that the
-// fast form below cannot decide, so its loops are short code, not fast.
+// fast form below cannot decide, so its loops are short code, not fast: 65536
+// tokens of 256 equal logits, all of which take it, 273 us (random ones 26), and
+// 4096 44.
 template <typename El>
 __device__ __forceinline__ void route_exact(const RouteArgs& p, long long t, double* keys) {
   const int lane = threadIdx.x & 63;
@@ -242,10 +244,17 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_exact_kernel(RouteArgs
 // is still open goes to route_exact: groups whose scores are closer than their
 // error, more candidates than fit, and, for a softmax with a bias, whose sum
 // is fp32, candidates that are close.
+//
+// Bound by instruction issue: the vector units are active in 82% of the cycles
+// that the CUs are busy (65536 tokens of 256 experts in 8 groups fp32, 33 us), with
+// 866 vector instructions for four tokens; the three waves of a unit hide each
+// other's waits, 45% of their cycles.  Scores are stored one by one: asked for,
+// they add 55 us.
 constexpr float kU = 0x1p-24f;
 
-// The larger of two numbers that are no NaN, in one instruction (fmaxf first
-// quiets what might be a signalling NaN: one more per operand).
+// The larger of two numbers that are no NaN: a median with infinity, where fmaxf
+// first quiets what might be a signalling NaN, one instruction more per operand.
+// (Where the compiler turns it back into a maximum, it quiets one as well.)
 __device__ __forceinline__ float larger(float a, float b) {
   return __builtin_amdgcn_fmed3f(a, b, INFINITY);
 }
@@ -668,7 +677,9 @@ route_kernel(RouteArgs p, int lanes_per_group, int per_lane) {
   }
 }
 
-// The gradient: kLanes lanes to a token, each holding kN neighbouring experts
+// The gradient, bound by instruction issue (16384 x 72 bf16 6.7 us: 605 vector
+// instructions for four tokens, the vector units active in 75% of the cycles):
+// kLanes lanes to a token, each holding kN neighbouring experts
 // (kWide: whole 16-byte pieces of a row) or experts at, at + kLanes, ...; lane k
 // holds pick k.
 template <typename El, int kLanes, int kN, bool kWide>

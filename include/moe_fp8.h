@@ -673,9 +673,10 @@ moe_status_t moe_layer_norm_grad(const void* dy, const void* x, int dtype, int T
  *
  * Sums are fp32 on the matrix cores, rounded once, to nearest even; the
  * activation is fp32 (exp and reciprocal from the hardware, ~1 ulp each).  The
- * same call gives the same bits.  Only valid rows are read; other rows of the
- * outputs are left as they are, or set to zero with zero_rest != 0.  An expert
- * without valid rows gets dw = 0.
+ * same call gives the same bits.  Only valid rows count (the products may load
+ * rows behind a segment's last one with its tile: whatever these hold has no
+ * part in any result); other rows of the outputs are left as they are, or set
+ * to zero with zero_rest != 0.  An expert without valid rows gets dw = 0.
  *
  *   a, da [rows_total, K]   c, dc [rows_total, N]   w, dw [E, N, K]
  *   h, dh [rows_total, 2I]  q, dq [rows_total, I]
