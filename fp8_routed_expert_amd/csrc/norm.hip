@@ -765,6 +765,8 @@ extern "C" moe_status_t moe_layer_norm_grad(const void* dy, const void* x, int d
   if (ok != MOE_OK) return ok;
   const bool params = dweight || dbias;
   if (!dx && !params) return T == 0 ? MOE_OK : MOE_INVALID_ARG;
+  // (the joining launch has 256 threads to 32 columns of both gradients)
+  if (params && (2LL * H + 31) / 32 * 256 > 0xffffffffLL) return MOE_UNSUPPORTED_SHAPE;
   if (T > 0 && (!dy || !x || !mean || !rstd)) return MOE_INVALID_ARG;
   const bool is_long = p.row.bytes > kNormLong;
   if (T > 0 && (params || is_long) &&

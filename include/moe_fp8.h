@@ -641,7 +641,9 @@ moe_status_t moe_route_tokens_grad(const void* logits, int dtype, int T, int E,
  *   mean, rstd [T] f32   written by moe_layer_norm (each may be NULL there),
  *            read by the gradient
  *   eps      >= 0
- *   dx, dweight, dbias   each may be NULL (not computed), not all
+ *   dx, dweight, dbias   each may be NULL (not computed), not all; for dweight
+ *            and dbias H is at most 268435440 (a launch holds 2^32 threads:
+ *            MOE_UNSUPPORTED_SHAPE)
  *   workspace  moe_layer_norm_workspace_bytes(T, H) bytes, 16-byte aligned;
  *            what the call leaves there is unspecified.  Calls (or captured
  *            graphs) that may run at the same time need one each.

@@ -1,13 +1,14 @@
-"""The address of a row's chunk, in 64 bits for every row number that a call
-takes, on the host (no GPU needed): the helper that the activation's kernels
-form their addresses with is compiled for the host and compared with exact
-integers."""
+"""Sizes that leave 31 or 32 bits, on the host (no GPU needed): the address of a
+row's chunk, which the activation's kernels form with a helper that is compiled
+for the host here and compared with exact integers, and the threads of a launch."""
 
+import ctypes
 import os
 import subprocess
 
 import pytest
 
+from fp8_routed_expert_amd import _lib
 from fp8_routed_expert_amd import build as lib_build
 
 MAIN = r"""
@@ -37,3 +38,13 @@ def test_chunk_addresses(tmp_path):
     assert len(lines) == 8 * 5 * 4
     for m, b, c, at in lines:
         assert at == m * b + 16 * c, (m, b, c)
+
+
+def test_norm_columns_of_one_launch():
+    """The columns of the norm's weight and bias gradients are joined by one
+    launch, which holds 2^32 threads, 256 for 32 columns of both."""
+    P, most = ctypes.c_void_p(4096), (2 ** 32 // 256 - 1) * 32 // 2
+    f = _lib.load().moe_layer_norm_grad
+    for T in (0, 1, 4):
+        for dw, db in ((P, P), (P, None), (None, P)):
+            assert f(P, P, 1, T, most + 1, P, 0, P, P, P, dw, db, P, 1 << 50, None) == 2, (T, dw, db)
